@@ -178,7 +178,8 @@ dg_status dg_fp8_grouped_masked_ue8m0_f32(const uint8_t* A, const int32_t* sA, c
  *   tt:                  A [K,M], B [N,K]
  * The scales keep the logical granularity and layouts of dg_fp8_gemm_nt: sA [ceil(K/128)][align4(M)]
  * (one per 1x128 K-group of each logical row of A), sB [ceil(N/128)][ceil(K/128)]. A stored [K,M]
- * needs M % 16 == 0; B stored [K,N] needs N % 16 == 0 (16-byte TMA strides). The tensor core reads
+ * needs M % 16 == 0; B stored [K,N] needs N % 16 == 0 (16-byte TMA strides). The TN calls, where neither
+ * operand has rows along K, take any K. The tensor core reads
  * the M/N-contiguous tiles directly (no transposition pass). Other conventions as dg_fp8_gemm_nt.
  */
 dg_status dg_fp8_gemm_nn(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, uint16_t* D,
@@ -292,6 +293,138 @@ dg_status dg_fp8_grouped_masked_swiglu_ue8m0(const uint8_t* A, const int32_t* sA
 dg_status dg_fp8_grouped_masked_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B,
                                                  const int32_t* sB, const int32_t* masked_m, float* H, int G,
                                                  int M_max, int N, int K, dg_stream_t stream);
+
+/*
+ * Training of the gated feed-forward block. The gated projection in the dense and contiguous forms with
+ * its backward pass, the casts between the BF16 activations and the products' FP8 operands, and dropout.
+ * These are additions of this library: the pages fuse the SwiGLU for decode only (§ "Mega MoE") and leave
+ * casts to other kernels (§ "GEMM arayüzü ve yerleşim kısıtları").
+ *
+ * One step of an expert layer (contiguous groups; the dense calls in brackets; sizes: M tokens, K features):
+ *   forward   dg_cast_fp8(x -> rows, blocks);  H = dg_fp8_grouped_contiguous_swiglu [dg_fp8_gemm_nt_swiglu], GU saved;
+ *             dg_cast_fp8(H -> rows);          y = dg_fp8_grouped_contiguous [dg_fp8_gemm_nt]
+ *   backward  dg_cast_fp8(dy -> rows, columns);  dH = dg_fp8_grouped_contiguous_nn [dg_fp8_gemm_nn];
+ *             dg_swiglu_backward_fp8(dH, GU -> dGU rows, dGU columns, H blocks);
+ *             dx  = dg_fp8_grouped_contiguous_nn [dg_fp8_gemm_nn] (dGU rows, W),
+ *             dW  = dg_fp8_k_grouped_gemm_tn_contiguous [dg_fp8_gemm_tn] (dGU columns, x blocks),
+ *             dW2 = the same (dy columns, H blocks).
+ *
+ * Dropout is a function of rng, a device array {seed, offset} of two uint64 that the host never reads (a
+ * captured graph draws new masks when the program updates it), of p, and of the element's flat index i:
+ * with T = round(65536 p), element i is dropped when 16 bits of Philox4x32-10 (Salmon et al., "Parallel
+ * random numbers: as easy as 1, 2, 3", SC'11) fall below T, else scaled by 65536 / (65536 - T), so the
+ * expectation is exact. The key is `seed`, the counter {i / 8, offset} (64 bits each, low words first), the
+ * 16 bits are half i % 2 (0: low) of word (i % 8) / 2. A dropped element is 0 whatever it was. No mask is
+ * stored: the backward pass draws it again. p in [0, 1), T <= 65535; with T = 0 rng is not read (may be NULL).
+ */
+
+/*
+ * The gated projection: H[m,j] = dropout(silu(D[m,j]) · D[m,I+j]), D = A·Bᵀ with B's N = 2I rows the I gate
+ * rows, then the I up rows (I a multiple of 128; SwiGLU as in dg_fp8_grouped_masked_swiglu). A, sA, B, sB,
+ * m_indices and the grouped padding rules are those of dg_fp8_gemm_nt and dg_fp8_grouped_contiguous.
+ *   H   [M, I] BF16 bits (or FP32), formed from the FP32 accumulators and rounded once; the dropout index
+ *       is m·I + j
+ *   GU  [M, 2I] BF16 bits, 16-byte aligned, or NULL: D, rounded, for the backward pass
+ * Rows of H and GU that the contiguous form leaves untouched in D stay untouched. Few tiles split K as the
+ * plain calls do (clusters or the workspace).
+ */
+dg_status dg_fp8_gemm_nt_swiglu(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, uint16_t* H,
+                                uint16_t* GU, const uint64_t* rng, double p, int M, int N, int K,
+                                dg_stream_t stream);
+dg_status dg_fp8_gemm_nt_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, float* H,
+                                    uint16_t* GU, const uint64_t* rng, double p, int M, int N, int K,
+                                    dg_stream_t stream);
+dg_status dg_fp8_gemm_nt_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                      uint16_t* H, uint16_t* GU, const uint64_t* rng, double p, int M, int N, int K,
+                                      dg_stream_t stream);
+dg_status dg_fp8_gemm_nt_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                          float* H, uint16_t* GU, const uint64_t* rng, double p, int M, int N, int K,
+                                          dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_swiglu(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                           const int32_t* m_indices, uint16_t* H, uint16_t* GU, const uint64_t* rng,
+                                           double p, int M_total, int N, int K, int G, dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                               const int32_t* m_indices, float* H, uint16_t* GU, const uint64_t* rng,
+                                               double p, int M_total, int N, int K, int G, dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                 const int32_t* sB, const int32_t* m_indices, uint16_t* H,
+                                                 uint16_t* GU, const uint64_t* rng, double p, int M_total, int N,
+                                                 int K, int G, dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                     const int32_t* sB, const int32_t* m_indices, float* H,
+                                                     uint16_t* GU, const uint64_t* rng, double p, int M_total, int N,
+                                                     int K, int G, dg_stream_t stream);
+
+/*
+ * The contiguous-layout grouped GEMM with B stored [G, K, N] (N contiguous): D[m] = Σ_k A[m,k]·B[g(m)][k,:], the
+ * input gradient of an expert layer from the forward pass's weights (its [G, N, K] is this B with N and K
+ * exchanged; its scales transposed per group). K a multiple of 128, N of 16.
+ *   A [M_total,K]   sA [K/128][align4(M_total)]   B [G,K,N]   sB [G][ceil(N/128)][K/128]   D [M_total,N]
+ * Everything else as dg_fp8_grouped_contiguous.
+ */
+dg_status dg_fp8_grouped_contiguous_nn(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                       const int32_t* m_indices, uint16_t* D, int M_total, int N, int K, int G,
+                                       dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_nn_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                           const int32_t* m_indices, float* D, int M_total, int N, int K, int G,
+                                           dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_nn_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                             const int32_t* m_indices, uint16_t* D, int M_total, int N, int K, int G,
+                                             dg_stream_t stream);
+dg_status dg_fp8_grouped_contiguous_nn_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                 const int32_t* sB, const int32_t* m_indices, float* D, int M_total,
+                                                 int N, int K, int G, dg_stream_t stream);
+
+/*
+ * The backward pass of the gated projection's activation, cast to FP8 where it is formed. From dH [M,I] and
+ * the saved GU = [g u] [M,2I] (BF16 bits), with t = dropout(dH) under the forward pass's rng and p, s = 1/(1 + e^-g):
+ *     dg = t·u·s·(1 + g·(1 - s)),   du = t·g·s      (FP32)
+ * and dGU = [dg du] [M,2I] in one or both of two forms (either pair may be NULL):
+ *   dGUr, sR [2I/128][align4(M)]: 1x128 groups of each row (A of the NN products: dX)
+ *   dGUc, sC [ceil(M/128)][2I]:   128x1 groups of each column (A, stored [K,M], of the TN and K-grouped products: dW)
+ *   Hb, sHb [I/128][ceil(M/128)]: optional: H = dropout(silu(g)·u) again, in 128x128 blocks (B, stored [K,N],
+ *                                 of the down projection's dW)
+ * m_indices [M] (or NULL): rows with m_indices[m] < 0 (padding) count as zero and are not read.
+ * The cast of a group is that of dg_cast_fp8.
+ */
+dg_status dg_swiglu_backward_fp8(const uint16_t* dH, const uint16_t* GU, const int32_t* m_indices,
+                                 const uint64_t* rng, double p, uint8_t* dGUr, float* sR, uint8_t* dGUc, float* sC,
+                                 uint8_t* Hb, float* sHb, int M, int I, dg_stream_t stream);
+dg_status dg_swiglu_backward_fp8_ue8m0(const uint16_t* dH, const uint16_t* GU, const int32_t* m_indices,
+                                       const uint64_t* rng, double p, uint8_t* dGUr, int32_t* sR, uint8_t* dGUc,
+                                       int32_t* sC, uint8_t* Hb, int32_t* sHb, int M, int I, dg_stream_t stream);
+
+/*
+ * E4M3 casts of X [G,M,N] (BF16 bits) from one read, in the layouts the products read. Each form is a pair of
+ * codes [G,M,N] (X's own order) and scales; forms that are not wanted are NULL:
+ *   Xr, sR [G][ceil(N/128)][align4(M)]: 1x128 groups of each row (A of the NT and NN products; entries m >= M are
+ *                                       0, packed 127)
+ *   Xc, sC [G][ceil(M/128)][align4(N)]: 128x1 groups of each column (A, stored [K,M], of the TN and K-grouped products)
+ *   Xb: 128x128 blocks, with sB [G][ceil(M/128)][ceil(N/128)] (B stored [N,K]) and/or sBt, its transpose
+ *       [G][ceil(N/128)][ceil(M/128)] (B stored [K,N])
+ * The cast of a group with the largest magnitude amax, a = max(amax, 2^-100) (amax = 0: codes 0, scale 1):
+ *   FP32 scales: code = e4m3_rne(clamp(x · (448/a), ±448)), scale = a/448 (IEEE FP32 divisions and product);
+ *   UE8M0: scale = the smallest power of two s with a/s <= 448, code = e4m3_rne(x/s); packed as everywhere,
+ *          the words' unused bytes 127.
+ * A NaN becomes the NaN code and does not set the scale; a group with an infinity dequantises to NaN.
+ * N a multiple of 16; X and the codes 16-byte aligned; outputs must not overlap X or one another. m_indices
+ * [M] (G = 1 only, or NULL): rows with m_indices[m] < 0 count as zero and are not read.
+ */
+dg_status dg_cast_fp8(const uint16_t* X, const int32_t* m_indices, uint8_t* Xr, float* sR, uint8_t* Xc, float* sC,
+                      uint8_t* Xb, float* sB, float* sBt, int G, int M, int N, dg_stream_t stream);
+dg_status dg_cast_fp8_ue8m0(const uint16_t* X, const int32_t* m_indices, uint8_t* Xr, int32_t* sR, uint8_t* Xc,
+                            int32_t* sC, uint8_t* Xb, int32_t* sB, int32_t* sBt, int G, int M, int N,
+                            dg_stream_t stream);
+
+/*
+ * Y[i] = R[i] + dropout(X[i]) over n elements (R may be NULL: Y = dropout(X)), in FP32, rounded once. Y may be X
+ * or R itself, and may not overlap them otherwise. Any alignment of the element type (16-byte aligned tensors
+ * are faster). The backward pass is the same call on dY, without R.
+ */
+dg_status dg_dropout_bf16(const uint16_t* X, const uint16_t* R, uint16_t* Y, const uint64_t* rng, double p, long long n,
+                          dg_stream_t stream);
+dg_status dg_dropout_f32(const float* X, const float* R, float* Y, const uint64_t* rng, double p, long long n,
+                         dg_stream_t stream);
 
 /*
  * Accumulating dense GEMM: D = C + A·Bᵀ, the full definition of fp8_gemm_nt ("DeepGEMM: İnce

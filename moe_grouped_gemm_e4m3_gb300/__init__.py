@@ -16,6 +16,12 @@ The names mirror the C ABI:
   D [G,M,N]
 * ``dg_fp8_grouped_masked_swiglu(A, sA, B, sB, masked_m, H)``  masked GEMM + SwiGLU: B [G, 2I, K], H [G, M_max, I]
 * ``dg_fp8_gemm_nt_acc_f32(A, sA, B, sB, C, D)``             D = C + A·Bᵀ (FP32 C and D; C may be D)
+* ``dg_fp8_gemm_nt_swiglu(A, sA, B, sB, H, GU=, rng=, p=)``   gated projection H = dropout(silu(gate)·up), dense;
+  ``dg_fp8_grouped_contiguous_swiglu`` over contiguous groups; GU [rows, 2I] saves the pre-activations
+* ``dg_swiglu_backward_fp8(dH, GU, dGUr, sR, dGUc, sC, Hb=, sHb=, ...)``  its backward pass up to the products, cast to E4M3
+* ``dg_fp8_grouped_contiguous_nn(A, sA, B, sB, m_indices, D)``  contiguous layout with B stored [G, K, N]
+* ``dg_cast_fp8(X, Xr=, sR=, Xc=, sC=, Xb=, sB=, sBt=, m_indices=)``  BF16 to E4M3 with 1x128, 128x1 and 128x128 scales
+* ``dg_dropout(X, Y, rng, p, R=)``  Y = R + dropout(X) from a counter-based generator, BF16 or FP32
 * ``*_ue8m0`` variants take power-of-two scales as packed UE8M0 int32 words (four K-groups per
   word, byte j = K-group 4q+j): sA int32 [ceil(ceil(K/128)/4), align4(rows)] (masked: leading G),
   sB int32 [G, ceil(N/128), ceil(ceil(K/128)/4)]. They run the block-scaled tensor-core kernel.
@@ -51,6 +57,13 @@ __all__ = [
     "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0", "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32", "EXPORTED_SYMBOLS", "DG_OK", "DG_ERR_INVALID_ARG", "DG_ERR_ALIGNMENT", "DG_ERR_UNSUPPORTED",
     "DG_ERR_CUDA", "DG_ERR_DEVICE_STATUS", "DG_DEV_BAD_GROUP_INDEX", "DG_DEV_BAD_MASKED_M",
     "DG_DEV_TIMEOUT", "DG_DEV_BAD_SCALE",
+    "dg_fp8_gemm_nt_swiglu", "dg_fp8_gemm_nt_swiglu_f32", "dg_fp8_gemm_nt_swiglu_ue8m0",
+    "dg_fp8_gemm_nt_swiglu_ue8m0_f32", "dg_fp8_grouped_contiguous_swiglu",
+    "dg_fp8_grouped_contiguous_swiglu_f32", "dg_fp8_grouped_contiguous_swiglu_ue8m0",
+    "dg_fp8_grouped_contiguous_swiglu_ue8m0_f32", "dg_fp8_grouped_contiguous_nn",
+    "dg_fp8_grouped_contiguous_nn_f32", "dg_fp8_grouped_contiguous_nn_ue8m0",
+    "dg_fp8_grouped_contiguous_nn_ue8m0_f32", "dg_swiglu_backward_fp8", "dg_swiglu_backward_fp8_ue8m0",
+    "dg_cast_fp8", "dg_cast_fp8_ue8m0", "dg_dropout",
 ]
 
 DG_OK, DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED, DG_ERR_CUDA, DG_ERR_DEVICE_STATUS = range(6)
@@ -74,6 +87,13 @@ EXPORTED_SYMBOLS = (
     "dg_fp8_gemm_nn_ue8m0", "dg_fp8_gemm_nn_ue8m0_f32", "dg_fp8_gemm_tn_ue8m0", "dg_fp8_gemm_tn_ue8m0_f32", "dg_fp8_gemm_tt_ue8m0", "dg_fp8_gemm_tt_ue8m0_f32",
     "dg_fp8_k_grouped_gemm_tn_contiguous", "dg_fp8_k_grouped_gemm_tn_contiguous_f32",
     "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0", "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32",
+    "dg_fp8_gemm_nt_swiglu", "dg_fp8_gemm_nt_swiglu_f32", "dg_fp8_gemm_nt_swiglu_ue8m0",
+    "dg_fp8_gemm_nt_swiglu_ue8m0_f32", "dg_fp8_grouped_contiguous_swiglu",
+    "dg_fp8_grouped_contiguous_swiglu_f32", "dg_fp8_grouped_contiguous_swiglu_ue8m0",
+    "dg_fp8_grouped_contiguous_swiglu_ue8m0_f32", "dg_fp8_grouped_contiguous_nn",
+    "dg_fp8_grouped_contiguous_nn_f32", "dg_fp8_grouped_contiguous_nn_ue8m0",
+    "dg_fp8_grouped_contiguous_nn_ue8m0_f32", "dg_swiglu_backward_fp8", "dg_swiglu_backward_fp8_ue8m0",
+    "dg_cast_fp8", "dg_cast_fp8_ue8m0", "dg_dropout_bf16", "dg_dropout_f32",
 )
 
 
@@ -138,6 +158,22 @@ def load(build_if_missing: bool = True):
                  "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0", "dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32"):
         f = getattr(lib, name)
         f.restype, f.argtypes = i32, [P, P, P, P, P, P, i32, i32, i32, i32, P]
+    f64 = ctypes.c_double
+    for ue in ("", "_ue8m0"):
+        for f32 in ("", "_f32"):
+            f = getattr(lib, f"dg_fp8_gemm_nt_swiglu{ue}{f32}")
+            f.restype, f.argtypes = i32, [P, P, P, P, P, P, P, f64, i32, i32, i32, P]
+            f = getattr(lib, f"dg_fp8_grouped_contiguous_swiglu{ue}{f32}")
+            f.restype, f.argtypes = i32, [P, P, P, P, P, P, P, P, f64, i32, i32, i32, i32, P]
+            f = getattr(lib, f"dg_fp8_grouped_contiguous_nn{ue}{f32}")
+            f.restype, f.argtypes = i32, [P, P, P, P, P, P, i32, i32, i32, i32, P]
+        f = getattr(lib, f"dg_swiglu_backward_fp8{ue}")
+        f.restype, f.argtypes = i32, [P, P, P, P, f64, P, P, P, P, P, P, i32, i32, P]
+        f = getattr(lib, f"dg_cast_fp8{ue}")
+        f.restype, f.argtypes = i32, [P, P, P, P, P, P, P, P, P, i32, i32, i32, P]
+    for name in ("dg_dropout_bf16", "dg_dropout_f32"):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = i32, [P, P, P, P, f64, ctypes.c_longlong, P]
     for name in ("dg_query_config", "dg_query_config_ue8m0"):
         f = getattr(lib, name)
         f.restype, f.argtypes = i32, [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
@@ -472,6 +508,214 @@ def dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0(A, sA, B, sB, k_offsets, D, stream
 
 def dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32(A, sA, B, sB, k_offsets, D, stream=None):
     return _k_grouped("dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32", True, A, sA, B, sB, k_offsets, D, stream)
+
+
+def _opt(t, name, dtypes, shape):
+    """The pointer of an optional tensor of this shape (None: null)."""
+    if t is None:
+        return None
+    _expect(t, name, shape)
+    return _ptr(t, name, dtypes)
+
+
+def _rng(rng, p):
+    """The pointer of the generator's state: a CUDA int64 (or uint64) tensor {seed, offset}."""
+    import torch
+    if rng is None:
+        return None
+    return _opt(rng, "rng", (torch.int64, torch.uint64), (2,))
+
+
+def _bf16():
+    import torch
+    return (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _gated(name, f32, A, sA, B, sB, m_indices, H, GU, rng, p, stream):
+    import torch
+    a, b = _shape(A, "A"), _shape(B, "B")
+    grouped = "contiguous" in name
+    if len(a) != 2 or len(b) != (3 if grouped else 2):
+        raise ValueError(f"gated projection: A must be [M, K] and B {'[G, 2I, K]' if grouped else '[2I, K]'}, "
+                         f"got {list(a)} and {list(b)}")
+    M, K = a
+    G, N = (b[0], b[1]) if grouped else (1, b[0])
+    if b[-1] != K:
+        raise ValueError(f"B has K = {b[-1]}, A has K = {K}")
+    if N % 2:
+        raise ValueError(f"B must hold I gate rows and I up rows, got {N}")
+    nks = _scale_k(name, K)
+    _expect(sA, "sA", (nks, _align4(M)))
+    _expect(sB, "sB", ((G,) if grouped else ()) + (_cdiv(N, 128), nks))
+    _expect(H, "H", (M, N // 2))
+    st = _scale_types(name)
+    head = (_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()), _ptr(sB, "sB", st))
+    tail = (_ptr(H, "H", _d_types(f32)), _opt(GU, "GU", _bf16(), (M, N)), _rng(rng, p), p, M, N, K)
+    if grouped:
+        _expect(m_indices, "m_indices", (M,))
+        head, tail = head + (_ptr(m_indices, "m_indices", (torch.int32,)),), tail + (G,)
+    _check(getattr(load(), name)(*head, *tail, _stream(stream)))
+    return H
+
+
+def dg_fp8_gemm_nt_swiglu(A, sA, B, sB, H, GU=None, rng=None, p=0.0, stream=None):
+    """Gated projection H [M, I] = dropout(silu(A·Bgᵀ) · (A·Buᵀ)); B [2I, K] holds the I gate rows, then the I
+    up rows (I a multiple of 128). GU (bfloat16 [M, 2I], optional) receives the pre-activations. With p > 0,
+    rng is a CUDA int64 tensor {seed, offset}, read on the device."""
+    return _gated("dg_fp8_gemm_nt_swiglu", False, A, sA, B, sB, None, H, GU, rng, p, stream)
+
+
+def dg_fp8_gemm_nt_swiglu_f32(A, sA, B, sB, H, GU=None, rng=None, p=0.0, stream=None):
+    """As dg_fp8_gemm_nt_swiglu, with H in FP32."""
+    return _gated("dg_fp8_gemm_nt_swiglu_f32", True, A, sA, B, sB, None, H, GU, rng, p, stream)
+
+
+def dg_fp8_gemm_nt_swiglu_ue8m0(A, sA, B, sB, H, GU=None, rng=None, p=0.0, stream=None):
+    """dg_fp8_gemm_nt_swiglu with packed UE8M0 scales."""
+    return _gated("dg_fp8_gemm_nt_swiglu_ue8m0", False, A, sA, B, sB, None, H, GU, rng, p, stream)
+
+
+def dg_fp8_gemm_nt_swiglu_ue8m0_f32(A, sA, B, sB, H, GU=None, rng=None, p=0.0, stream=None):
+    return _gated("dg_fp8_gemm_nt_swiglu_ue8m0_f32", True, A, sA, B, sB, None, H, GU, rng, p, stream)
+
+
+def dg_fp8_grouped_contiguous_swiglu(A, sA, B, sB, m_indices, H, GU=None, rng=None, p=0.0, stream=None):
+    """The gated projection over contiguous groups: B [G, 2I, K], row m uses expert m_indices[m] (-1: padding,
+    untouched in H and GU)."""
+    return _gated("dg_fp8_grouped_contiguous_swiglu", False, A, sA, B, sB, m_indices, H, GU, rng, p, stream)
+
+
+def dg_fp8_grouped_contiguous_swiglu_f32(A, sA, B, sB, m_indices, H, GU=None, rng=None, p=0.0, stream=None):
+    return _gated("dg_fp8_grouped_contiguous_swiglu_f32", True, A, sA, B, sB, m_indices, H, GU, rng, p, stream)
+
+
+def dg_fp8_grouped_contiguous_swiglu_ue8m0(A, sA, B, sB, m_indices, H, GU=None, rng=None, p=0.0, stream=None):
+    """dg_fp8_grouped_contiguous_swiglu with packed UE8M0 scales."""
+    return _gated("dg_fp8_grouped_contiguous_swiglu_ue8m0", False, A, sA, B, sB, m_indices, H, GU, rng, p, stream)
+
+
+def dg_fp8_grouped_contiguous_swiglu_ue8m0_f32(A, sA, B, sB, m_indices, H, GU=None, rng=None, p=0.0, stream=None):
+    return _gated("dg_fp8_grouped_contiguous_swiglu_ue8m0_f32", True, A, sA, B, sB, m_indices, H, GU, rng, p, stream)
+
+
+def _contig_nn(name, f32, A, sA, B, sB, m_indices, D, stream):
+    import torch
+    a, b = _shape(A, "A"), _shape(B, "B")
+    if len(a) != 2 or len(b) != 3:
+        raise ValueError(f"contiguous NN: A must be [M_total, K] and B [G, K, N], got {list(a)} and {list(b)}")
+    M, K = a
+    G, N = b[0], b[2]
+    if b[1] != K:
+        raise ValueError(f"B has K = {b[1]}, A has K = {K}")
+    nks = _scale_k(name, K)
+    _expect(sA, "sA", (nks, _align4(M)))
+    _expect(sB, "sB", (G, _cdiv(N, 128), nks))
+    _expect(m_indices, "m_indices", (M,))
+    _expect(D, "D", (M, N))
+    st = _scale_types(name)
+    _check(getattr(load(), name)(_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()),
+                                 _ptr(sB, "sB", st), _ptr(m_indices, "m_indices", (torch.int32,)),
+                                 _ptr(D, "D", _d_types(f32)), M, N, K, G, _stream(stream)))
+    return D
+
+
+def dg_fp8_grouped_contiguous_nn(A, sA, B, sB, m_indices, D, stream=None):
+    """Contiguous-layout grouped GEMM with B stored [G, K, N] (N contiguous; K a multiple of 128), e.g. the
+    experts' input gradient dX = dY·W from the forward pass's W; sB [G, ceil(N/128), K/128]."""
+    return _contig_nn("dg_fp8_grouped_contiguous_nn", False, A, sA, B, sB, m_indices, D, stream)
+
+
+def dg_fp8_grouped_contiguous_nn_f32(A, sA, B, sB, m_indices, D, stream=None):
+    return _contig_nn("dg_fp8_grouped_contiguous_nn_f32", True, A, sA, B, sB, m_indices, D, stream)
+
+
+def dg_fp8_grouped_contiguous_nn_ue8m0(A, sA, B, sB, m_indices, D, stream=None):
+    """dg_fp8_grouped_contiguous_nn with packed UE8M0 scales."""
+    return _contig_nn("dg_fp8_grouped_contiguous_nn_ue8m0", False, A, sA, B, sB, m_indices, D, stream)
+
+
+def dg_fp8_grouped_contiguous_nn_ue8m0_f32(A, sA, B, sB, m_indices, D, stream=None):
+    return _contig_nn("dg_fp8_grouped_contiguous_nn_ue8m0_f32", True, A, sA, B, sB, m_indices, D, stream)
+
+
+def _swiglu_backward(name, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream):
+    import torch
+    h = _shape(dH, "dH")
+    if len(h) != 2:
+        raise ValueError(f"dH must be [M, I], got {list(h)}")
+    M, I = h
+    _expect(GU, "GU", (M, 2 * I))
+    st, q = _scale_types(name), _fp8_types()
+    wM, wN = _scale_k(name, M), _scale_k(name, 2 * I)
+    _check(getattr(load(), name)(
+        _ptr(dH, "dH", _bf16()), _ptr(GU, "GU", _bf16()), _opt(m_indices, "m_indices", (torch.int32,), (M,)),
+        _rng(rng, p), p, _opt(dGUr, "dGUr", q, (M, 2 * I)), _opt(sR, "sR", st, (wN, _align4(M))),
+        _opt(dGUc, "dGUc", q, (M, 2 * I)), _opt(sC, "sC", st, (wM, 2 * I)), _opt(Hb, "Hb", q, (M, I)),
+        _opt(sHb, "sHb", st, (_cdiv(I, 128), wM)), M, I, _stream(stream)))
+    return dGUr, dGUc
+
+
+def dg_swiglu_backward_fp8(dH, GU, dGUr=None, sR=None, dGUc=None, sC=None, Hb=None, sHb=None, m_indices=None,
+                           rng=None, p=0.0, stream=None):
+    """The gated projection's backward pass up to the products: from dH [M, I] and the saved GU [M, 2I]
+    (bfloat16), the gradients of the pre-activations as E4M3 in one or both forms: dGUr with sR
+    [2I/128, align4(M)] (A of the NN products: dX = dGU·W) and dGUc with sC [ceil(M/128), 2I] (A of the TN
+    and K-grouped products: dW = dGUᵀ·X). Hb with sHb [I/128, ceil(M/128)], optional: H again in 128x128 blocks
+    (B of the down projection's weight gradient). Rows with m_indices[m] < 0 count as zero. rng and p as in
+    the forward call."""
+    return _swiglu_backward("dg_swiglu_backward_fp8", dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream)
+
+
+def dg_swiglu_backward_fp8_ue8m0(dH, GU, dGUr=None, sR=None, dGUc=None, sC=None, Hb=None, sHb=None, m_indices=None,
+                                 rng=None, p=0.0, stream=None):
+    """dg_swiglu_backward_fp8 with power-of-two scales packed as UE8M0: sR [ceil(2I/512), align4(M)], sC
+    [ceil(M/512), 2I], sHb [I/128, ceil(M/512)] int32."""
+    return _swiglu_backward("dg_swiglu_backward_fp8_ue8m0", dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream)
+
+
+def _cast(name, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream):
+    import torch
+    x = _shape(X, "X")
+    if len(x) not in (2, 3):
+        raise ValueError(f"X must be [M, N] or [G, M, N], got {list(x)}")
+    M, N = x[-2:]
+    g = x[:-2]
+    st, q = _scale_types(name), _fp8_types()
+    wM, wN = _scale_k(name, M), _scale_k(name, N)
+    _check(getattr(load(), name)(
+        _ptr(X, "X", _bf16()), _opt(m_indices, "m_indices", (torch.int32,), (M,)), _opt(Xr, "Xr", q, x),
+        _opt(sR, "sR", st, g + (wN, _align4(M))), _opt(Xc, "Xc", q, x), _opt(sC, "sC", st, g + (wM, _align4(N))),
+        _opt(Xb, "Xb", q, x), _opt(sB, "sB", st, g + (_cdiv(M, 128), wN)),
+        _opt(sBt, "sBt", st, g + (_cdiv(N, 128), wM)), g[0] if g else 1, M, N, _stream(stream)))
+
+
+def dg_cast_fp8(X, Xr=None, sR=None, Xc=None, sC=None, Xb=None, sB=None, sBt=None, m_indices=None, stream=None):
+    """E4M3 casts of X (bfloat16 [M, N] or [G, M, N]) in the layouts the products read, from one read of X:
+    Xr with sR [ceil(N/128), align4(M)]: 1x128 groups of each row (A of the NT and NN products);
+    Xc with sC [ceil(M/128), align4(N)]: 128x1 groups of each column (A, stored [K, M], of the TN and K-grouped products);
+    Xb with sB [ceil(M/128), ceil(N/128)] (B stored [N, K]) and/or sBt, its transpose (B stored [K, N]): 128x128 blocks.
+    Rows with m_indices[m] < 0 count as zero."""
+    _cast("dg_cast_fp8", X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream)
+
+
+def dg_cast_fp8_ue8m0(X, Xr=None, sR=None, Xc=None, sC=None, Xb=None, sB=None, sBt=None, m_indices=None, stream=None):
+    """dg_cast_fp8 with power-of-two scales packed as UE8M0 words: sR [ceil(N/512), align4(M)], sC
+    [ceil(M/512), align4(N)], sB [ceil(M/128), ceil(N/512)], sBt [ceil(N/128), ceil(M/512)] int32."""
+    _cast("dg_cast_fp8_ue8m0", X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream)
+
+
+def dg_dropout(X, Y, rng, p, R=None, stream=None):
+    """Y = R + dropout(X) (R optional), bfloat16 or float32 tensors of one shape; Y may be X or R. rng is a CUDA
+    int64 tensor {seed, offset}; the mask is a function of it, p and the flat index. Backward: the same
+    call on the gradient, without R."""
+    import torch
+    f32 = X.dtype == torch.float32
+    dt = (torch.float32,) if f32 else _bf16()
+    shape = _shape(X, "X")
+    _expect(Y, "Y", shape)
+    f = load().dg_dropout_f32 if f32 else load().dg_dropout_bf16
+    _check(f(_ptr(X, "X", dt), _opt(R, "R", dt, shape), _ptr(Y, "Y", dt), _rng(rng, p), p, X.numel(), _stream(stream)))
+    return Y
 
 
 def dg_fp8_grouped_masked_swiglu(A, sA, B, sB, masked_m, H, stream=None):

@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -238,7 +239,9 @@ struct Config {
   int raster_m;
 };
 
-Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false) {
+// wide_only: BN = 256 whatever N (the gated projection, whose tile pairs 128 gate and 128 up rows).
+Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false,
+                     bool wide_only = false) {
   // Cost model calibrated on GB300 (sm_103a), times in microseconds per CTA:
   //  * compute: one K-block (BM=128, BK=128) costs ~0.55 (BN=256) or ~0.50 (BN=128: an N=128 MMA
   //    takes as long as an N=256 one, for half the work);
@@ -260,10 +263,11 @@ Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool 
   int best_s = 1;
   double best_t = 1e300;
   const int max_s = (mode == dg::kMasked) ? 1 : kMaxSplits;
-  if (block_scaled) bn = 256;
+  if (block_scaled) wide_only = true;
+  if (wide_only) bn = 256;
   for (int cand_bn = 128; cand_bn <= 256; cand_bn += 128) {
-    if (cand_bn == 256 && N <= 128 && !block_scaled) continue;
-    if (cand_bn == 128 && block_scaled) continue;
+    if (cand_bn == 256 && N <= 128 && !wide_only) continue;
+    if (cand_bn == 128 && wide_only) continue;
     const int n_blocks = ceil_div(N, cand_bn);
     const int tiles = m_blocks * n_blocks;
     const double t_compute = block_scaled ? 0.30 : (cand_bn == 256 ? 0.55 : 0.50);
@@ -292,7 +296,7 @@ Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool 
   // Tuning overrides (environment): DG_BLOCK_N in {128, 256} and DG_SPLITS >= 1 (dense and
   // contiguous only; a split that would exceed one wave of units is still allowed here).
   int bn_final = bn, tiles_final = tiles;
-  if (const char* e = block_scaled ? nullptr : std::getenv("DG_BLOCK_N")) {
+  if (const char* e = wide_only ? nullptr : std::getenv("DG_BLOCK_N")) {
     const int v = std::atoi(e);
     if (v == 128 || v == 256) { bn_final = v; tiles_final = m_blocks * ceil_div(N, v); }
   }
@@ -411,6 +415,26 @@ constexpr size_t kNoAllocCounterBytes = 4096 * sizeof(int);   // 4096 output til
 constexpr size_t kNoAllocWorkspaceBytes = size_t(20) << 20;   // 20 MiB of FP32 partials
 dg_status noalloc_scratch(void** out);
 
+// The gated projection's arguments beside the GEMM's: where the pre-activations go (or null), and the
+// dropout of H.
+struct GatedArgs {
+  uint16_t* GU;
+  dg::Dropout drop;
+};
+
+// The dropout of probability p as the kernels take it.
+dg_status make_dropout(const uint64_t* rng, double p, dg::Dropout* d) {
+  if (!(p >= 0.0 && p < 1.0)) return fail(DG_ERR_INVALID_ARG, "dropout: p must be in [0, 1)");
+  const double t = std::floor(p * 65536.0 + 0.5);
+  if (t >= 65536.0) return fail(DG_ERR_INVALID_ARG, "dropout: p rounds to 1 (it is held in 1/65536)");
+  if (t > 0.0 && !rng) return fail(DG_ERR_INVALID_ARG, "dropout: null rng with p > 0");
+  if (!aligned(rng, 8)) return fail(DG_ERR_ALIGNMENT, "dropout: rng must be 8-byte aligned");
+  d->rng = rng;
+  d->threshold = (uint32_t)t;
+  d->scale = (float)(65536.0 / (65536.0 - t));
+  return DG_OK;
+}
+
 // Common implementation of the six GEMM entry points.
 //   mode dense: rows = M, G = 1;  contiguous: rows = M_total;  masked: rows = M_max (per group).
 //   sA/sB are FP32 scales, or (block_scaled) packed UE8M0 words: sA [G][ceil(nkb/4)][ldsa] and
@@ -419,11 +443,12 @@ dg_status noalloc_scratch(void** out);
 //   noalloc (dense, BF16, FP32 scales only): split-K scratch comes from the fixed array of the
 //   allocation-free entry point instead of the lazily grown workspace; a shape that needs more
 //   than it holds returns DG_ERR_UNSUPPORTED.
+//   gated (dense and contiguous): the gated projection; D is H [rows, N/2].
 dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, const uint8_t* B, const void* sB,
                    const int32_t* idx, void* D, int rows, int N, int K, int G, cudaStream_t stream,
                    bool block_scaled = false, const float* C = nullptr, bool accumulate = false,
                    bool swiglu = false, bool a_mn = false, bool b_mn = false, bool noalloc = false,
-                   float* h_scales = nullptr) {
+                   float* h_scales = nullptr, const GatedArgs* gated = nullptr) {
   t_last_error.clear();
   // h_scales: the fused SwiGLU writes H as FP8 codes (D, bytes) and these 1x128-group scales
   const bool quant_h = h_scales != nullptr;
@@ -438,17 +463,23 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
     return fail(DG_ERR_INVALID_ARG, "the accumulating form needs a C pointer and FP32 D (dense only)");
   if (swiglu && (mode != dg::kMasked || accumulate))
     return fail(DG_ERR_INVALID_ARG, "the fused SwiGLU form is masked and not accumulating");
-  if (swiglu && N % 256 != 0)
+  if (gated && (mode == dg::kMasked || swiglu || accumulate || a_mn || b_mn || noalloc))
+    return fail(DG_ERR_INVALID_ARG, "the gated projection is dense or contiguous, NT");
+  if ((swiglu || gated) && N % 256 != 0)
     return fail(DG_ERR_ALIGNMENT, "fused SwiGLU: B must hold 2I rows per group with I a multiple of 128");
-  if ((a_mn || b_mn) && mode != dg::kDense)
-    return fail(DG_ERR_INVALID_ARG, "the NN/TN/TT layouts are dense");
+  if ((a_mn || b_mn) && mode != dg::kDense && (a_mn || mode != dg::kContiguous))
+    return fail(DG_ERR_INVALID_ARG, "the TN/TT layouts are dense, the NN layout dense or contiguous");
   if (rows == 0 || N == 0 || G == 0) return DG_OK;
   if (K == 0) return fail(DG_ERR_INVALID_ARG, "K must be positive");
   if (!A || !sA || !B || !sB || !D) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
   if (a_mn && rows % 16 != 0) return fail(DG_ERR_ALIGNMENT, "A stored [K,M]: M must be a multiple of 16");
   if (b_mn && N % 16 != 0) return fail(DG_ERR_ALIGNMENT, "B stored [K,N]: N must be a multiple of 16");
   if (mode != dg::kDense && !idx) return fail(DG_ERR_INVALID_ARG, mode == dg::kMasked ? "null masked_m" : "null m_indices");
-  if (K % 16 != 0) return fail(DG_ERR_ALIGNMENT, "K must be a multiple of 16 (16-byte rows of E4M3 A and B)");
+  // (with both operands stored [K, ...] no row runs along K)
+  if (K % 16 != 0 && !(a_mn && b_mn))
+    return fail(DG_ERR_ALIGNMENT, "K must be a multiple of 16 (16-byte rows of E4M3 A and B)");
+  if (b_mn && mode == dg::kContiguous && K % 128 != 0)
+    return fail(DG_ERR_ALIGNMENT, "contiguous NN: K must be a multiple of 128 (the groups of B [G,K,N] are K rows apart)");
   if (N % (out_f32 ? 4 : 8) != 0)
     return fail(DG_ERR_ALIGNMENT, out_f32 ? "N must be a multiple of 4 (16-byte rows of FP32 D)"
                                           : "N must be a multiple of 8 (16-byte rows of BF16 D)");
@@ -464,17 +495,21 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
       return fail(DG_ERR_INVALID_ARG, "C and D overlap without being the same matrix");
   }
   const long long rows_total = (long long)rows * (mode == dg::kMasked ? G : 1);
-  const long long b_rows = (long long)N * (mode == dg::kDense ? 1 : G);
-  if (rows_total > INT_MAX - 256 || b_rows > INT_MAX - 256 || K > INT_MAX - 256)
+  // B's extent along its rows' axis: G·N rows of K, or (stored [G, K, N]) N columns of G·K rows
+  const long long b_rows = (long long)N * (mode == dg::kDense || b_mn ? 1 : G);
+  const long long b_ks = (long long)K * (mode == dg::kDense || !b_mn ? 1 : G);
+  if (gated && gated->GU && !aligned(gated->GU, 16)) return fail(DG_ERR_ALIGNMENT, "GU must be 16-byte aligned");
+  if (rows_total > INT_MAX - 256 || b_rows > INT_MAX - 256 || b_ks > INT_MAX - 256)
     return fail(DG_ERR_UNSUPPORTED, "a tensor extent exceeds 2^31 - 257");
 
   DeviceState* st = nullptr;
   dg_status s = device_state(&st);
   if (s != DG_OK) return s;
   const int sms = effective_sms(*st);
-  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled);
+  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
+  // (the gated kernels have the footprint of the plain BN = 256 ones: the same cluster capacities)
   if (!swiglu) fit_cluster_splits(cfg, mode, K, block_scaled, out_f32);
-  const int d_cols = swiglu ? N / 2 : N;   // width of D (fused SwiGLU: H has I = N/2 columns)
+  const int d_cols = swiglu || gated ? N / 2 : N;   // width of D (fused SwiGLU: H has I = N/2 columns)
   if (swiglu) {
     // one tile = 128 gate rows + 128 up rows of B; no host split-K (the tail split may still apply)
     cfg.block_n = 256;
@@ -488,7 +523,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   if ((long long)cfg.tiles * cfg.splits > INT_MAX / 2) return fail(DG_ERR_UNSUPPORTED, "too many tiles");
 
   dg::LaunchArgs a;
-  std::memset(&a, 0, sizeof(a));
+  std::memset(static_cast<void*>(&a), 0, sizeof(a));
   dg::GemmParams& p = a.p;
   p.M = rows;
   p.N = N;
@@ -498,8 +533,8 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   p.nnb = ceil_div(N, 128);
   p.ldsa = dg_get_tma_aligned_size(rows, 4);
   p.num_m_blocks = ceil_div(rows, 128);
-  p.num_n_blocks = swiglu ? d_cols / 128 : ceil_div(N, cfg.block_n);
-  p.swiglu_i = swiglu ? d_cols : 0;
+  p.num_n_blocks = swiglu ? d_cols / 128 : ceil_div(N, cfg.block_n);   // (gated: 2I/256, the same I/128 blocks)
+  p.swiglu_i = swiglu || gated ? d_cols : 0;
   p.flags = (a_mn ? dg::kFlagAMN : 0) | (b_mn ? dg::kFlagBMN : 0) | (accumulate ? dg::kFlagAccumulate : 0) |
             wait_limit_flags();
   p.num_splits = cfg.splits;
@@ -529,7 +564,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   const bool cluster = use_cluster_split(cfg, mode, out_f32, block_scaled, swiglu);
   // Pairs of CTAs share B tiles (kFlagPairB): the persistent units are pairs of 128-row blocks by
   // BN columns, walked by clusters of 2; no tail split.
-  const int pair_cap = cluster ? 0 : pair_clusters(cfg, mode, rows, out_f32, block_scaled, swiglu, a_mn || b_mn);
+  const int pair_cap = cluster ? 0 : pair_clusters(cfg, mode, rows, out_f32, block_scaled, swiglu || gated, a_mn || b_mn);
   const bool pair = pair_cap > 0;
   if (pair) {
     const int m_pairs = ceil_div(ceil_div(rows, 128), 2);
@@ -578,12 +613,14 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                             128, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A")) != DG_OK) {
     return s;
   }
+  // rows of B's boxes: the gated tile's 64-row quarters (FP32 scales) or gate and up halves
+  const int b_box = gated && !block_scaled ? 64 : (swiglu || gated ? 128 : (pair ? cfg.block_n / 2 : cfg.block_n));
   if (b_mn) {   // B stored [K, N]: N contiguous, boxes of 128 N-bytes x 128 K-rows
-    if ((s = encode_2d(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, (uint64_t)b_rows, (uint64_t)K, (uint64_t)b_rows, 128,
+    if ((s = encode_2d(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, (uint64_t)b_rows, (uint64_t)b_ks, (uint64_t)b_rows, 128,
                        128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B")) != DG_OK)
       return s;
   } else if ((s = encode_2d(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, (uint64_t)K, (uint64_t)b_rows, (uint64_t)K, 128,
-                            (uint32_t)(swiglu ? 128 : (pair ? cfg.block_n / 2 : cfg.block_n)),
+                            (uint32_t)b_box,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B")) != DG_OK) {
     return s;
   }
@@ -598,6 +635,15 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                   (uint64_t)d_cols * 2, 32, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE, "D", CU_TENSOR_MAP_SWIZZLE_64B);
   }
   if (s != DG_OK) return s;
+  if (gated) {
+    a.gated.gu = gated->GU;
+    a.gated.drop = gated->drop;
+    // (without GU the map only has to be valid)
+    if ((s = encode_2d(&a.gated.tmGU, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, gated->GU ? static_cast<void*>(gated->GU) : D,
+                       (uint64_t)N, (uint64_t)rows_total, (uint64_t)N * 2, 32, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE, "GU",
+                       CU_TENSOR_MAP_SWIZZLE_64B)) != DG_OK)
+      return s;
+  }
 
   a.block_n = cfg.block_n;
   a.out_f32 = out_f32;
@@ -607,11 +653,16 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   if (print_configs()) {
     static const char* names[3] = {"dense", "contiguous", "masked"};
     std::fprintf(stderr, "[dg] %s%s%s%s rows=%d N=%d K=%d G=%d: BM=128 BN=%d stages=%d splits=%d%s grid=%d tiles=%d\n",
-                 names[mode], block_scaled ? "/ue8m0" : "", swiglu ? "/swiglu" : "", out_f32 ? "/f32" : "", rows, N, K,
+                 names[mode], block_scaled ? "/ue8m0" : "", swiglu || gated ? "/swiglu" : "", out_f32 ? "/f32" : "", rows, N, K,
                  p.G, cfg.block_n, cfg.stages, cfg.splits, cluster ? " (cluster)" : (pair ? " (pairs sharing B)" : ""),
                  cfg.grid, cfg.tiles);
   }
   cudaError_t e;
+  if (gated) {
+    e = block_scaled ? dg::launch_bs_gated(a, static_cast<dg::Mode>(mode)) : dg::launch_gated(a, static_cast<dg::Mode>(mode));
+    if (e != cudaSuccess) return fail_cuda(e, "kernel launch");
+    return DG_OK;
+  }
   if (swiglu) {
     e = block_scaled ? dg::launch_bs_swiglu(a) : dg::launch_masked_swiglu(a, quant_h);
     if (e != cudaSuccess) return fail_cuda(e, "kernel launch");
@@ -712,6 +763,114 @@ dg_status run_k_grouped(bool out_f32, const uint8_t* A, const void* sA, const ui
   const cudaError_t e = block_scaled ? dg::launch_bs_kgrouped(a) : dg::launch_kgrouped(a);
   if (e != cudaSuccess) return fail_cuda(e, "kernel launch");
   return DG_OK;
+}
+
+// The gated projection's entry points: dense (idx null) and contiguous.
+dg_status run_gated(int mode, bool out_f32, const uint8_t* A, const void* sA, const uint8_t* B, const void* sB,
+                    const int32_t* idx, void* H, uint16_t* GU, const uint64_t* rng, double p, int rows, int N, int K, int G,
+                    dg_stream_t stream, bool block_scaled) {
+  t_last_error.clear();
+  GatedArgs g{GU, {}};
+  const dg_status s = make_dropout(rng, p, &g.drop);
+  if (s != DG_OK) return s;
+  return run_gemm(mode, out_f32, A, sA, B, sB, idx, H, rows, N, K, G, static_cast<cudaStream_t>(stream), block_scaled,
+                  nullptr, false, false, false, false, false, nullptr, &g);
+}
+
+// What every elementwise launch needs; also brings up the device.
+dg_status stream_args(dg_stream_t stream, dg::StreamArgs* out) {
+  DeviceState* st = nullptr;
+  const dg_status s = device_state(&st);
+  if (s != DG_OK) return s;
+  out->stream = static_cast<cudaStream_t>(stream);
+  out->sms = effective_sms(*st);
+  out->pdl = pdl_setting();
+  return DG_OK;
+}
+
+dg_status run_dropout(const void* X, const void* R, void* Y, bool f32, const uint64_t* rng, double p, long long n,
+                      dg_stream_t stream) {
+  t_last_error.clear();
+  if (n < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  dg::Dropout d;
+  dg_status s = make_dropout(rng, p, &d);
+  if (s != DG_OK) return s;
+  if (n == 0) return DG_OK;
+  if (!X || !Y) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  const uintptr_t size = f32 ? 4 : 2;
+  if (!aligned(X, size) || !aligned(R, size) || !aligned(Y, size))
+    return fail(DG_ERR_ALIGNMENT, "X, R and Y must be aligned to their element");
+  const uintptr_t bytes = (uintptr_t)n * size, y = reinterpret_cast<uintptr_t>(Y);
+  for (const void* in : {X, R}) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(in);
+    if (in && x != y && x < y + bytes && y < x + bytes)
+      return fail(DG_ERR_INVALID_ARG, "Y overlaps an input without being the same tensor");
+  }
+  dg::StreamArgs sa;
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const cudaError_t e = dg::launch_dropout(X, R, Y, f32, d, n, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "dropout launch");
+}
+
+// One form's pointers: codes with scales, or neither.
+dg_status check_form(const char* what, const void* q, const void* s, const void* s2 = nullptr) {
+  if (q && !s && !s2) return fail(DG_ERR_INVALID_ARG, std::string(what) + ": codes without scales");
+  if (!q && (s || s2)) return fail(DG_ERR_INVALID_ARG, std::string(what) + ": scales without codes");
+  if (!aligned(q, 16)) return fail(DG_ERR_ALIGNMENT, std::string(what) + ": codes must be 16-byte aligned");
+  if (!aligned(s, 4) || !aligned(s2, 4)) return fail(DG_ERR_ALIGNMENT, std::string(what) + ": scales must be 4-byte aligned");
+  return DG_OK;
+}
+
+dg_status run_cast(const uint16_t* X, const int32_t* m_indices, uint8_t* Xr, void* sR, uint8_t* Xc, void* sC, uint8_t* Xb,
+                   void* sB, void* sBt, int G, int M, int N, dg_stream_t stream, bool ue8m0) {
+  t_last_error.clear();
+  if (G < 0 || M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  if (G == 0 || M == 0 || N == 0) return DG_OK;
+  if (!X) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  dg_status s;
+  if ((s = check_form("rows", Xr, sR)) != DG_OK || (s = check_form("columns", Xc, sC)) != DG_OK ||
+      (s = check_form("blocks", Xb, sB, sBt)) != DG_OK)
+    return s;
+  if (!Xr && !Xc && !Xb) return fail(DG_ERR_INVALID_ARG, "no form asked for");
+  if (m_indices && G != 1) return fail(DG_ERR_INVALID_ARG, "m_indices goes with one matrix (G = 1)");
+  if (N % 16 != 0) return fail(DG_ERR_ALIGNMENT, "N must be a multiple of 16 (16-byte rows of codes)");
+  if (!aligned(X, 16)) return fail(DG_ERR_ALIGNMENT, "X must be 16-byte aligned");
+  if (!aligned(m_indices, 4)) return fail(DG_ERR_ALIGNMENT, "m_indices must be 4-byte aligned");
+  if (M > INT_MAX - 256 || N > INT_MAX - 256 ||
+      (double)G * (((long long)M + 127) / 128) * (((long long)N + 127) / 128) > (double)INT_MAX)
+    return fail(DG_ERR_UNSUPPORTED, "too many 128x128 tiles");
+  dg::StreamArgs sa;
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const dg::CastForms f{Xr, Xc, Xb, sR, sC, sB, sBt};
+  const cudaError_t e = dg::launch_cast(X, m_indices, f, G, M, N, ue8m0, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "cast launch");
+}
+
+dg_status run_swiglu_backward(const uint16_t* dH, const uint16_t* GU, const int32_t* m_indices, const uint64_t* rng, double p,
+                              uint8_t* dGUr, void* sR, uint8_t* dGUc, void* sC, uint8_t* Hb, void* sHb, int M, int I,
+                              dg_stream_t stream, bool ue8m0) {
+  t_last_error.clear();
+  if (M < 0 || I < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  dg::Dropout d;
+  dg_status s = make_dropout(rng, p, &d);
+  if (s != DG_OK) return s;
+  if (I % 128 != 0) return fail(DG_ERR_ALIGNMENT, "I must be a multiple of 128");
+  if (M == 0 || I == 0) return DG_OK;
+  if (!dH || !GU) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  if ((s = check_form("rows", dGUr, sR)) != DG_OK || (s = check_form("columns", dGUc, sC)) != DG_OK ||
+      (s = check_form("blocks of H", Hb, sHb)) != DG_OK)
+    return s;
+  if (!dGUr && !dGUc) return fail(DG_ERR_INVALID_ARG, "no form of the gradients asked for");
+  if (!aligned(dH, 16) || !aligned(GU, 16)) return fail(DG_ERR_ALIGNMENT, "dH and GU must be 16-byte aligned");
+  if (!aligned(m_indices, 4)) return fail(DG_ERR_ALIGNMENT, "m_indices must be 4-byte aligned");
+  if (M > INT_MAX - 256 || I > INT_MAX / 2 - 256 || ((long long)M + 127) / 128 * (I / 128) > INT_MAX)
+    return fail(DG_ERR_UNSUPPORTED, "too many 128x128 tiles");
+  dg::StreamArgs sa;
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const dg::CastForms gu{dGUr, dGUc, nullptr, sR, sC, nullptr, nullptr};
+  const dg::CastForms h{nullptr, nullptr, Hb, nullptr, nullptr, nullptr, sHb};
+  const cudaError_t e = dg::launch_swiglu_backward(dH, GU, m_indices, d, gu, h, M, I, ue8m0, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "SwiGLU backward launch");
 }
 
 }  // namespace
@@ -974,6 +1133,130 @@ dg_status dg_fp8_gemm_nt_ue8m0_acc_f32(const uint8_t* A, const int32_t* sA, cons
                                        const float* C, float* D, int M, int N, int K, dg_stream_t stream) {
   return run_gemm(dg::kDense, true, A, sA, B, sB, nullptr, D, M, N, K, 1, static_cast<cudaStream_t>(stream), true,
                   C, true);
+}
+
+dg_status dg_fp8_gemm_nt_swiglu(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, uint16_t* H,
+                                uint16_t* GU,
+                                const uint64_t* rng, double p, int M, int N, int K, dg_stream_t stream) {
+  return run_gated(dg::kDense, false, A, sA, B, sB, nullptr, H, GU, rng, p, M, N, K, 1, stream, false);
+}
+
+dg_status dg_fp8_gemm_nt_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB, float* H,
+                                    uint16_t* GU,
+                                    const uint64_t* rng, double p, int M, int N, int K, dg_stream_t stream) {
+  return run_gated(dg::kDense, true, A, sA, B, sB, nullptr, H, GU, rng, p, M, N, K, 1, stream, false);
+}
+
+dg_status dg_fp8_gemm_nt_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                      uint16_t* H, uint16_t* GU,
+                                      const uint64_t* rng, double p, int M, int N, int K, dg_stream_t stream) {
+  return run_gated(dg::kDense, false, A, sA, B, sB, nullptr, H, GU, rng, p, M, N, K, 1, stream, true);
+}
+
+dg_status dg_fp8_gemm_nt_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                          float* H, uint16_t* GU,
+                                          const uint64_t* rng, double p, int M, int N, int K, dg_stream_t stream) {
+  return run_gated(dg::kDense, true, A, sA, B, sB, nullptr, H, GU, rng, p, M, N, K, 1, stream, true);
+}
+
+dg_status dg_fp8_grouped_contiguous_swiglu(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                           const int32_t* m_indices, uint16_t* H, uint16_t* GU, const uint64_t* rng,
+                                           double p, int M_total, int N, int K, int G,
+                                           dg_stream_t stream) {
+  return run_gated(dg::kContiguous, false, A, sA, B, sB, m_indices, H, GU, rng, p, M_total, N, K, G, stream,
+                   false);
+}
+
+dg_status dg_fp8_grouped_contiguous_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                               const int32_t* m_indices, float* H, uint16_t* GU, const uint64_t* rng,
+                                               double p, int M_total, int N, int K, int G,
+                                               dg_stream_t stream) {
+  return run_gated(dg::kContiguous, true, A, sA, B, sB, m_indices, H, GU, rng, p, M_total, N, K, G, stream,
+                   false);
+}
+
+dg_status dg_fp8_grouped_contiguous_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                 const int32_t* sB,
+                                                 const int32_t* m_indices, uint16_t* H, uint16_t* GU,
+                                                 const uint64_t* rng, double p, int M_total, int N, int K, int G,
+                                                 dg_stream_t stream) {
+  return run_gated(dg::kContiguous, false, A, sA, B, sB, m_indices, H, GU, rng, p, M_total, N, K, G, stream,
+                   true);
+}
+
+dg_status dg_fp8_grouped_contiguous_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                     const int32_t* sB,
+                                                     const int32_t* m_indices, float* H, uint16_t* GU,
+                                                     const uint64_t* rng, double p, int M_total, int N, int K, int G,
+                                                     dg_stream_t stream) {
+  return run_gated(dg::kContiguous, true, A, sA, B, sB, m_indices, H, GU, rng, p, M_total, N, K, G, stream,
+                   true);
+}
+
+dg_status dg_fp8_grouped_contiguous_nn(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                       const int32_t* m_indices, uint16_t* D, int M_total, int N, int K, int G,
+                                       dg_stream_t stream) {
+  return run_gemm(dg::kContiguous, false, A, sA, B, sB, m_indices, D, M_total, N, K, G, static_cast<cudaStream_t>(stream),
+                                       false, nullptr, false, false, false, true);
+}
+
+dg_status dg_fp8_grouped_contiguous_nn_f32(const uint8_t* A, const float* sA, const uint8_t* B, const float* sB,
+                                           const int32_t* m_indices, float* D, int M_total, int N, int K, int G,
+                                           dg_stream_t stream) {
+  return run_gemm(dg::kContiguous, true, A, sA, B, sB, m_indices, D, M_total, N, K, G, static_cast<cudaStream_t>(stream),
+                                           false, nullptr, false, false, false, true);
+}
+
+dg_status dg_fp8_grouped_contiguous_nn_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* B, const int32_t* sB,
+                                             const int32_t* m_indices, uint16_t* D, int M_total, int N, int K, int G,
+                                             dg_stream_t stream) {
+  return run_gemm(dg::kContiguous, false, A, sA, B, sB, m_indices, D, M_total, N, K, G, static_cast<cudaStream_t>(stream),
+                                             true, nullptr, false, false, false, true);
+}
+
+dg_status dg_fp8_grouped_contiguous_nn_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* B,
+                                                 const int32_t* sB,
+                                                 const int32_t* m_indices, float* D, int M_total, int N, int K, int G,
+                                                 dg_stream_t stream) {
+  return run_gemm(dg::kContiguous, true, A, sA, B, sB, m_indices, D, M_total, N, K, G, static_cast<cudaStream_t>(stream),
+                                                 true, nullptr, false, false, false, true);
+}
+
+dg_status dg_swiglu_backward_fp8(const uint16_t* dH, const uint16_t* GU, const int32_t* m_indices,
+                                 const uint64_t* rng,
+                                 double p, uint8_t* dGUr, float* sR, uint8_t* dGUc, float* sC, uint8_t* Hb, float* sHb, int M, int I,
+                                 dg_stream_t stream) {
+  return run_swiglu_backward(dH, GU, m_indices, rng, p, dGUr, sR, dGUc, sC, Hb, sHb, M, I, stream, false);
+}
+
+dg_status dg_cast_fp8(const uint16_t* X, const int32_t* m_indices, uint8_t* Xr, float* sR, uint8_t* Xc, float* sC,
+                      uint8_t* Xb,
+                      float* sB, float* sBt, int G, int M, int N, dg_stream_t stream) {
+  return run_cast(X, m_indices, Xr, sR, Xc, sC, Xb, sB, sBt, G, M, N, stream, false);
+}
+
+dg_status dg_swiglu_backward_fp8_ue8m0(const uint16_t* dH, const uint16_t* GU, const int32_t* m_indices,
+                                       const uint64_t* rng,
+                                       double p, uint8_t* dGUr, int32_t* sR, uint8_t* dGUc, int32_t* sC, uint8_t* Hb, int32_t* sHb, int M, int I,
+                                       dg_stream_t stream) {
+  return run_swiglu_backward(dH, GU, m_indices, rng, p, dGUr, sR, dGUc, sC, Hb, sHb, M, I, stream, true);
+}
+
+dg_status dg_cast_fp8_ue8m0(const uint16_t* X, const int32_t* m_indices, uint8_t* Xr, int32_t* sR, uint8_t* Xc,
+                            int32_t* sC, uint8_t* Xb,
+                            int32_t* sB, int32_t* sBt, int G, int M, int N, dg_stream_t stream) {
+  return run_cast(X, m_indices, Xr, sR, Xc, sC, Xb, sB, sBt, G, M, N, stream, true);
+}
+
+dg_status dg_dropout_bf16(const uint16_t* X, const uint16_t* R, uint16_t* Y, const uint64_t* rng, double p,
+                          long long n,
+                          dg_stream_t stream) {
+  return run_dropout(X, R, Y, false, rng, p, n, stream);
+}
+
+dg_status dg_dropout_f32(const float* X, const float* R, float* Y, const uint64_t* rng, double p, long long n,
+                         dg_stream_t stream) {
+  return run_dropout(X, R, Y, true, rng, p, n, stream);
 }
 
 int dg_get_tma_aligned_size(int x, int elem_bytes) {

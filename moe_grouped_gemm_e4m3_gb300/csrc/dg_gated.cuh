@@ -1,0 +1,165 @@
+// dg_gated.cuh — the epilogue of the gated projection H = dropout(silu(X·Wgᵀ) · (X·Wuᵀ)) in the dense
+// and contiguous forms, shared by the FP32-scale and the block-scaled kernel.
+//
+// A tile covers 128 columns of H: 128 gate rows and the 128 up rows of the weights. Each epilogue warp
+// holds, for its 32 rows, 64 gate columns (acc[0..63]) and the same 64 up columns (acc[64..127]), so
+// silu(g)·u needs no exchange between warps. On request it also stores the pre-activations, rounded to
+// BF16, at columns [j] (gate) and [I + j] (up) of GU, for the backward pass. H is formed from the FP32
+// values. Whole 32-row slabs leave through TMA (64-byte boxes, two staging buffers a warp);
+// slabs with rows that must stay untouched use predicated 16-byte stores.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "dg_philox.cuh"
+#include "dg_ptx.cuh"
+#include "dg_vec.cuh"
+
+namespace dg {
+
+// What the gated kernels take beside GemmParams.
+struct GatedExt {
+  CUtensorMap tmGU;   // GU, BF16 [rows, 2I]: boxes of 32 rows x 32 columns (valid, unused where gu is null)
+  uint16_t* gu;       // the saved pre-activations, or null
+  Dropout drop;
+};
+struct NoExt {};
+
+// silu(x) = x / (1 + e^-x), the gate function of SwiGLU, with the fast exponential and division
+// (relative error ~1e-6). For x below about -87 the denominator overflows and the quotient is -0, the
+// function's limit. (An IEEE-rounded division or reciprocal there takes a slow special-case path:
+// it made the fused kernel 50% slower than the GEMM alone on decode-sized outputs.)
+__device__ __forceinline__ float silu_f32(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
+
+// Eight columns of one row, from the summed pre-activations: h and (on request) g and u to memory.
+// The path of the rows that a cluster split reduces.
+template <bool OUT_F32>
+__device__ __forceinline__ void gated_store8(const GatedExt& e, void* H, int I, size_t row, int col, const float (&g)[8],
+                                             const float (&u)[8]) {
+  if (e.gu) {
+    store8(reinterpret_cast<__nv_bfloat16*>(e.gu) + row * 2 * I + col, g);
+    store8(reinterpret_cast<__nv_bfloat16*>(e.gu) + row * 2 * I + I + col, u);
+  }
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = silu_f32(g[j]) * u[j];
+  if (e.drop.threshold) dropout8(h, Philox(e.drop.rng)((row * I + col) / 8), e.drop.threshold, e.drop.scale);
+  if constexpr (OUT_F32)
+    store8(static_cast<float*>(H) + row * I + col, h);
+  else
+    store8(static_cast<__nv_bfloat16*>(H) + row * I + col, h);
+}
+
+// One 32-row x 64-byte box (32 BF16 or 16 FP32 columns, v[0..]) through the warp's staging buffers.
+template <bool F32>
+__device__ __forceinline__ void gated_box(const CUtensorMap* tm, uint8_t* staging, uint32_t box_bytes, uint32_t& count,
+                                          const float* v, int col, int row, int lane) {
+  const uint32_t sel = count & 1;
+  if (count >= 2) {
+    if (lane == 0) tma_store_wait_read_1();   // the box that used this buffer has been read
+    __syncwarp();
+  }
+  uint8_t* buf = staging + sel * box_bytes;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {   // four 16-byte pieces per 64-byte row, 64-byte swizzle
+    const uint32_t phys = (uint32_t)(j ^ ((lane >> 1) & 3));
+    uint4 w;
+    if constexpr (F32)
+      w = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                     __float_as_uint(v[4 * j + 3]));
+    else
+      w = make_uint4(round_bf16x2(v[8 * j], v[8 * j + 1]), round_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                     round_bf16x2(v[8 * j + 4], v[8 * j + 5]), round_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    *reinterpret_cast<uint4*>(buf + lane * 64 + phys * 16) = w;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(tm, buf, col, row);
+    tma_store_commit();
+  }
+  ++count;
+  __syncwarp();
+}
+
+// The epilogue of one warp's 32 rows x 64 columns of H. row0: its first row of H; write_row: whether this
+// lane's row is stored; all_rows: whether TMA may store the slab (rows past the matrix are clipped there).
+template <bool OUT_F32>
+__device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensorMap* tmH, void* H, int I, float* acc,
+                                               int row0, int col0, bool write_row, bool all_rows, uint8_t* staging,
+                                               uint32_t box_bytes, uint32_t& count, int lane) {
+  const size_t row = (size_t)row0 + lane;
+  if (e.gu) {
+    if (all_rows) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 32 * b, (b >> 1) * I + col0 + (b & 1) * 32, row0, lane);
+    } else if (write_row) {
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(e.gu) + row * 2 * I + col0;
+#pragma unroll
+      for (int j = 0; j < 128; j += 8) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = acc[j + k];
+        store8(dst + (j >= 64 ? I - 64 : 0) + j, v);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 64; ++j) acc[j] = silu_f32(acc[j]) * acc[64 + j];
+  if (e.drop.threshold) {
+    const Philox gen(e.drop.rng);
+    const uint64_t index = (row * I + col0) / 8;
+#pragma unroll
+    for (int j = 0; j < 64; j += 8) dropout8(*reinterpret_cast<float(*)[8]>(acc + j), gen(index + j / 8), e.drop.threshold, e.drop.scale);
+  }
+  if (all_rows) {
+    constexpr int kCols = OUT_F32 ? 16 : 32;
+#pragma unroll
+    for (int b = 0; b < 64 / kCols; ++b)
+      gated_box<OUT_F32>(tmH, staging, box_bytes, count, acc + kCols * b, col0 + kCols * b, row0, lane);
+  } else if (write_row) {
+#pragma unroll
+    for (int j = 0; j < 64; j += 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = acc[j + k];
+      if constexpr (OUT_F32)
+        store8(static_cast<float*>(H) + row * I + col0 + j, v);
+      else
+        store8(static_cast<__nv_bfloat16*>(H) + row * I + col0 + j, v);
+    }
+  }
+}
+
+// Cluster split-K: sums the rows r = rank (mod S) of the S partial tiles of a cluster in range order and
+// stores them. `part`: this CTA's partial tile in shared memory, rows of `row_bytes`, tile columns as
+// the epilogue warps hold them: [64 gate | 64 up] for columns 0..63 of H, then for 64..127.
+// m_indices: the contiguous form's rows (null: dense); g: the tile's group.
+template <bool OUT_F32>
+__device__ __forceinline__ void gated_cluster_reduce(const GatedExt& e, void* H, int I, uint32_t part, uint32_t row_bytes,
+                                                     int S, int rank, int threads, int a_row, int rows, int n_blk, int g,
+                                                     const int32_t* m_indices, int* status, int bad_group_bit) {
+  const int c = (threadIdx.x % 16) * 8;                          // first of eight columns of H in the tile
+  const uint32_t off = (uint32_t)((c / 64) * 128 + c % 64) * 4;  // their gate partials; up 64 columns on
+  for (int r = rank + (int)(threadIdx.x / 16) * S; r < rows; r += threads / 16 * S) {
+    const uint32_t at = part + r * row_bytes + off;
+    const float4 g0 = cluster_sum_v4(at, S), g1 = cluster_sum_v4(at + 16, S);
+    const float4 u0 = cluster_sum_v4(at + 256, S), u1 = cluster_sum_v4(at + 272, S);
+    if (m_indices) {
+      const int idx = __ldg(m_indices + a_row + r);
+      if (idx != g) {
+        if (idx != -1 && c == 0) atomicOr(status, bad_group_bit);
+        continue;   // a padding row (or another group's): left untouched
+      }
+    }
+    const float gs[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+    const float us[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+    gated_store8<OUT_F32>(e, H, I, (size_t)a_row + r, n_blk * 128 + c, gs, us);
+  }
+}
+
+}  // namespace dg

@@ -4,6 +4,6 @@
 
 namespace dg {
 cudaError_t launch_bs_swiglu(const LaunchArgs& a) {
-  return a.out_f32 ? launch_bs_instance<kMasked, true, true>(a) : launch_bs_instance<kMasked, false, true>(a);
+  return a.out_f32 ? launch_bs_instance<kMasked, true, kSwiglu>(a) : launch_bs_instance<kMasked, false, kSwiglu>(a);
 }
 }  // namespace dg

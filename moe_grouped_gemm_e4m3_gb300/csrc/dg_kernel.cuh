@@ -42,6 +42,7 @@
 
 #include <cstdint>
 
+#include "dg_gated.cuh"
 #include "dg_ptx.cuh"
 
 namespace dg {
@@ -104,8 +105,13 @@ constexpr int kFlagPairB = 0x10;
 // D then points to the codes [G·M_max, I] (bytes) and h_scales to the scales [G][I/128][ldsa]
 // (the MN-major LHS scale layout of the masked GEMM). A separate instantiation: holding a row's 128
 // H values until their amax is known raises the epilogue's register pressure.
+// kSwigluGated: the dense and contiguous forms (dg_gated.cuh): H, and on request the pre-activations,
+// with dropout; their extra arguments travel in GatedExt.
 constexpr int kSwiglu = 1;
 constexpr int kSwigluFp8 = 2;
+constexpr int kSwigluGated = 3;
+template <int SWIGLU>
+using KernelExt = std::conditional_t<SWIGLU == kSwigluGated, GatedExt, NoExt>;
 // Bits 8..31 of the flags word hold the time limit of the pipeline waits in microseconds
 // (kWaitLimitShift, mbar_wait).
 
@@ -397,12 +403,6 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t& a, uint32_
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
 }
 
-// silu(x) = x / (1 + e^-x), the gate function of SwiGLU, with the fast exponential and division
-// (relative error ~1e-6). For x below about -87 the denominator overflows and the quotient is -0, the
-// function's limit. (An IEEE-rounded division or reciprocal there takes a slow special-case path:
-// it made the fused kernel 50% slower than the GEMM alone on decode-sized outputs.)
-__device__ __forceinline__ float silu_f32(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
-
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -426,16 +426,22 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 // SWIGLU (masked form only, BN = 256): the tile's 256 B rows are 128 gate rows (block n of [0, I))
 // and the 128 up rows I + 128·n ..; the epilogue pairs the two halves and stores
 // H = silu(gate)·up, 128 columns of the [G·M_max, I] output per tile.
+//
+// kSwigluGated (dense and contiguous forms, BN = 256): the same 256 B rows, but ordered gate 0..63, up
+// 0..63, gate 64..127, up 64..127 in the tile (four 64-row boxes), so that each epilogue warp owns
+// matching gate and up columns and the two warps of a quadrant exchange nothing.
 
 template <int BN, int EPI_COLS, int STAGES, int NBUF, Mode MODE, bool OUT_F32, int SWIGLU>
 __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const __grid_constant__ CUtensorMap tmD, const GemmParams p) {
+                    const __grid_constant__ CUtensorMap tmD, const GemmParams p,
+                    const __grid_constant__ KernelExt<SWIGLU> ext) {
   using R = Roles<BN, EPI_COLS>;
   using Plan = SmemPlan<BN, STAGES, R::kEpiWarps, NBUF>;
   constexpr int kEpiWarps = R::kEpiWarps;
   // cluster split-K (kFlagClusterSplit) is compiled into the dense and contiguous forms only
-  constexpr bool kClusterCapable = (MODE == kDense || MODE == kContiguous) && !SWIGLU;
+  constexpr bool kGated = SWIGLU == kSwigluGated;
+  constexpr bool kClusterCapable = (MODE == kDense || MODE == kContiguous) && (!SWIGLU || kGated);
   constexpr int kChunks = EPI_COLS / 32;   // 32-column TMEM loads per epilogue thread and K-block
   constexpr uint32_t kTmemCols = NBUF * BN;
   static_assert(kTmemCols == 128 || kTmemCols == 256 || kTmemCols == 512, "TMEM allocation: power of two");
@@ -447,7 +453,9 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
   // issuers would share a stage, and one could wait for the use two phases ahead while the barrier
   // is still one phase behind: the parity test would pass early and the ring would lose step.
   static_assert(STAGES % 2 == 0 && NBUF % 2 == 0, "stage and TMEM-buffer counts must be even (two issuers)");
-  static_assert(!SWIGLU || (BN == 256 && EPI_COLS == 128 && MODE == kMasked), "fused SwiGLU: masked, BN = 256");
+  static_assert(!SWIGLU || (BN == 256 && EPI_COLS == 128), "fused SwiGLU: BN = 256");
+  static_assert(!SWIGLU || (kGated ? MODE == kDense || MODE == kContiguous : MODE == kMasked),
+                "fused SwiGLU: masked; gated: dense and contiguous");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -572,9 +580,19 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
               tma_load_2d(&tmA, sa, &full_bar[s], kb * 128, tile.a_row, policy);
             if (p.flags & kFlagBMN) {  // B stored [K, N]: BN/128 boxes of 128 K-rows x 128 N-bytes, 16 KB apart
 #pragma unroll
-              for (int h = 0; h < BN / 128; ++h)
-                tma_load_2d(&tmB, sa + Plan::kABytes + h * 128 * 128, &full_bar[s], b_row + h * 128, kb * 128,
-                            policy_b);
+              for (int h = 0; h < BN / 128; ++h) {
+                // contiguous: B [G, K, N] with K a multiple of 128, group g's rows at g·K
+                const int n = (MODE == kContiguous ? tile.n_blk * BN : b_row) + h * 128;
+                const int k = (MODE == kContiguous ? tile.g * p.K : 0) + kb * 128;
+                tma_load_2d(&tmB, sa + Plan::kABytes + h * 128 * 128, &full_bar[s], n, k, policy_b);
+              }
+            } else if constexpr (kGated) {
+              // (B's tensor map box is 64 rows)
+              const int gate_row = tile.g * p.N + tile.n_blk * 128;
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                tma_load_2d(&tmB, sa + Plan::kABytes + h * 64 * 128, &full_bar[s], kb * 128,
+                            gate_row + (h & 1) * p.swiglu_i + (h >> 1) * 64, policy_b);
             } else if constexpr (SWIGLU) {
               // gate rows 128·n .. and up rows I + 128·n .. (B's tensor map box is 128 rows)
               const int gate_row = tile.g * p.N + tile.n_blk * 128;
@@ -742,6 +760,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       __syncwarp();
       // The first column of this warp (as a row of B: fused SwiGLU puts the up rows at I + 128·n).
       auto first_col = [&](int n_blk) -> int {
+        if constexpr (kGated) return n_blk * 128;   // the gate's scale block; the up scales are I/128 blocks on
         return SWIGLU ? (cgrp ? p.swiglu_i : 0) + n_blk * 128 : n_blk * BN + cgrp * EPI_COLS;
       };
       // Only what the K loop needs is live across it; the rest of the tile is re-read afterwards.
@@ -769,12 +788,18 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         return (active && row_live && kb < kb_end) ? __ldg(sa_ptr + (size_t)kb * p.ldsa) : 0.0f;
       };
       auto fetch_sb = [&](int kb) -> float { return (active && kb < kb_end) ? __ldg(sb_ptr + kb) : 0.0f; };
+      auto fetch_su = [&](int kb) -> float {   // gated: the up columns' scale
+        return (active && kb < kb_end) ? __ldg(sb_ptr + (size_t)(p.swiglu_i / 128) * p.nkb + kb) : 0.0f;
+      };
       float sa_cur = fetch_sa(kb_begin), sb_cur = fetch_sb(kb_begin);
+      float su_cur = 0.0f, su_nxt = 0.0f;
+      if constexpr (kGated) su_cur = fetch_su(kb_begin);
 
       for (int kb = kb_begin; kb < kb_end; ++kb, ++acc_it) {
         const int b = acc_it % NBUF;
         const uint32_t aph = (acc_it / NBUF) & 1;
         const float sa_nxt = fetch_sa(kb + 1), sb_nxt = fetch_sb(kb + 1);
+        if constexpr (kGated) su_nxt = fetch_su(kb + 1);
         // All 32 lanes wait together: one warp-wide instruction stream, uniform by construction
         // (every lane sees the same barrier phase, timer value and abort flag).
         if (!mbar_wait(&tfull_bar[b], aph, abort_flag, p.status, p.flags)) { alive = false; break; }
@@ -801,6 +826,10 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
               const float scale = sa_cur * sb_cur;
               scale2 = make_float2(scale, scale);
             }
+            if (kGated && c == 2) {   // columns 64..127 of the warp are up columns
+              const float scale = sa_cur * su_cur;
+              scale2 = make_float2(scale, scale);
+            }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               acc2[c * 16 + j] = __ffma2_rn(make_float2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1])),
@@ -819,6 +848,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         }
         sa_cur = sa_nxt;
         sb_cur = sb_nxt;
+        if constexpr (kGated) su_cur = su_nxt;
       }
       if (!alive) break;
       if (kClusterCapable && (p.flags & kFlagClusterSplit)) {   // one unit per CTA: the reduction follows the loop
@@ -884,7 +914,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         }
       }
 
-      if constexpr (SWIGLU) {
+      if constexpr (SWIGLU && !kGated) {
         // Fused SwiGLU: warp cgrp 1 (up) hands its accumulators to warp cgrp 0 (gate) of the same
         // quadrant, 32 columns per round, through its own staging buffer; both warps hold the same
         // 32 rows. The hand-over is guarded by two mbarriers per quadrant (bounded waits). The gate
@@ -1031,6 +1061,11 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       const int d_row = tile.a_row + row_in_tile;   // row in D's 2-D view
       if (!__any_sync(0xffffffffu, write_row)) continue;   // no row of this warp is stored
       const bool use_tma = (MODE == kDense) || __all_sync(0xffffffffu, write_row);
+      if constexpr (kGated) {
+        gated_epilogue<OUT_F32>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32, tile.n_blk * 128 + cgrp * 64,
+                                write_row, use_tma, staging, Plan::kStagingBox, store_count, lane);
+        continue;
+      }
       if (!col_exists) continue;
       if (use_tma) {
         // 32-row x 64-byte boxes (32 BF16 or 16 FP32 columns) alternate between two staging
@@ -1133,6 +1168,10 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         constexpr int kRowsPerPass = R::kEpiThreads / kVec;   // 4 (BN=256) or 8 (BN=128)
         const int c4 = threadIdx.x % kVec;
         const int n = n_blk * BN + c4 * 4;
+        if constexpr (kGated) {
+          gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
+                                        g, MODE == kContiguous ? p.m_indices : nullptr, p.status, kStatusBadGroup);
+        } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {
           float4 tot = cluster_sum_v4(part + r * kRowBytes + c4 * 16, S);
           if (n >= p.N) continue;

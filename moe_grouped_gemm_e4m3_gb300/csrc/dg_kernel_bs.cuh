@@ -85,11 +85,13 @@ static_assert(kSfCol0 + BsSmemPlan::kSfSlots * kSfSlotCols <= kBsTmemCols, "scal
 // SWIGLU (masked form only): the tile's 256 B rows are 128 gate rows (block n of [0, I)) and the
 // matching 128 up rows (block n of [I, 2I)), and the epilogue stores H = silu(gate)·up, 128
 // columns of H per tile. The whole K loop accumulates in TMEM, so each epilogue warp loads both
-// its gate and its up columns itself: no hand-over between warps.
-template <Mode MODE, bool OUT_F32, bool SWIGLU = false>
+// its gate and its up columns itself: no hand-over between warps. kSwigluGated: the same tile in the
+// dense and contiguous forms, with the epilogue of dg_gated.cuh.
+template <Mode MODE, bool OUT_F32, int SWIGLU = 0>
 __global__ void __launch_bounds__(BsRoles::kThreads, 1)
     fp8_gemm_bs_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                       const __grid_constant__ CUtensorMap tmD, const GemmParams p) {
+                       const __grid_constant__ CUtensorMap tmD, const GemmParams p,
+                       const __grid_constant__ KernelExt<SWIGLU> ext) {
   using R = BsRoles;
   using Plan = BsSmemPlan;
   constexpr int BN = 256;
@@ -98,7 +100,9 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
   constexpr int SLOTS = Plan::kSfSlots;
   // cluster split-K (kFlagClusterSplit) is compiled into the dense and contiguous forms only
   constexpr bool kClusterCapable = MODE == kDense || MODE == kContiguous;
-  static_assert(!SWIGLU || MODE == kMasked, "fused SwiGLU: masked form only");
+  constexpr bool kGated = SWIGLU == kSwigluGated;
+  static_assert(!SWIGLU || (kGated ? MODE == kDense || MODE == kContiguous : MODE == kMasked),
+                "fused SwiGLU: masked; gated: dense and contiguous");
   constexpr uint32_t kIdesc = make_idesc_e4m3_bs(128, BN);
 
   extern __shared__ uint8_t smem_raw[];
@@ -208,8 +212,11 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, gate_row, policy);
               tma_load_2d(&tmB, sa + Plan::kABytes + 128 * 128, &full_bar[s], kb * 128, gate_row + p.swiglu_i, policy);
             } else if (p.flags & kFlagBMN) {  // B stored [K, N]: two boxes of 128 K-rows x 128 N-bytes, 16 KB apart
-              tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], b_row, kb * 128, policy);
-              tma_load_2d(&tmB, sa + Plan::kABytes + 128 * 128, &full_bar[s], b_row + 128, kb * 128, policy);
+              // (contiguous: B [G, K, N] with K a multiple of 128, group g's rows at g·K)
+              const int n = MODE == kContiguous ? tile.n_blk * BN : b_row;
+              const int k = (MODE == kContiguous ? tile.g * p.K : 0) + kb * 128;
+              tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], n, k, policy);
+              tma_load_2d(&tmB, sa + Plan::kABytes + 128 * 128, &full_bar[s], n + 128, k, policy);
             } else {
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, b_row, policy);
             }
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       const int m_local = tile.m_blk * 128 + row_in_tile;
       const bool row_exists = row_in_tile < tile.rows;
       const int n_col0 = tile.n_blk * BN + cgrp * EPI_COLS;
-      const bool col_exists = n_col0 < p.N;
+      const bool col_exists = SWIGLU || n_col0 < p.N;   // (fused SwiGLU: I is a multiple of 128)
 
       if (kClusterCapable && (p.flags & kFlagClusterSplit)) {
         // one unit per CTA: the partial goes to this CTA's stage buffers (idle once the MMA is
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
 
       // (fused SwiGLU: the split-K step above publishes and reduces each warp's 64 gate and 64 up
       // columns under its own 128 slots of the partial tile, so the last split holds both)
-      if constexpr (SWIGLU) {
+      if constexpr (SWIGLU && !kGated) {
         // H = silu(gate)·up for this warp's 64 of the tile's 128 columns of H (row stride I)
         if (!active || !__any_sync(0xffffffffu, row_exists)) continue;
 #pragma unroll
@@ -590,6 +597,11 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       const int d_row = tile.a_row + row_in_tile;
       if (!__any_sync(0xffffffffu, write_row)) continue;   // no row of this warp is stored
       const bool use_tma = (MODE == kDense) || __all_sync(0xffffffffu, write_row);
+      if constexpr (kGated) {
+        gated_epilogue<OUT_F32>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32, tile.n_blk * 128 + cgrp * 64,
+                                write_row, use_tma, staging, Plan::kStagingBox, store_count, lane);
+        continue;
+      }
       if (!col_exists) continue;
       if (use_tma) {
         constexpr int kColsPerBox = OUT_F32 ? 16 : 32;
@@ -679,6 +691,10 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         constexpr int kRowsPerPass = R::kEpiThreads / kVec;
         const int c4 = threadIdx.x % kVec;
         const int n = n_blk * BN + c4 * 4;
+        if constexpr (kGated) {
+          gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
+                                        g, MODE == kContiguous ? p.m_indices : nullptr, p.status, kStatusBadGroup);
+        } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {
           float4 tot = cluster_sum_v4(part + r * kRowBytes + c4 * 16, S);
           if (n >= p.N) continue;

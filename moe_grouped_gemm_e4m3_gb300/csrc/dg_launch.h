@@ -7,12 +7,14 @@
 
 #include "dg_kernel.cuh"
 #include "dg_kernel_bs.cuh"
+#include "dg_philox.cuh"
 
 namespace dg {
 
 struct LaunchArgs {
   CUtensorMap tmA, tmB, tmD;
   GemmParams p;
+  GatedExt gated;   // the gated forms only
   int block_n;   // 128 or 256
   bool out_f32;
   int grid;
@@ -39,6 +41,9 @@ cudaError_t launch_kgrouped(const LaunchArgs& a);
 // The masked form fused with SwiGLU (block_n 256, FP32-scale kernel); fp8_h: H as FP8 codes and
 // 1x128-group scales.
 cudaError_t launch_masked_swiglu(const LaunchArgs& a, bool fp8_h = false);
+// The gated projection (dense and contiguous forms, block_n 256), FP32 scales and block-scaled.
+cudaError_t launch_gated(const LaunchArgs& a, Mode mode);
+cudaError_t launch_bs_gated(const LaunchArgs& a, Mode mode);
 // The block-scaled kernel for packed UE8M0 scales (block_n is always 256).
 cudaError_t launch_bs(const LaunchArgs& a, Mode mode);
 // The block-scaled masked form fused with SwiGLU.
@@ -53,6 +58,29 @@ cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int 
                              cudaStream_t stream);
 // A's scales row-major [G][M][nkb] -> MN-major [G][nkb][ldsa] (rows m >= M zero).
 cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, cudaStream_t stream);
+// What the elementwise kernels' launches need: the stream, the SMs they may fill, and whether they may
+// start before the previous kernel of the stream ends (dg_set_pdl).
+struct StreamArgs {
+  cudaStream_t stream;
+  int sms;
+  bool pdl;
+};
+// Y = R + dropout(X) over n elements, BF16 or FP32; r may be null (dg_dropout.cu).
+cudaError_t launch_dropout(const void* x, const void* r, void* y, bool f32, const Dropout& d, long long n,
+                           const StreamArgs& s);
+// The E4M3 forms of a matrix (dg_cast.cu): each with its codes and scales, or null codes.
+struct CastForms {
+  uint8_t *q_row, *q_col, *q_blk;
+  void *s_row, *s_col;       // FP32 scales or packed UE8M0 words
+  void *s_blk, *s_blk_t;     // of the 128x128 blocks: [Mb][Nb] and [Nb][Mb]; either may be null
+};
+cudaError_t launch_cast(const uint16_t* x, const int32_t* m_indices, const CastForms& f, int G, int M, int N,
+                        bool ue8m0, const StreamArgs& s);
+// The backward pass of the gated activation, cast to E4M3: gu is [M, 2I]; rows/cols: forms of [dG dU]
+// (no blocks), h: the blocks of H (or null codes).
+cudaError_t launch_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices,
+                                   const Dropout& d, const CastForms& dgu, const CastForms& h, int M, int I,
+                                   bool ue8m0, const StreamArgs& s);
 // How many clusters of `cluster` CTAs of the dense / contiguous instantiation for (block_n,
 // out_f32) can be resident at once (0 if the query fails).
 int cluster_capacity_dense(int block_n, bool out_f32, int cluster);
@@ -60,11 +88,29 @@ int cluster_capacity_contiguous(int block_n, bool out_f32, int cluster);
 // The same for the block-scaled kernel (dense or contiguous).
 int cluster_capacity_bs(Mode mode, bool out_f32, int cluster);
 
+// Launches an elementwise kernel on a 1-D grid.
+template <typename... Params, typename... Args>
+cudaError_t launch_plain(void (*kernel)(Params...), int grid, int threads, size_t smem_bytes, const StreamArgs& s,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes;
+  cfg.stream = s.stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = s.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Launches `kernel` on a 1-D grid of `grid` CTAs: as clusters of `cluster` CTAs when cluster > 1,
 // and with programmatic stream serialization when pdl is set (the kernels wait for the previous
 // kernel's results with griddepcontrol.wait before their first global read).
-template <typename Kernel>
-cudaError_t launch_kernel(Kernel kernel, const LaunchArgs& a, int threads, size_t smem_bytes) {
+template <typename Ext>
+cudaError_t launch_kernel(void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, GemmParams, Ext), const LaunchArgs& a,
+                          int threads, size_t smem_bytes) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.grid, 1, 1);
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
@@ -86,7 +132,10 @@ cudaError_t launch_kernel(Kernel kernel, const LaunchArgs& a, int threads, size_
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kernel, a.tmA, a.tmB, a.tmD, a.p);
+  if constexpr (std::is_same_v<Ext, GatedExt>)
+    return cudaLaunchKernelEx(&cfg, kernel, a.tmA, a.tmB, a.tmD, a.p, a.gated);
+  else
+    return cudaLaunchKernelEx(&cfg, kernel, a.tmA, a.tmB, a.tmD, a.p, Ext{});
 }
 
 // Resident clusters of `cluster` CTAs of `kernel` (an occupancy query; nothing runs; 0 on error).
@@ -145,7 +194,7 @@ int cluster_capacity_instance(int cluster) {
   constexpr int NBUF = tmem_bufs_for(BN);
   using R = Roles<BN, EPI_COLS>;
   using Plan = SmemPlan<BN, STAGES, R::kEpiWarps, NBUF>;
-  return clusters_resident(fp8_gemm_kernel<BN, EPI_COLS, STAGES, NBUF, MODE, OUT_F32, false>, R::kThreads,
+  return clusters_resident(fp8_gemm_kernel<BN, EPI_COLS, STAGES, NBUF, MODE, OUT_F32, 0>, R::kThreads,
                            Plan::kDynamicBytes, cluster);
 }
 
@@ -156,7 +205,7 @@ int cluster_capacity_mode(int block_n, bool out_f32, int cluster) {
   return out_f32 ? cluster_capacity_instance<128, MODE, true>(cluster) : cluster_capacity_instance<128, MODE, false>(cluster);
 }
 
-template <Mode MODE, bool OUT_F32, bool SWIGLU = false>
+template <Mode MODE, bool OUT_F32, int SWIGLU = 0>
 cudaError_t launch_bs_instance(const LaunchArgs& a) {
   auto kernel = fp8_gemm_bs_kernel<MODE, OUT_F32, SWIGLU>;
   static bool configured[64] = {};
