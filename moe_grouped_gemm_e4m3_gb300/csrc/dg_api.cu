@@ -506,6 +506,11 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   dg_status s = device_state(&st);
   if (s != DG_OK) return s;
   const int sms = effective_sms(*st);
+  if (gated && mode == dg::kDense && rows <= dg::kFewTokens) {   // the weights' read is the whole cost
+    const cudaError_t e = dg::launch_gated_few(A, sA, B, sB, D, gated->GU, gated->drop, rows, N / 2, K, out_f32, block_scaled,
+                                               dg::StreamArgs{stream, sms, pdl_setting()});
+    return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
+  }
   Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
   // (the gated kernels have the footprint of the plain BN = 256 ones: the same cluster capacities)
   if (!swiglu) fit_cluster_splits(cfg, mode, K, block_scaled, out_f32);
@@ -659,7 +664,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   }
   cudaError_t e;
   if (gated) {
-    e = block_scaled ? dg::launch_bs_gated(a, static_cast<dg::Mode>(mode)) : dg::launch_gated(a, static_cast<dg::Mode>(mode));
+    e = block_scaled ? dg::launch_bs_gated(a) : dg::launch_gated(a);
     if (e != cudaSuccess) return fail_cuda(e, "kernel launch");
     return DG_OK;
   }

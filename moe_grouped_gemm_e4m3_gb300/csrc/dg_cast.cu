@@ -16,7 +16,7 @@
 // (2^-100 keeps 448/a finite.) A NaN becomes the NaN code. A group with an infinity dequantises to
 // NaN: its scale is infinite, or UE8M0's NaN.
 //
-// One CTA takes one 128x128 tile, which holds whole groups of every form: the input is read once
+// One CTA takes a 128x128 tile at a time, which holds whole groups of every form: the input is read once
 // into registers, and the maxima along rows (shuffles within 16 lanes), columns and the block (shared
 // memory) come from there. Bound by HBM: 2 bytes read and 1 byte written per form and element.
 #include <cuda_bf16.h>
@@ -79,232 +79,392 @@ __device__ __forceinline__ uint32_t codes4(const float* v, float f0, float f1, f
          (e4m3x2_satfinite(__fmul_rn(v[2], f2), __fmul_rn(v[3], f3)) << 16);
 }
 
-template <int THREADS>
-struct TileShared {
-  float part[THREADS / 32][128];   // each warp's column maxima
+__device__ __forceinline__ void put_codes8(uint8_t* p, const float (&v)[8], const float (&f)[8]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, f[0], f[1], f[2], f[3]), codes4(v + 4, f[4], f[5], f[6], f[7]));
+}
+
+__device__ __forceinline__ void put_codes8(uint8_t* p, const float (&v)[8], float f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, f, f, f, f), codes4(v + 4, f, f, f, f));
+}
+
+// The maxima of eight lines over 16 lanes, lane c of them getting line c % 8: at each of three steps a lane
+// passes on the half of its lines that its partner keeps (8 shuffles; reducing line by line takes 32).
+__device__ __forceinline__ float max8_over_16(const float (&v)[8], int c) {
+  float a[4], b[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float keep = c & 1 ? v[2 * k + 1] : v[2 * k], pass = c & 1 ? v[2 * k] : v[2 * k + 1];
+    a[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 1));
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float keep = c & 2 ? a[2 * k + 1] : a[2 * k], pass = c & 2 ? a[2 * k] : a[2 * k + 1];
+    b[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 2));
+  }
+  const float keep = c & 4 ? b[1] : b[0], pass = c & 4 ? b[0] : b[1];
+  const float m = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 4));
+  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+}
+
+// Asynchronous copy of 16 bytes to this thread's own place in shared memory (zeros if !live). No other thread
+// reads it, so wait_copies is all the synchronisation it needs.
+__device__ __forceinline__ void copy_16(uint4* to, const void* from, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// ---------------------------------------------------------------------------------------------
+// The cast of a BF16 matrix. Thread t holds columns 8·(t % 16).. of the tile's rows i·16 + t/16, i < 8. A
+// persistent CTA copies its next tile into shared memory while it works on this one.
+constexpr int kCastThreads = 256, kCastRows = 8, kCastStep = 16, kCastCtas = 3;
+
+struct CastShared {
+  uint4 next[2][kCastRows][kCastThreads];
+  float part[kCastThreads / 32][128];   // each warp's column maxima
   float factor[128];
   float top[4];
 };
 
-// One tile's place: group g of matrices [M, N] (N is the stored width), tile row mb, tile column nb.
-struct TilePlace {
-  int g, mb, nb, M, N;
-};
-
-// Casts one 128x128 tile into the asked forms. Thread t holds, for i < ROWS, the eight columns
-// 8·(t % 16).. of tile row i·(THREADS/16) + t/16, given by value(i, float (&)[8]): zeros where the matrix
-// has no such row or column.
-template <bool UE, int THREADS, typename Value>
-__device__ __forceinline__ void cast_tile(TileShared<THREADS>& sh, const CastForms& f, const TilePlace& at,
-                                          const Value& value) {
-  constexpr int kRows = 128 * 16 / THREADS, kStep = THREADS / 16;
-  const int t = threadIdx.x, cg = t % 16, warp = t / 32, lane = t % 32;
-  const int row0 = at.mb * 128 + t / 16, col = at.nb * 128 + cg * 8;
-  const int Mb = (at.M + 127) / 128, Nb = (at.N + 127) / 128;
-  const bool col_live = col < at.N;
-  const size_t line0 = (size_t)at.g * at.M;
-
-  if (f.q_row) {
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      float v[8];
-      value(i, v);
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float fac;
-      uint32_t scale;
-      group_scale<UE>(m, fac, scale);
-      if (cg == i) mine = scale;
-      const int row = row0 + i * kStep;
-      if (row < at.M && col_live)
-        *reinterpret_cast<uint2*>(f.q_row + (line0 + row) * at.N + col) =
-            make_uint2(codes4(v, fac, fac, fac, fac), codes4(v + 4, fac, fac, fac, fac));
-    }
-    // lane cg = i of a row's 16 puts the scale of row i; the rows past M up to align4(M) get the filler
-    const int ldm = (at.M + 3) / 4 * 4, row = row0 + cg * kStep;
-    if (cg < kRows && row < ldm)
-      put_scale_major<UE>(f.s_row, (size_t)at.g * (UE ? (Nb + 3) / 4 : Nb), at.nb, Nb, ldm, row,
-                          row < at.M ? mine : (UE ? 127u : 0u));
-  }
-  if (!f.q_col && !f.q_blk) return;
-
-  float m[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float v[8];
-    value(i, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(v[j]));
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
-  __syncthreads();   // the previous tile's factors have been read
-  if (lane < 16) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sh.part[warp][cg * 8 + j] = m[j];
-  }
-  __syncthreads();
-  if (t < 128) {
-    float top = 0.0f;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, sh.part[w][t]);
-    if (f.q_col) {
-      float fac;
-      uint32_t scale;
-      group_scale<UE>(top, fac, scale);
-      sh.factor[t] = fac;
-      const int n = at.nb * 128 + t, ldn = (at.N + 3) / 4 * 4;
-      if (n < ldn)
-        put_scale_major<UE>(f.s_col, (size_t)at.g * (UE ? (Mb + 3) / 4 : Mb), at.mb, Mb, ldn, n,
-                            n < at.N ? scale : (UE ? 127u : 0u));
-    }
-    const uint32_t block = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // magnitudes: ordered as integers
-    if (lane == 0) sh.top[warp] = __uint_as_float(block);
-  }
-  __syncthreads();
-  float cf[8], bf = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) cf[j] = f.q_col ? sh.factor[cg * 8 + j] : 0.0f;
-  if (f.q_blk) {
-    uint32_t scale;
-    group_scale<UE>(fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3])), bf, scale);
-    if (t == 0) {
-      if (f.s_blk) put_scale_last<UE>(f.s_blk, (size_t)at.g * Mb + at.mb, at.nb, Nb, scale);
-      if (f.s_blk_t) put_scale_last<UE>(f.s_blk_t, (size_t)at.g * Nb + at.nb, at.mb, Mb, scale);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i * kStep;
-    if (row >= at.M || !col_live) continue;
-    float v[8];
-    value(i, v);
-    const size_t off = (line0 + row) * at.N + col;
-    if (f.q_col)
-      *reinterpret_cast<uint2*>(f.q_col + off) =
-          make_uint2(codes4(v, cf[0], cf[1], cf[2], cf[3]), codes4(v + 4, cf[4], cf[5], cf[6], cf[7]));
-    if (f.q_blk)
-      *reinterpret_cast<uint2*>(f.q_blk + off) = make_uint2(codes4(v, bf, bf, bf, bf), codes4(v + 4, bf, bf, bf, bf));
-  }
-}
-
-constexpr int kCastThreads = 256;
-
 template <bool UE>
-__global__ void __launch_bounds__(kCastThreads) cast_kernel(const uint16_t* __restrict__ x,
-                                                            const int32_t* __restrict__ m_indices, const CastForms f,
-                                                            int M, int N) {
-  __shared__ TileShared<kCastThreads> sh;
-  constexpr int kRows = 128 * 16 / kCastThreads, kStep = kCastThreads / 16;
+__global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uint16_t* __restrict__ x,
+                                                                       const int32_t* __restrict__ m_indices,
+                                                                       const CastForms f, int M, int N, int tiles) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  CastShared& sh = *reinterpret_cast<CastShared*>(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int Mb = (M + 127) / 128, Nb = (N + 127) / 128;
-  TilePlace at;
-  at.nb = blockIdx.x % Nb;
-  at.mb = blockIdx.x / Nb % Mb;
-  at.g = blockIdx.x / Nb / Mb;
-  at.M = M;
-  at.N = N;
-  const int row0 = at.mb * 128 + threadIdx.x / 16, col = at.nb * 128 + threadIdx.x % 16 * 8;
-  const uint16_t* src = x + ((size_t)at.g * M + row0) * N + col;
-  uint4 raw[kRows];
+  const int t = threadIdx.x, cg = t % 16, warp = t / 32, lane = t % 32;
+  const int Mb = (M + 127) / 128, Nb = (N + 127) / 128, ldm = (M + 3) / 4 * 4;
+  const bool across = f.q_col || f.q_blk;   // anything beside rows
+
+  auto fetch = [&](int tile, int buf) {
+    const int nb = tile % Nb, mb = tile / Nb % Mb, g = tile / Nb / Mb;
+    const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
+    const uint16_t* src = x + ((size_t)g * M + row0) * N + col;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i * kStep;
-    const bool live = row < M && col < N && (!m_indices || __ldg(m_indices + row) >= 0);
-    raw[i] = live ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)i * kStep * N)) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kCastRows; ++i) {
+      const int row = row0 + i * kCastStep;
+      const bool live = row < M && col < N && (!m_indices || __ldg(m_indices + row) >= 0);
+      copy_16(&sh.next[buf][i][t], live ? src + (size_t)i * kCastStep * N : x, live);
+    }
+  };
+
+  int buf = 0;
+  if (blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  commit_copies();
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, buf ^ 1);
+    commit_copies();
+    wait_copies<1>();
+    const int nb = tile % Nb, mb = tile / Nb % Mb, g = tile / Nb / Mb;
+    const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
+    const bool col_live = col < N;
+    const size_t off0 = ((size_t)g * M + row0) * N + col;
+    uint4 raw[kCastRows];
+#pragma unroll
+    for (int i = 0; i < kCastRows; ++i) raw[i] = sh.next[buf][i][t];
+    // magnitudes, two BF16 a step; a NaN gives way to the other operand, here at the latest to 0
+    auto mag = [](uint32_t w) { w &= 0x7FFF7FFFu; return *reinterpret_cast<__nv_bfloat162*>(&w); };
+    const __nv_bfloat162 none = mag(0);
+
+    if (f.q_row) {
+      float m[8];
+#pragma unroll
+      for (int i = 0; i < kCastRows; ++i) {
+        const __nv_bfloat162 w = __hmax2(__hmax2(__hmax2(mag(raw[i].x), none), mag(raw[i].y)), __hmax2(__hmax2(mag(raw[i].z), none), mag(raw[i].w)));
+        m[i] = fmaxf(__low2float(w), __high2float(w));
+      }
+      float fac;
+      uint32_t scale;
+      group_scale<UE>(max8_over_16(m, cg), fac, scale);   // of row cg % 8
+      // the rows past M up to align4(M) get the filler
+      const int row = row0 + cg * kCastStep;
+      if (cg < 8 && row < ldm)
+        put_scale_major<UE>(f.s_row, (size_t)g * (UE ? (Nb + 3) / 4 : Nb), nb, Nb, ldm, row, row < M ? scale : (UE ? 127u : 0u));
+#pragma unroll
+      for (int i = 0; i < kCastRows; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, fac, i, 16);
+        float v[8];
+        unpack8(raw[i], v);
+        if (row0 + i * kCastStep < M && col_live) put_codes8(f.q_row + off0 + (size_t)i * kCastStep * N, v, fi);
+      }
+    }
+    if (!across) continue;
+
+    __nv_bfloat162 m[4] = {none, none, none, none};
+#pragma unroll
+    for (int i = 0; i < kCastRows; ++i) {
+      m[0] = __hmax2(m[0], mag(raw[i].x));
+      m[1] = __hmax2(m[1], mag(raw[i].y));
+      m[2] = __hmax2(m[2], mag(raw[i].z));
+      m[3] = __hmax2(m[3], mag(raw[i].w));
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __hmax2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+    if (lane < 16) {
+      float4* to = reinterpret_cast<float4*>(&sh.part[warp][cg * 8]);
+      to[0] = make_float4(__low2float(m[0]), __high2float(m[0]), __low2float(m[1]), __high2float(m[1]));
+      to[1] = make_float4(__low2float(m[2]), __high2float(m[2]), __low2float(m[3]), __high2float(m[3]));
+    }
+    __syncthreads();   // (every thread has read the previous tile's factors by then)
+    if (t < 128) {
+      float top = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kCastThreads / 32; ++w) top = fmaxf(top, sh.part[w][t]);
+      if (f.q_col) {
+        float fac;
+        uint32_t scale;
+        group_scale<UE>(top, fac, scale);
+        sh.factor[t] = fac;
+        const int n = nb * 128 + t;
+        if (n < N) put_scale_major<UE>(f.s_col, (size_t)g * (UE ? (Mb + 3) / 4 : Mb), mb, Mb, N, n, scale);   // (N % 16 == 0)
+      }
+      const uint32_t block = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // magnitudes: ordered as integers
+      if (lane == 0) sh.top[warp] = __uint_as_float(block);
+    }
+    __syncthreads();
+    float cf[8], bf = 0.0f;
+    {
+      const float4 a = *reinterpret_cast<const float4*>(&sh.factor[cg * 8]), b = *reinterpret_cast<const float4*>(&sh.factor[cg * 8 + 4]);
+      cf[0] = a.x; cf[1] = a.y; cf[2] = a.z; cf[3] = a.w;
+      cf[4] = b.x; cf[5] = b.y; cf[6] = b.z; cf[7] = b.w;
+    }
+    if (f.q_blk) {
+      uint32_t scale;
+      group_scale<UE>(fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3])), bf, scale);
+      if (t == 0) {
+        if (f.s_blk) put_scale_last<UE>(f.s_blk, (size_t)g * Mb + mb, nb, Nb, scale);
+        if (f.s_blk_t) put_scale_last<UE>(f.s_blk_t, (size_t)g * Nb + nb, mb, Mb, scale);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCastRows; ++i) {
+      if (row0 + i * kCastStep >= M || !col_live) continue;
+      float v[8];
+      unpack8(raw[i], v);
+      const size_t off = off0 + (size_t)i * kCastStep * N;
+      if (f.q_col) put_codes8(f.q_col + off, v, cf);
+      if (f.q_blk) put_codes8(f.q_blk + off, v, bf);
+    }
   }
-  cast_tile<UE, kCastThreads>(sh, f, at, [&](int i, float(&v)[8]) { unpack8(raw[i], v); });
+  wait_copies<0>();
 }
 
+// ---------------------------------------------------------------------------------------------
 // The backward pass of H = dropout(silu(g)·u), from the saved BF16 g and u and the gradient dH:
 //   t = dropout(dH) (the forward pass's mask and scale), s = 1/(1 + e^-g),
 //   dg = t·u·s·(1 + g·(1 - s)),  du = t·g·s,
-// in FP32, cast straight to the row and column forms of [dG dU] ([M, 2I]); and, if asked, the blocks of H
-// formed again from g and u. The tile of dG and the tile of dU use the same inputs.
-constexpr int kGateThreads = 512;
+// in FP32, cast straight to the row and column forms of [dG dU] ([M, 2I]); and, if asked (BLOCKS), the blocks
+// of H formed again from g and u. One tile of inputs gives a tile of dG and a tile of dU. Thread t holds
+// columns 8·(t % 16).. of the tile's rows i·32 + t/16, i < 4. Persistent, with the next tile's inputs
+// copied ahead as above: one CTA of 512 threads an SM, since dG and dU stay in registers between their
+// maxima and their codes.
+constexpr int kGateThreads = 512, kGateRows = 4, kGateStep = 32;
 
-template <bool UE>
-__global__ void __launch_bounds__(kGateThreads) swiglu_backward_kernel(const uint16_t* __restrict__ dh,
-                                                                       const uint16_t* __restrict__ gu,
-                                                                       const int32_t* __restrict__ m_indices,
-                                                                       const Dropout d, const CastForms f_gu,
-                                                                       const CastForms f_h, int M, int I) {
-  __shared__ TileShared<kGateThreads> sh;
-  constexpr int kRows = 128 * 16 / kGateThreads, kStep = kGateThreads / 16;
+struct GateShared {
+  uint4 next[2][3 * kGateRows][kGateThreads];
+  float part[2][kGateThreads / 32][128];   // each warp's column maxima of dG and dU
+  float factor[2][128];
+  float h_top[kGateThreads / 32];
+  float h_factor;
+};
+
+template <bool UE, bool BLOCKS>
+__global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const uint16_t* __restrict__ dh,
+                                                                          const uint16_t* __restrict__ gu,
+                                                                          const int32_t* __restrict__ m_indices,
+                                                                          const Dropout d, const CastForms f,
+                                                                          const CastForms f_h, int M, int I, int tiles) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  GateShared& sh = *reinterpret_cast<GateShared*>(smem);
   griddep_wait();
   griddep_launch_dependents();
-  const int nI = I / 128;
-  const int nb = blockIdx.x % nI, mb = blockIdx.x / nI;
-  const int row0 = mb * 128 + threadIdx.x / 16, col = nb * 128 + threadIdx.x % 16 * 8;
-  uint4 rt[kRows], rg[kRows], ru[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int row = row0 + i * kStep;
-    const bool live = row < M && (!m_indices || __ldg(m_indices + row) >= 0);
-    const size_t at = (size_t)row * I + col, at2 = (size_t)row * 2 * I + col;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    rt[i] = live ? __ldg(reinterpret_cast<const uint4*>(dh + at)) : zero;
-    rg[i] = live ? __ldg(reinterpret_cast<const uint4*>(gu + at2)) : zero;
-    ru[i] = live ? __ldg(reinterpret_cast<const uint4*>(gu + at2 + I)) : zero;
-  }
+  const int t = threadIdx.x, cg = t % 16, warp = t / 32, lane = t % 32;
+  const int nI = I / 128, Mb = (M + 127) / 128, ldm = (M + 3) / 4 * 4;
   const bool drop = d.threshold != 0;
   const Philox gen = drop ? Philox(d.rng) : Philox();
-  float dg[kRows][8], du[kRows][8], h[kRows][8];
+
+  auto fetch = [&](int tile, int buf) {
+    const int row0 = tile / nI * 128 + t / 16, col = tile % nI * 128 + cg * 8;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float t[8], g[8], u[8];
-    unpack8(rt[i], t);
-    unpack8(rg[i], g);
-    unpack8(ru[i], u);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (drop) {
-      w = gen(((uint64_t)(row0 + i * kStep) * I + col) / 8);
-      dropout8(t, w, d.threshold, d.scale);
+    for (int i = 0; i < kGateRows; ++i) {
+      const int row = row0 + i * kGateStep;
+      const bool live = row < M && (!m_indices || __ldg(m_indices + row) >= 0);
+      const size_t at = live ? (size_t)row * I + col : 0, at2 = live ? (size_t)row * 2 * I + col : 0;
+      copy_16(&sh.next[buf][3 * i][t], dh + at, live);
+      copy_16(&sh.next[buf][3 * i + 1][t], gu + at2, live);
+      copy_16(&sh.next[buf][3 * i + 2][t], gu + at2 + I, live);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-g[j])), a = g[j] * s;
-      dg[i][j] = t[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
-      du[i][j] = t[j] * a;
-      h[i][j] = a * u[j];
-    }
-    if (drop) dropout8(h[i], w, d.threshold, d.scale);
-  }
-  TilePlace at{0, mb, nb, M, 2 * I};
-  auto take = [](const float(&from)[8], float(&v)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = from[j];
   };
-  cast_tile<UE, kGateThreads>(sh, f_gu, at, [&](int i, float(&v)[8]) { take(dg[i], v); });
-  at.nb = nI + nb;
-  cast_tile<UE, kGateThreads>(sh, f_gu, at, [&](int i, float(&v)[8]) { take(du[i], v); });
-  if (f_h.q_blk) {
-    at = TilePlace{0, mb, nb, M, I};
-    cast_tile<UE, kGateThreads>(sh, f_h, at, [&](int i, float(&v)[8]) { take(h[i], v); });
+
+  int buf = 0;
+  if (blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  commit_copies();
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, buf ^ 1);
+    commit_copies();
+    wait_copies<1>();
+    const int nb = tile % nI, mb = tile / nI;
+    const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
+    float v[2][kGateRows][8], h[BLOCKS ? kGateRows : 1][8];   // dG and dU; H
+    float line[8], cmax[2][8], hmax = 0.0f;                    // row maxima of dG, then of dU; column maxima
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[a][j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kGateRows; ++i) {
+      float dt[8], g[8], u[8];
+      unpack8(sh.next[buf][3 * i][t], dt);
+      unpack8(sh.next[buf][3 * i + 1][t], g);
+      unpack8(sh.next[buf][3 * i + 2][t], u);
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (drop) {
+        w = gen(((uint64_t)(row0 + i * kGateStep) * I + col) / 8);
+        dropout8(dt, w, d.threshold, d.scale);
+      }
+      line[i] = line[4 + i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-g[j])), gs = g[j] * s;
+        const float dg = dt[j] * u[j] * s * (1.0f + g[j] * (1.0f - s)), du = dt[j] * gs;
+        v[0][i][j] = dg;
+        v[1][i][j] = du;
+        line[i] = fmaxf(line[i], fabsf(dg));
+        line[4 + i] = fmaxf(line[4 + i], fabsf(du));
+        cmax[0][j] = fmaxf(cmax[0][j], fabsf(dg));
+        cmax[1][j] = fmaxf(cmax[1][j], fabsf(du));
+        if constexpr (BLOCKS) h[i][j] = gs * u[j];
+      }
+      if constexpr (BLOCKS) {
+        if (drop) dropout8(h[i], w, d.threshold, d.scale);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) hmax = fmaxf(hmax, fabsf(h[i][j]));
+      }
+    }
+    const size_t off0 = (size_t)row0 * 2 * I + col;
+
+    if (f.q_row) {
+      float fac;
+      uint32_t scale;
+      group_scale<UE>(max8_over_16(line, cg), fac, scale);   // of row cg % 4, of dG (cg % 8 < 4) or dU
+      const int row = row0 + (cg & 3) * kGateStep;
+      if (cg < 8 && row < ldm)
+        put_scale_major<UE>(f.s_row, 0, nb + (cg >> 2) * nI, 2 * nI, ldm, row, row < M ? scale : (UE ? 127u : 0u));
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int i = 0; i < kGateRows; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, fac, a * 4 + i, 16);
+          if (row0 + i * kGateStep < M) put_codes8(f.q_row + off0 + (size_t)i * kGateStep * 2 * I + a * I, v[a][i], fi);
+        }
+    }
+    if (!f.q_col && !BLOCKS) continue;
+
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) cmax[a][j] = fmaxf(cmax[a][j], __shfl_xor_sync(0xffffffffu, cmax[a][j], 16));
+      if (lane < 16) {
+        float4* to = reinterpret_cast<float4*>(&sh.part[a][warp][cg * 8]);
+        to[0] = make_float4(cmax[a][0], cmax[a][1], cmax[a][2], cmax[a][3]);
+        to[1] = make_float4(cmax[a][4], cmax[a][5], cmax[a][6], cmax[a][7]);
+      }
+    }
+    if constexpr (BLOCKS) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(hmax));   // magnitudes: ordered as integers
+      if (lane == 0) sh.h_top[warp] = __uint_as_float(top);
+    }
+    __syncthreads();   // (every thread has read the previous tile's factors by then)
+    if (t < 256) {
+      const int a = t / 128, c = t % 128;
+      float top = 0.0f, fac;
+#pragma unroll
+      for (int w = 0; w < kGateThreads / 32; ++w) top = fmaxf(top, sh.part[a][w][c]);
+      uint32_t scale;
+      group_scale<UE>(top, fac, scale);
+      sh.factor[a][c] = fac;
+      if (f.q_col) put_scale_major<UE>(f.s_col, 0, mb, Mb, 2 * I, a * I + nb * 128 + c, scale);
+    } else if (BLOCKS && warp == 8) {
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(lane < kGateThreads / 32 ? sh.h_top[lane] : 0.0f));
+      float fac;
+      uint32_t scale;
+      group_scale<UE>(__uint_as_float(top), fac, scale);
+      if (lane == 0) {
+        sh.h_factor = fac;
+        put_scale_last<UE>(f_h.s_blk_t, nb, mb, Mb, scale);
+      }
+    }
+    __syncthreads();
+    if (f.q_col) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const float4 p = *reinterpret_cast<const float4*>(&sh.factor[a][cg * 8]), q = *reinterpret_cast<const float4*>(&sh.factor[a][cg * 8 + 4]);
+        const float cf[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < kGateRows; ++i)
+          if (row0 + i * kGateStep < M) put_codes8(f.q_col + off0 + (size_t)i * kGateStep * 2 * I + a * I, v[a][i], cf);
+      }
+    }
+    if constexpr (BLOCKS) {
+      const float hf = sh.h_factor;
+#pragma unroll
+      for (int i = 0; i < kGateRows; ++i)
+        if (row0 + i * kGateStep < M) put_codes8(f_h.q_blk + (size_t)(row0 + i * kGateStep) * I + col, h[i], hf);
+    }
   }
+  wait_copies<0>();
+}
+
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, bool (&done)[64]) {   // once per device and kernel
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  done[dev] = e == cudaSuccess;
+  return e;
+}
+
+template <bool UE>
+cudaError_t launch_cast_as(const uint16_t* x, const int32_t* m_indices, const CastForms& f, int G, int M, int N,
+                           const StreamArgs& s) {
+  static bool done[64] = {};
+  const cudaError_t e = allow_smem(cast_kernel<UE>, sizeof(CastShared), done);
+  if (e != cudaSuccess) return e;
+  const int tiles = G * ((M + 127) / 128) * ((N + 127) / 128), most = kCastCtas * s.sms;
+  return launch_plain(cast_kernel<UE>, tiles < most ? tiles : most, kCastThreads, sizeof(CastShared), s, x, m_indices, f, M,
+                      N, tiles);
+}
+
+template <bool UE, bool BLOCKS>
+cudaError_t launch_backward_as(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices, const Dropout& d,
+                               const CastForms& dgu, const CastForms& h, int M, int I, const StreamArgs& s) {
+  static bool done[64] = {};
+  const cudaError_t e = allow_smem(swiglu_backward_kernel<UE, BLOCKS>, sizeof(GateShared), done);
+  if (e != cudaSuccess) return e;
+  const int tiles = (M + 127) / 128 * (I / 128);
+  return launch_plain(swiglu_backward_kernel<UE, BLOCKS>, tiles < s.sms ? tiles : s.sms, kGateThreads, sizeof(GateShared), s, dh,
+                      gu, m_indices, d, dgu, h, M, I, tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_cast(const uint16_t* x, const int32_t* m_indices, const CastForms& f, int G, int M, int N,
                         bool ue8m0, const StreamArgs& s) {
-  const int tiles = G * ((M + 127) / 128) * ((N + 127) / 128);
-  return launch_plain(ue8m0 ? cast_kernel<true> : cast_kernel<false>, tiles, kCastThreads, 0, s, x, m_indices, f, M, N);
+  return ue8m0 ? launch_cast_as<true>(x, m_indices, f, G, M, N, s) : launch_cast_as<false>(x, m_indices, f, G, M, N, s);
 }
 
 cudaError_t launch_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices,
                                    const Dropout& d, const CastForms& dgu, const CastForms& h, int M, int I,
                                    bool ue8m0, const StreamArgs& s) {
-  const int tiles = (M + 127) / 128 * (I / 128);
-  return launch_plain(ue8m0 ? swiglu_backward_kernel<true> : swiglu_backward_kernel<false>, tiles, kGateThreads, 0, s,
-                      dh, gu, m_indices, d, dgu, h, M, I);
+  auto go = [&](auto kernel) { return kernel(dh, gu, m_indices, d, dgu, h, M, I, s); };
+  if (h.q_blk) return ue8m0 ? go(launch_backward_as<true, true>) : go(launch_backward_as<false, true>);
+  return ue8m0 ? go(launch_backward_as<true, false>) : go(launch_backward_as<false, false>);
 }
 
 }  // namespace dg

@@ -87,50 +87,52 @@ __device__ __forceinline__ void gated_box(const CUtensorMap* tm, uint8_t* stagin
 
 // The epilogue of one warp's 32 rows x 64 columns of H. row0: its first row of H; write_row: whether this
 // lane's row is stored; all_rows: whether TMA may store the slab (rows past the matrix are clipped there).
+// Boxes go out in the order G, U, H of one half of the columns, then of the other, so that the staging
+// buffers drain while h is formed.
 template <bool OUT_F32>
 __device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensorMap* tmH, void* H, int I, float* acc,
                                                int row0, int col0, bool write_row, bool all_rows, uint8_t* staging,
                                                uint32_t box_bytes, uint32_t& count, int lane) {
   const size_t row = (size_t)row0 + lane;
-  if (e.gu) {
-    if (all_rows) {
+  auto form_h = [&](int b) {   // columns 32·b .. of H, in place of their gate values
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 32 * b, (b >> 1) * I + col0 + (b & 1) * 32, row0, lane);
-    } else if (write_row) {
+    for (int j = 32 * b; j < 32 * b + 32; ++j) acc[j] = silu_f32(acc[j]) * acc[64 + j];
+    if (e.drop.threshold) {
+      const Philox gen(e.drop.rng);
+      const uint64_t index = (row * I + col0) / 8;
+#pragma unroll
+      for (int j = 32 * b; j < 32 * b + 32; j += 8)
+        dropout8(*reinterpret_cast<float(*)[8]>(acc + j), gen(index + j / 8), e.drop.threshold, e.drop.scale);
+    }
+  };
+  if (all_rows) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (e.gu) {
+        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 32 * b, col0 + 32 * b, row0, lane);
+        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 64 + 32 * b, I + col0 + 32 * b, row0, lane);
+      }
+      form_h(b);
+      constexpr int kCols = OUT_F32 ? 16 : 32;
+#pragma unroll
+      for (int c = 32 * b; c < 32 * b + 32; c += kCols)
+        gated_box<OUT_F32>(tmH, staging, box_bytes, count, acc + c, col0 + c, row0, lane);
+    }
+  } else if (write_row) {
+    if (e.gu) {
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(e.gu) + row * 2 * I + col0;
 #pragma unroll
-      for (int j = 0; j < 128; j += 8) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = acc[j + k];
-        store8(dst + (j >= 64 ? I - 64 : 0) + j, v);
-      }
+      for (int j = 0; j < 128; j += 8)
+        store8(dst + (j >= 64 ? I - 64 : 0) + j, *reinterpret_cast<float(*)[8]>(acc + j));
     }
-  }
-#pragma unroll
-  for (int j = 0; j < 64; ++j) acc[j] = silu_f32(acc[j]) * acc[64 + j];
-  if (e.drop.threshold) {
-    const Philox gen(e.drop.rng);
-    const uint64_t index = (row * I + col0) / 8;
-#pragma unroll
-    for (int j = 0; j < 64; j += 8) dropout8(*reinterpret_cast<float(*)[8]>(acc + j), gen(index + j / 8), e.drop.threshold, e.drop.scale);
-  }
-  if (all_rows) {
-    constexpr int kCols = OUT_F32 ? 16 : 32;
-#pragma unroll
-    for (int b = 0; b < 64 / kCols; ++b)
-      gated_box<OUT_F32>(tmH, staging, box_bytes, count, acc + kCols * b, col0 + kCols * b, row0, lane);
-  } else if (write_row) {
+    form_h(0);
+    form_h(1);
 #pragma unroll
     for (int j = 0; j < 64; j += 8) {
-      float v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = acc[j + k];
       if constexpr (OUT_F32)
-        store8(static_cast<float*>(H) + row * I + col0 + j, v);
+        store8(static_cast<float*>(H) + row * I + col0 + j, *reinterpret_cast<float(*)[8]>(acc + j));
       else
-        store8(static_cast<__nv_bfloat16*>(H) + row * I + col0 + j, v);
+        store8(static_cast<__nv_bfloat16*>(H) + row * I + col0 + j, *reinterpret_cast<float(*)[8]>(acc + j));
     }
   }
 }

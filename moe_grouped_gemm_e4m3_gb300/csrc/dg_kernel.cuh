@@ -208,8 +208,9 @@ __device__ __forceinline__ Sched make_sched(const GemmParams& p, int tiles, int 
   return s;
 }
 
-// Decodes work unit t (warp-cooperative for masked and contiguous modes).
-template <int BN, Mode MODE>
+// Decodes work unit t (warp-cooperative for masked and contiguous modes). MAY_BE_DENSE: the contiguous
+// form with m_indices null is the dense one (one group, every row stored).
+template <int BN, Mode MODE, bool MAY_BE_DENSE = false>
 __device__ __forceinline__ Tile decode_tile(const GemmParams& p, const Sched& sc, int t, int lane) {
   Tile tile;
   tile.skip = false;
@@ -296,6 +297,7 @@ __device__ __forceinline__ Tile decode_tile(const GemmParams& p, const Sched& sc
       // A block's group is the largest valid index among its rows (padding rows are -1).
       // Rows with an index outside [-1, G) are flagged and never stored.
       auto block_group = [&](int m_blk) -> int {
+        if (MAY_BE_DENSE && !p.m_indices) return 0;
         int mx = -1;
         bool bad = false;
 #pragma unroll
@@ -427,7 +429,8 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 // and the 128 up rows I + 128·n ..; the epilogue pairs the two halves and stores
 // H = silu(gate)·up, 128 columns of the [G·M_max, I] output per tile.
 //
-// kSwigluGated (dense and contiguous forms, BN = 256): the same 256 B rows, but ordered gate 0..63, up
+// kSwigluGated (dense and contiguous forms in one instantiation, BN = 256; the separate dense one spilled
+// 84 bytes into its K loop: 145 us instead of 119 on 4096x4096x7168): the same 256 B rows, but ordered gate 0..63, up
 // 0..63, gate 64..127, up 64..127 in the tile (four 64-row boxes), so that each epilogue warp owns
 // matching gate and up columns and the two warps of a quadrant exchange nothing.
 
@@ -454,8 +457,8 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
   // is still one phase behind: the parity test would pass early and the ring would lose step.
   static_assert(STAGES % 2 == 0 && NBUF % 2 == 0, "stage and TMEM-buffer counts must be even (two issuers)");
   static_assert(!SWIGLU || (BN == 256 && EPI_COLS == 128), "fused SwiGLU: BN = 256");
-  static_assert(!SWIGLU || (kGated ? MODE == kDense || MODE == kContiguous : MODE == kMasked),
-                "fused SwiGLU: masked; gated: dense and contiguous");
+  static_assert(!SWIGLU || (kGated ? MODE == kContiguous : MODE == kMasked),
+                "fused SwiGLU: masked; gated: contiguous, which with m_indices null is dense");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -558,9 +561,9 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       // the contiguous form, where a group's B (29 MB for N=4096, K=7168) fits in L2 and serves
       // all of that group's m-blocks (evict-first doubled its DRAM reads at the same speed).
       const uint64_t policy = l2_policy_evict_last();
-      const uint64_t policy_b = (MODE != kContiguous && p.M > 128) ? l2_policy_evict_first() : policy;
+      const uint64_t policy_b = ((kGated ? !p.m_indices : MODE != kContiguous) && p.M > 128) ? l2_policy_evict_first() : policy;
       for (int t = unit0; alive && t < total_units; t += ustep) {
-        const Tile tile = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         const int b_row = (MODE == kKGrouped ? 0 : tile.g * p.N) + tile.n_blk * BN;
         // Lane 0 runs the tile's K loop on its own (no warp-wide step per K-block).
@@ -672,7 +675,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       int last_b = -1;
       uint32_t last_ph = 0;
       for (int t = unit0; alive && t < total_units; t += ustep) {
-        const Tile tile = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         const uint32_t nk = (uint32_t)(tile.kb1 - tile.kb0);
         // Lane 0 runs this issuer's K-blocks of the tile on its own (no warp-wide step per K-block).
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       int kb_begin, kb_end;
       {
         const Sched sc = {stash[8], stash[9], stash[10], stash[11]};
-        const Tile tile0 = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile0 = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile0.skip) continue;
         if (lane == 0) {
           stash[0] = tile0.g; stash[1] = tile0.m_blk; stash[2] = tile0.n_blk; stash[3] = tile0.split;
@@ -1053,7 +1056,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       } else {
         write_row = false;
         if (row_exists) {
-          const int idx = __ldg(p.m_indices + m_local);
+          const int idx = (kGated && !p.m_indices) ? 0 : __ldg(p.m_indices + m_local);
           write_row = (idx == tile.g);
           if (idx != tile.g && idx != -1) atomicOr(p.status, kStatusBadGroup);
         }
@@ -1170,7 +1173,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         const int n = n_blk * BN + c4 * 4;
         if constexpr (kGated) {
           gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
-                                        g, MODE == kContiguous ? p.m_indices : nullptr, p.status, kStatusBadGroup);
+                                        g, p.m_indices, p.status, kStatusBadGroup);
         } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {
           float4 tot = cluster_sum_v4(part + r * kRowBytes + c4 * 16, S);

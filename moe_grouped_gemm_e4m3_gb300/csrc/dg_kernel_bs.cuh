@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
   // cluster split-K (kFlagClusterSplit) is compiled into the dense and contiguous forms only
   constexpr bool kClusterCapable = MODE == kDense || MODE == kContiguous;
   constexpr bool kGated = SWIGLU == kSwigluGated;
-  static_assert(!SWIGLU || (kGated ? MODE == kDense || MODE == kContiguous : MODE == kMasked),
-                "fused SwiGLU: masked; gated: dense and contiguous");
+  static_assert(!SWIGLU || (kGated ? MODE == kContiguous : MODE == kMasked),
+                "fused SwiGLU: masked; gated: contiguous, which with m_indices null is dense");
   constexpr uint32_t kIdesc = make_idesc_e4m3_bs(128, BN);
 
   extern __shared__ uint8_t smem_raw[];
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       for (int s = 0; s < STAGES; ++s) issued_phase[s] = -1;
       const uint64_t policy = l2_policy_evict_last();
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
-        const Tile tile = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         // (K-grouped: B [K_total, N] is shared by the groups, and A's M coordinate is the m-block's)
         const int b_row = (MODE == kKGrouped ? 0 : tile.g * p.N) + tile.n_blk * BN;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       const uint32_t a_step = a_mn ? 256u : 2u, b_step = b_mn ? 256u : 2u;
       const uint32_t idesc_layout = kIdesc | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16);
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
-        const Tile tile = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         int ok = 1;
         if (lane == 0) {
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         return true;
       };
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
-        const Tile tile = decode_tile<BN, MODE>(p, sc, t, lane);
+        const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         // (an empty K range, possible in the K-grouped form, is posted as such: the epilogue stores
         // zeros, and no scale slot is written for it)
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       if constexpr (MODE == kContiguous) {
         write_row = false;
         if (row_exists) {
-          const int idx = __ldg(p.m_indices + m_local);
+          const int idx = (kGated && !p.m_indices) ? 0 : __ldg(p.m_indices + m_local);
           write_row = (idx == tile.g);
           if (idx != tile.g && idx != -1) atomicOr(p.status, kStatusBadGroup);
         }
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         const int n = n_blk * BN + c4 * 4;
         if constexpr (kGated) {
           gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
-                                        g, MODE == kContiguous ? p.m_indices : nullptr, p.status, kStatusBadGroup);
+                                        g, p.m_indices, p.status, kStatusBadGroup);
         } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {
           float4 tot = cluster_sum_v4(part + r * kRowBytes + c4 * 16, S);

@@ -42,8 +42,8 @@ cudaError_t launch_kgrouped(const LaunchArgs& a);
 // 1x128-group scales.
 cudaError_t launch_masked_swiglu(const LaunchArgs& a, bool fp8_h = false);
 // The gated projection (dense and contiguous forms, block_n 256), FP32 scales and block-scaled.
-cudaError_t launch_gated(const LaunchArgs& a, Mode mode);
-cudaError_t launch_bs_gated(const LaunchArgs& a, Mode mode);
+cudaError_t launch_gated(const LaunchArgs& a);
+cudaError_t launch_bs_gated(const LaunchArgs& a);
 // The block-scaled kernel for packed UE8M0 scales (block_n is always 256).
 cudaError_t launch_bs(const LaunchArgs& a, Mode mode);
 // The block-scaled masked form fused with SwiGLU.
@@ -68,6 +68,10 @@ struct StreamArgs {
 // Y = R + dropout(X) over n elements, BF16 or FP32; r may be null (dg_dropout.cu).
 cudaError_t launch_dropout(const void* x, const void* r, void* y, bool f32, const Dropout& d, long long n,
                            const StreamArgs& s);
+// The dense gated projection for at most kFewTokens tokens (dg_gated_few.cu).
+constexpr int kFewTokens = 16;
+cudaError_t launch_gated_few(const uint8_t* A, const void* sA, const uint8_t* B, const void* sB, void* H, uint16_t* GU,
+                             const Dropout& drop, int M, int I, int K, bool out_f32, bool ue8m0, const StreamArgs& s);
 // The E4M3 forms of a matrix (dg_cast.cu): each with its codes and scales, or null codes.
 struct CastForms {
   uint8_t *q_row, *q_col, *q_blk;

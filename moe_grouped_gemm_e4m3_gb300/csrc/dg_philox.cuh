@@ -60,4 +60,10 @@ __device__ __forceinline__ void dropout8(float (&v)[8], const uint4& w, uint32_t
   }
 }
 
+// The same for element j (of eight) alone.
+__device__ __forceinline__ float dropout1(float v, const uint4& w, int j, uint32_t threshold, float scale) {
+  const uint32_t word = j < 4 ? (j < 2 ? w.x : w.y) : (j < 6 ? w.z : w.w);
+  return ((word >> (16 * (j & 1))) & 0xFFFFu) >= threshold ? __fmul_rn(v, scale) : 0.0f;
+}
+
 }  // namespace dg

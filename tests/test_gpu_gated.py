@@ -127,7 +127,7 @@ class Problem:
 
 
 @pytest.mark.parametrize("scales", SCALES)
-@pytest.mark.parametrize("M,I,K", [(1, 128, 16), (1, 256, 1040), (3, 384, 144), (64, 128, 640), (127, 128, 128),
+@pytest.mark.parametrize("M,I,K", [(1, 128, 16), (1, 256, 1040), (3, 384, 144), (8, 128, 7168), (9, 256, 528), (16, 128, 80), (17, 128, 144), (64, 128, 640), (127, 128, 128),
                                    (128, 256, 272), (129, 128, 1024), (300, 384, 528), (257, 1024, 2064)])
 def test_dense(dg, M, I, K, scales):
     Problem(M, I, K, scales).check(dg)
@@ -143,7 +143,9 @@ def test_contiguous(dg, sizes, I, K, scales):
 @pytest.mark.parametrize("scales", SCALES)
 @pytest.mark.parametrize("p", [0.1, 0.5])
 def test_dropout_in_the_epilogue(dg, scales, p):
-    Problem(5, 256, 1040, scales).check(dg, p)            # K split in a cluster
+    Problem(5, 256, 1040, scales).check(dg, p)            # few tokens: no tiles
+    Problem(13, 128, 2064, scales).check(dg, p)
+    Problem(40, 256, 1040, scales).check(dg, p)           # K split in a cluster
     Problem(300, 128, 272, scales).check(dg, p)
     Problem(None, 128, 272, scales, sizes=[100, 0, 200], holes=[50]).check(dg, p)
 
@@ -188,7 +190,7 @@ def test_bad_group_index_is_flagged(dg, scales):
 
 @pytest.mark.parametrize("scales", SCALES)
 def test_timeout_and_recovery(dg, scales):
-    for prob in (Problem(300, 256, 1024, scales), Problem(4, 256, 2048, scales), Problem(None, 128, 256, scales, sizes=[100, 60])):
+    for prob in (Problem(300, 256, 1024, scales), Problem(20, 256, 2048, scales), Problem(None, 128, 256, scales, sizes=[100, 60])):
         ref, _ = prob.run(dg, False)
         prev = dg.dg_set_wait_limit_us(0)
         try:
