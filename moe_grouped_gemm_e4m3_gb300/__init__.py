@@ -239,6 +239,31 @@ def _expect(t, name, shape):
         raise ValueError(f"{name} has shape {list(got)}, expected {list(shape)}")
 
 
+def _pointers(*tensors):
+    """The pointers of (tensor, name, dtypes, shape) arguments, checked in one pass where all is well. Otherwise
+    every shape is looked at before any pointer is taken, and the first thing wrong is named. The name of an
+    optional argument ends in "?": None is a null pointer there."""
+    ptrs = []
+    try:
+        for t, name, dtypes, shape in tensors:
+            if t is None and name[-1] == "?":
+                ptrs.append(None)
+            elif t.dtype in dtypes and t.shape == shape and t.is_cuda and t.is_contiguous():
+                ptrs.append(t.data_ptr())
+            else:
+                break
+        else:
+            return ptrs
+    except (AttributeError, TypeError):
+        pass
+    given = [(t, name.rstrip("?"), dtypes, shape) for t, name, dtypes, shape in tensors if t is not None or name[-1] != "?"]
+    for t, name, _, shape in given:
+        _expect(t, name, shape)
+    for t, name, dtypes, _ in given:
+        _ptr(t, name, dtypes)
+    raise AssertionError("unreachable: an argument was refused without a reason")
+
+
 def _cdiv(a, b):
     return -(-a // b)
 
@@ -304,10 +329,10 @@ def _check_scales_2d(name, sA, sB, M, N, K):
 def _dense(name, f32, A, sA, B, sB, D, stream):
     M, N, K = _dense_shapes(name, A, B)
     _check_scales_2d(name, sA, sB, M, N, K)
-    _expect(D, "D", (M, N))
-    lib = load()
-    _check(getattr(lib, name)(_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", _scale_types(name)), _ptr(B, "B", _fp8_types()),
-                              _ptr(sB, "sB", _scale_types(name)), _ptr(D, "D", _d_types(f32)), M, N, K, _stream(stream)))
+    q, st = _fp8_types(), _scale_types(name)
+    ptrs = _pointers((A, "A", q, A.shape), (sA, "sA", st, sA.shape), (B, "B", q, B.shape), (sB, "sB", st, sB.shape),
+                     (D, "D", _d_types(f32), (M, N)))
+    _check(getattr(load(), name)(*ptrs, M, N, K, _stream(stream)))
     return D
 
 
@@ -420,16 +445,11 @@ _LAYOUTS = {"nn": (False, True), "tn": (True, True), "tt": (True, False)}
 def _dense_layout(name, f32, A, sA, B, sB, D, M, N, K, stream):
     a_t, b_n = _LAYOUTS[name[len("dg_fp8_gemm_"):len("dg_fp8_gemm_") + 2]]
     M, N, K = int(M), int(N), int(K)
-    nks = _scale_k(name, K)
-    _expect(A, "A", (K, M) if a_t else (M, K))
-    _expect(B, "B", (K, N) if b_n else (N, K))
-    _expect(sA, "sA", (nks, _align4(M)))
-    _expect(sB, "sB", (_cdiv(N, 128), nks))
-    _expect(D, "D", (M, N))
-    lib = load()
-    st = _scale_types(name)
-    _check(getattr(lib, name)(_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()),
-                              _ptr(sB, "sB", st), _ptr(D, "D", _d_types(f32)), M, N, K, _stream(stream)))
+    nks, q, st = _scale_k(name, K), _fp8_types(), _scale_types(name)
+    ptrs = _pointers((A, "A", q, (K, M) if a_t else (M, K)), (sA, "sA", st, (nks, _align4(M))),
+                     (B, "B", q, (K, N) if b_n else (N, K)), (sB, "sB", st, (_cdiv(N, 128), nks)),
+                     (D, "D", _d_types(f32), (M, N)))
+    _check(getattr(load(), name)(*ptrs, M, N, K, _stream(stream)))
     return D
 
 
@@ -497,15 +517,11 @@ def _k_grouped(name, f32, A, sA, B, sB, k_offsets, D, stream):
     G = o[0] - 1
     if b[0] != K_total:
         raise ValueError(f"B has K_total = {b[0]}, A has K_total = {K_total}")
-    nks = _scale_k(name, K_total)
-    _expect(sA, "sA", (nks, _align4(M)))
-    _expect(sB, "sB", (_cdiv(N, 128), nks))
-    _expect(D, "D", (G, M, N))
-    lib = load()
-    st = _scale_types(name)
-    _check(getattr(lib, name)(_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()),
-                              _ptr(sB, "sB", st), _ptr(k_offsets, "k_offsets", _i32()),
-                              _ptr(D, "D", _d_types(f32)), G, M, N, K_total, _stream(stream)))
+    nks, q, st = _scale_k(name, K_total), _fp8_types(), _scale_types(name)
+    ptrs = _pointers((A, "A", q, (K_total, M)), (sA, "sA", st, (nks, _align4(M))), (B, "B", q, (K_total, N)),
+                     (sB, "sB", st, (_cdiv(N, 128), nks)), (k_offsets, "k_offsets", _i32(), (G + 1,)),
+                     (D, "D", _d_types(f32), (G, M, N)))
+    _check(getattr(load(), name)(*ptrs, G, M, N, K_total, _stream(stream)))
     return D
 
 
@@ -529,14 +545,6 @@ def dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32(A, sA, B, sB, k_offsets, D, st
     return _k_grouped("dg_fp8_k_grouped_gemm_tn_contiguous_ue8m0_f32", True, A, sA, B, sB, k_offsets, D, stream)
 
 
-def _opt(t, name, dtypes, shape):
-    """The pointer of an optional tensor of this shape (None: null)."""
-    if t is None:
-        return None
-    _expect(t, name, shape)
-    return _ptr(t, name, dtypes)
-
-
 @functools.cache
 def _i32():
     import torch
@@ -547,11 +555,6 @@ def _i32():
 def _rng_types():
     import torch
     return (torch.int64, torch.uint64)
-
-
-def _rng(rng):
-    """The pointer of the generator's state: a CUDA int64 (or uint64) tensor {seed, offset}."""
-    return None if rng is None else _opt(rng, "rng", _rng_types(), (2,))
 
 
 @functools.cache
@@ -572,17 +575,18 @@ def _gated(name, f32, A, sA, B, sB, m_indices, H, GU, rng, p, stream):
         raise ValueError(f"B has K = {b[-1]}, A has K = {K}")
     if N % 2:
         raise ValueError(f"B must hold I gate rows and I up rows, got {N}")
-    nks = _scale_k(name, K)
-    _expect(sA, "sA", (nks, _align4(M)))
-    _expect(sB, "sB", ((G,) if grouped else ()) + (_cdiv(N, 128), nks))
-    _expect(H, "H", (M, N // 2))
-    st = _scale_types(name)
-    head = (_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()), _ptr(sB, "sB", st))
-    tail = (_ptr(H, "H", _d_types(f32)), _opt(GU, "GU", _bf16(), (M, N)), _rng(rng), p, M, N, K)
+    nks, q, st = _scale_k(name, K), _fp8_types(), _scale_types(name)
+    sb = (_cdiv(N, 128), nks)
+    # (of a dense call the m_indices argument is an absent optional one, and not passed on)
+    pA, psA, pB, psB, pidx, pH, pGU, prng = _pointers(
+        (A, "A", q, (M, K)), (sA, "sA", st, (nks, _align4(M))), (B, "B", q, b), (sB, "sB", st, (G,) + sb if grouped else sb),
+        (m_indices, "m_indices" if grouped else "m_indices?", _i32(), (M,)), (H, "H", _d_types(f32), (M, N // 2)),
+        (GU, "GU?", _bf16(), (M, N)), (rng, "rng?", _rng_types(), (2,)))
+    f = getattr(load(), name)
     if grouped:
-        _expect(m_indices, "m_indices", (M,))
-        head, tail = head + (_ptr(m_indices, "m_indices", _i32()),), tail + (G,)
-    _check(getattr(load(), name)(*head, *tail, _stream(stream)))
+        _check(f(pA, psA, pB, psB, pidx, pH, pGU, prng, p, M, N, K, G, _stream(stream)))
+    else:
+        _check(f(pA, psA, pB, psB, pH, pGU, prng, p, M, N, K, _stream(stream)))
     return H
 
 
@@ -634,15 +638,11 @@ def _contig_nn(name, f32, A, sA, B, sB, m_indices, D, stream):
     G, N = b[0], b[2]
     if b[1] != K:
         raise ValueError(f"B has K = {b[1]}, A has K = {K}")
-    nks = _scale_k(name, K)
-    _expect(sA, "sA", (nks, _align4(M)))
-    _expect(sB, "sB", (G, _cdiv(N, 128), nks))
-    _expect(m_indices, "m_indices", (M,))
-    _expect(D, "D", (M, N))
-    st = _scale_types(name)
-    _check(getattr(load(), name)(_ptr(A, "A", _fp8_types()), _ptr(sA, "sA", st), _ptr(B, "B", _fp8_types()),
-                                 _ptr(sB, "sB", st), _ptr(m_indices, "m_indices", _i32()),
-                                 _ptr(D, "D", _d_types(f32)), M, N, K, G, _stream(stream)))
+    nks, q, st = _scale_k(name, K), _fp8_types(), _scale_types(name)
+    ptrs = _pointers((A, "A", q, (M, K)), (sA, "sA", st, (nks, _align4(M))), (B, "B", q, (G, K, N)),
+                     (sB, "sB", st, (G, _cdiv(N, 128), nks)), (m_indices, "m_indices", _i32(), (M,)),
+                     (D, "D", _d_types(f32), (M, N)))
+    _check(getattr(load(), name)(*ptrs, M, N, K, G, _stream(stream)))
     return D
 
 
@@ -670,14 +670,13 @@ def _swiglu_backward(name, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, 
     if len(h) != 2:
         raise ValueError(f"dH must be [M, I], got {list(h)}")
     M, I = h
-    _expect(GU, "GU", (M, 2 * I))
-    st, q = _scale_types(name), _fp8_types()
+    st, q, b = _scale_types(name), _fp8_types(), _bf16()
     wM, wN = _scale_k(name, M), _scale_k(name, 2 * I)
-    _check(getattr(load(), name)(
-        _ptr(dH, "dH", _bf16()), _ptr(GU, "GU", _bf16()), _opt(m_indices, "m_indices", _i32(), (M,)),
-        _rng(rng), p, _opt(dGUr, "dGUr", q, (M, 2 * I)), _opt(sR, "sR", st, (wN, _align4(M))),
-        _opt(dGUc, "dGUc", q, (M, 2 * I)), _opt(sC, "sC", st, (wM, 2 * I)), _opt(Hb, "Hb", q, (M, I)),
-        _opt(sHb, "sHb", st, (_cdiv(I, 128), wM)), M, I, _stream(stream)))
+    p_dh, p_gu, p_idx, p_rng, *forms = _pointers(
+        (dH, "dH", b, h), (GU, "GU", b, (M, 2 * I)), (m_indices, "m_indices?", _i32(), (M,)), (rng, "rng?", _rng_types(), (2,)),
+        (dGUr, "dGUr?", q, (M, 2 * I)), (sR, "sR?", st, (wN, _align4(M))), (dGUc, "dGUc?", q, (M, 2 * I)),
+        (sC, "sC?", st, (wM, 2 * I)), (Hb, "Hb?", q, h), (sHb, "sHb?", st, (_cdiv(I, 128), wM)))
+    _check(getattr(load(), name)(p_dh, p_gu, p_idx, p_rng, p, *forms, M, I, _stream(stream)))
     return dGUr, dGUc
 
 
@@ -704,14 +703,13 @@ def _cast(name, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream):
     if len(x) not in (2, 3):
         raise ValueError(f"X must be [M, N] or [G, M, N], got {list(x)}")
     M, N = x[-2:]
-    g = x[:-2]
+    g = tuple(x[:-2])
     st, q = _scale_types(name), _fp8_types()
-    wM, wN = _scale_k(name, M), _scale_k(name, N)
-    _check(getattr(load(), name)(
-        _ptr(X, "X", _bf16()), _opt(m_indices, "m_indices", _i32(), (M,)), _opt(Xr, "Xr", q, x),
-        _opt(sR, "sR", st, g + (wN, _align4(M))), _opt(Xc, "Xc", q, x), _opt(sC, "sC", st, g + (wM, _align4(N))),
-        _opt(Xb, "Xb", q, x), _opt(sB, "sB", st, g + (_cdiv(M, 128), wN)),
-        _opt(sBt, "sBt", st, g + (_cdiv(N, 128), wM)), g[0] if g else 1, M, N, _stream(stream)))
+    wM, wN, Mb, Nb = _scale_k(name, M), _scale_k(name, N), _cdiv(M, 128), _cdiv(N, 128)
+    ptrs = _pointers((X, "X", _bf16(), x), (m_indices, "m_indices?", _i32(), (M,)), (Xr, "Xr?", q, x),
+                     (sR, "sR?", st, g + (wN, _align4(M))), (Xc, "Xc?", q, x), (sC, "sC?", st, g + (wM, _align4(N))),
+                     (Xb, "Xb?", q, x), (sB, "sB?", st, g + (Mb, wN)), (sBt, "sBt?", st, g + (Nb, wM)))
+    _check(getattr(load(), name)(*ptrs, g[0] if g else 1, M, N, _stream(stream)))
 
 
 def dg_cast_fp8(X, Xr=None, sR=None, Xc=None, sC=None, Xb=None, sB=None, sBt=None, m_indices=None, stream=None):
@@ -733,12 +731,11 @@ def dg_dropout(X, Y, rng, p, R=None, stream=None):
     """Y = R + dropout(X) (R optional), bfloat16 or float32 tensors of one shape; Y may be X or R. rng is a CUDA
     int64 tensor {seed, offset}; the mask is a function of it, p and the flat index. Backward: the same
     call on the gradient, without R."""
-    dt = _f32() if getattr(X, "dtype", None) in _f32() else _bf16()
-    f32 = dt is _f32()
-    shape = _shape(X, "X")
-    _expect(Y, "Y", shape)
+    f32 = getattr(X, "dtype", None) in _f32()
+    dt, shape = _f32() if f32 else _bf16(), _shape(X, "X")
+    pX, pR, pY, prng = _pointers((X, "X", dt, shape), (R, "R?", dt, shape), (Y, "Y", dt, shape), (rng, "rng?", _rng_types(), (2,)))
     f = load().dg_dropout_f32 if f32 else load().dg_dropout_bf16
-    _check(f(_ptr(X, "X", dt), _opt(R, "R", dt, shape), _ptr(Y, "Y", dt), _rng(rng), p, X.numel(), _stream(stream)))
+    _check(f(pX, pR, pY, prng, p, X.numel(), _stream(stream)))
     return Y
 
 

@@ -239,9 +239,7 @@ struct Config {
   int raster_m;
 };
 
-// wide_only: BN = 256 whatever N (the gated projection, whose tile pairs 128 gate and 128 up rows).
-Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false,
-                     bool wide_only = false) {
+Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false) {
   // Cost model calibrated on GB300 (sm_103a), times in microseconds per CTA:
   //  * compute: one K-block (BM=128, BK=128) costs ~0.55 (BN=256) or ~0.50 (BN=128: an N=128 MMA
   //    takes as long as an N=256 one, for half the work);
@@ -263,11 +261,10 @@ Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool 
   int best_s = 1;
   double best_t = 1e300;
   const int max_s = (mode == dg::kMasked) ? 1 : kMaxSplits;
-  if (block_scaled) wide_only = true;
-  if (wide_only) bn = 256;
+  if (block_scaled) bn = 256;
   for (int cand_bn = 128; cand_bn <= 256; cand_bn += 128) {
-    if (cand_bn == 256 && N <= 128 && !wide_only) continue;
-    if (cand_bn == 128 && wide_only) continue;
+    if (cand_bn == 256 && N <= 128 && !block_scaled) continue;
+    if (cand_bn == 128 && block_scaled) continue;
     const int n_blocks = ceil_div(N, cand_bn);
     const int tiles = m_blocks * n_blocks;
     const double t_compute = block_scaled ? 0.30 : (cand_bn == 256 ? 0.55 : 0.50);
@@ -296,7 +293,7 @@ Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool 
   // Tuning overrides (environment): DG_BLOCK_N in {128, 256} and DG_SPLITS >= 1 (dense and
   // contiguous only; a split that would exceed one wave of units is still allowed here).
   int bn_final = bn, tiles_final = tiles;
-  if (const char* e = wide_only ? nullptr : std::getenv("DG_BLOCK_N")) {
+  if (const char* e = block_scaled ? nullptr : std::getenv("DG_BLOCK_N")) {
     const int v = std::atoi(e);
     if (v == 128 || v == 256) { bn_final = v; tiles_final = m_blocks * ceil_div(N, v); }
   }
@@ -511,8 +508,8 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                                                dg::StreamArgs{stream, sms, pdl_setting()});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
-  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
-  // (the gated kernels have the footprint of the plain BN = 256 ones: the same cluster capacities)
+  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled);
+  // (the gated kernels have the footprint of the plain ones: the same cluster capacities)
   if (!swiglu) fit_cluster_splits(cfg, mode, K, block_scaled, out_f32);
   const int d_cols = swiglu || gated ? N / 2 : N;   // width of D (fused SwiGLU: H has I = N/2 columns)
   if (swiglu) {
@@ -538,7 +535,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   p.nnb = ceil_div(N, 128);
   p.ldsa = dg_get_tma_aligned_size(rows, 4);
   p.num_m_blocks = ceil_div(rows, 128);
-  p.num_n_blocks = swiglu ? d_cols / 128 : ceil_div(N, cfg.block_n);   // (gated: 2I/256, the same I/128 blocks)
+  p.num_n_blocks = swiglu ? d_cols / 128 : ceil_div(N, cfg.block_n);   // (gated: I over block_n/2 columns of H)
   p.swiglu_i = swiglu || gated ? d_cols : 0;
   p.flags = (a_mn ? dg::kFlagAMN : 0) | (b_mn ? dg::kFlagBMN : 0) | (accumulate ? dg::kFlagAccumulate : 0) |
             wait_limit_flags();
@@ -618,8 +615,8 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                             128, 128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "A")) != DG_OK) {
     return s;
   }
-  // rows of B's boxes: the gated tile's 64-row quarters (FP32 scales) or gate and up halves
-  const int b_box = gated && !block_scaled ? 64 : (swiglu || gated ? 128 : (pair ? cfg.block_n / 2 : cfg.block_n));
+  // rows of B's boxes: the gated tile's quarters (FP32 scales), or gate and up halves
+  const int b_box = gated && !block_scaled ? cfg.block_n / 4 : (swiglu || gated ? 128 : (pair ? cfg.block_n / 2 : cfg.block_n));
   if (b_mn) {   // B stored [K, N]: N contiguous, boxes of 128 N-bytes x 128 K-rows
     if ((s = encode_2d(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, (uint64_t)b_rows, (uint64_t)b_ks, (uint64_t)b_rows, 128,
                        128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B")) != DG_OK)

@@ -1,9 +1,9 @@
 // dg_gated.cuh — the epilogue of the gated projection H = dropout(silu(X·Wgᵀ) · (X·Wuᵀ)) in the dense
 // and contiguous forms, shared by the FP32-scale and the block-scaled kernel.
 //
-// A tile covers 128 columns of H: 128 gate rows and the 128 up rows of the weights. Each epilogue warp
-// holds, for its 32 rows, 64 gate columns (acc[0..63]) and the same 64 up columns (acc[64..127]), so
-// silu(g)·u needs no exchange between warps. On request it also stores the pre-activations, rounded to
+// A tile covers 128 (BN = 256) or 64 (BN = 128) columns of H: as many gate rows and the matching up rows of
+// the weights. Each epilogue warp holds, for its 32 rows, HC = 64 or 32 gate columns (acc[0..]) and the same
+// up columns (acc[HC..]), so silu(g)·u needs no exchange between warps. On request it also stores the pre-activations, rounded to
 // BF16, at columns [j] (gate) and [I + j] (up) of GU, for the backward pass. H is formed from the FP32
 // values. Whole 32-row slabs leave through TMA (64-byte boxes, two staging buffers a warp);
 // slabs with rows that must stay untouched use predicated 16-byte stores.
@@ -92,18 +92,17 @@ __device__ __forceinline__ void gated_box(const CUtensorMap* tm, uint8_t* stagin
   __syncwarp();
 }
 
-// The epilogue of one warp's 32 rows x 64 columns of H. row0: its first row of H; write_row: whether this
+// The epilogue of one warp's 32 rows x HC columns of H. row0: its first row of H; write_row: whether this
 // lane's row is stored; all_rows: whether TMA may store the slab (rows past the matrix are clipped there).
-// Boxes go out in the order G, U, H of one half of the columns, then of the other, so that the staging
-// buffers drain while h is formed.
-template <bool OUT_F32>
+// Boxes go out in the order G, U, H of each 32 columns, so that the staging buffers drain while h is formed.
+template <bool OUT_F32, int HC>
 __device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensorMap* tmH, void* H, int I, float* acc,
                                                int row0, int col0, bool write_row, bool all_rows, uint8_t* staging,
                                                uint32_t box_bytes, uint32_t& count, int lane) {
   const size_t row = (size_t)row0 + lane;
   auto form_h = [&](int b) {   // columns 32·b .. of H, in place of their gate values
 #pragma unroll
-    for (int j = 32 * b; j < 32 * b + 32; ++j) acc[j] = silu_f32(acc[j]) * acc[64 + j];
+    for (int j = 32 * b; j < 32 * b + 32; ++j) acc[j] = silu_f32(acc[j]) * acc[HC + j];
     if (e.drop.threshold) {
       const Philox gen(e.drop.rng);
       const uint64_t index = (row * I + col0) / 8;
@@ -114,10 +113,10 @@ __device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensor
   };
   if (all_rows) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < HC / 32; ++b) {
       if (e.gu) {
         gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 32 * b, col0 + 32 * b, row0, lane);
-        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + 64 + 32 * b, I + col0 + 32 * b, row0, lane);
+        gated_box<false>(&e.tmGU, staging, box_bytes, count, acc + HC + 32 * b, I + col0 + 32 * b, row0, lane);
       }
       form_h(b);
       constexpr int kCols = OUT_F32 ? 16 : 32;
@@ -129,13 +128,13 @@ __device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensor
     if (e.gu) {
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(e.gu) + row * 2 * I + col0;
 #pragma unroll
-      for (int j = 0; j < 128; j += 8)
-        store8(dst + (j >= 64 ? I - 64 : 0) + j, *reinterpret_cast<float(*)[8]>(acc + j));
+      for (int j = 0; j < 2 * HC; j += 8)
+        store8(dst + (j >= HC ? I - HC : 0) + j, *reinterpret_cast<float(*)[8]>(acc + j));
     }
-    form_h(0);
-    form_h(1);
 #pragma unroll
-    for (int j = 0; j < 64; j += 8) {
+    for (int b = 0; b < HC / 32; ++b) form_h(b);
+#pragma unroll
+    for (int j = 0; j < HC; j += 8) {
       if constexpr (OUT_F32)
         store8(static_cast<float*>(H) + row * I + col0 + j, *reinterpret_cast<float(*)[8]>(acc + j));
       else
@@ -146,17 +145,18 @@ __device__ __forceinline__ void gated_epilogue(const GatedExt& e, const CUtensor
 
 // Cluster split-K: sums the rows r = rank (mod S) of the S partial tiles of a cluster in range order and
 // stores them. `part`: this CTA's partial tile in shared memory, rows of `row_bytes`, tile columns as
-// the epilogue warps hold them: [64 gate | 64 up] for columns 0..63 of H, then for 64..127.
+// the epilogue warps hold them: [HC gate | HC up] for columns 0..HC-1 of H, then for the next HC.
 // m_indices: the contiguous form's rows (null: dense); g: the tile's group.
-template <bool OUT_F32>
+template <bool OUT_F32, int HC>
 __device__ __forceinline__ void gated_cluster_reduce(const GatedExt& e, void* H, int I, uint32_t part, uint32_t row_bytes,
                                                      int S, int rank, int threads, int a_row, int rows, int n_blk, int g,
                                                      const int32_t* m_indices, int* status, int bad_group_bit) {
-  // A warp reads a row: 16 lanes the 64 gate (or up) columns of one half, 256 bytes side by side. (Lanes of
-  // 8 columns, 32 bytes apart, cost 5 us a tile more: 64x4096x7168 16.4 us against 11.3 of the plain call.)
-  const int c = (threadIdx.x % 32) * 4;                          // first of four columns of H in the tile
-  const uint32_t off = (uint32_t)((c / 64) * 128 + c % 64) * 4;  // their gate partials; up 64 columns on
-  for (int r = rank + (int)(threadIdx.x / 32) * S; r < rows; r += threads / 32 * S) {
+  // Neighbouring lanes read neighbouring float4, HC/4 of them side by side. (Lanes of 8 columns, 32 bytes
+  // apart, cost 4 us a tile more: 64x4096x7168 16.4 us instead of 12.3.)
+  constexpr int kLanes = HC / 2;                                    // lanes a row
+  const int c = (threadIdx.x % kLanes) * 4;                         // first of four columns of H in the tile
+  const uint32_t off = (uint32_t)((c / HC) * 2 * HC + c % HC) * 4;  // their gate partials; up HC columns on
+  for (int r = rank + (int)(threadIdx.x / kLanes) * S; r < rows; r += threads / kLanes * S) {
     const uint32_t at = part + r * row_bytes + off;
     // every peer's two float4 are requested before the first add
     float4 gs[kMaxClusterCtas], us[kMaxClusterCtas];
@@ -165,7 +165,7 @@ __device__ __forceinline__ void gated_cluster_reduce(const GatedExt& e, void* H,
       if (s < S) {
         const uint32_t peer = cluster_map(at, (uint32_t)s);
         gs[s] = ld_cluster_v4(peer);
-        us[s] = ld_cluster_v4(peer + 256);
+        us[s] = ld_cluster_v4(peer + HC * 4);
       }
     float4 g4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u4 = g4;
 #pragma unroll
@@ -181,7 +181,7 @@ __device__ __forceinline__ void gated_cluster_reduce(const GatedExt& e, void* H,
         continue;   // a padding row (or another group's): left untouched
       }
     }
-    gated_store4<OUT_F32>(e, H, I, (size_t)a_row + r, n_blk * 128 + c, g4, u4);
+    gated_store4<OUT_F32>(e, H, I, (size_t)a_row + r, n_blk * 2 * HC + c, g4, u4);
   }
 }
 

@@ -429,10 +429,10 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 // and the 128 up rows I + 128·n ..; the epilogue pairs the two halves and stores
 // H = silu(gate)·up, 128 columns of the [G·M_max, I] output per tile.
 //
-// kSwigluGated (dense and contiguous forms in one instantiation, BN = 256; the separate dense one spilled
-// 84 bytes into its K loop: 145 us instead of 119 on 4096x4096x7168): the same 256 B rows, but ordered gate 0..63, up
-// 0..63, gate 64..127, up 64..127 in the tile (four 64-row boxes), so that each epilogue warp owns
-// matching gate and up columns and the two warps of a quadrant exchange nothing.
+// kSwigluGated (dense and contiguous forms in one instantiation; the separate dense one spilled 84 bytes into
+// its K loop: 145 us instead of 115 on 4096x4096x7168): the tile's B rows are BN/4 gate, BN/4 up, BN/4 gate,
+// BN/4 up rows (four boxes), so that each epilogue warp owns matching gate and up columns and the two warps
+// of a quadrant exchange nothing.
 
 template <int BN, int EPI_COLS, int STAGES, int NBUF, Mode MODE, bool OUT_F32, int SWIGLU>
 __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
   // issuers would share a stage, and one could wait for the use two phases ahead while the barrier
   // is still one phase behind: the parity test would pass early and the ring would lose step.
   static_assert(STAGES % 2 == 0 && NBUF % 2 == 0, "stage and TMEM-buffer counts must be even (two issuers)");
-  static_assert(!SWIGLU || (BN == 256 && EPI_COLS == 128), "fused SwiGLU: BN = 256");
+  static_assert(!SWIGLU || kGated || (BN == 256 && EPI_COLS == 128), "fused SwiGLU: BN = 256");
+  static_assert(BN == 2 * EPI_COLS, "two column groups of epilogue warps");
   static_assert(!SWIGLU || (kGated ? MODE == kContiguous : MODE == kMasked),
                 "fused SwiGLU: masked; gated: contiguous, which with m_indices null is dense");
 
@@ -590,12 +591,12 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
                 tma_load_2d(&tmB, sa + Plan::kABytes + h * 128 * 128, &full_bar[s], n, k, policy_b);
               }
             } else if constexpr (kGated) {
-              // (B's tensor map box is 64 rows)
-              const int gate_row = tile.g * p.N + tile.n_blk * 128;
+              // (B's tensor map box is BN/4 rows)
+              const int gate_row = tile.g * p.N + tile.n_blk * (BN / 2);
 #pragma unroll
               for (int h = 0; h < 4; ++h)
-                tma_load_2d(&tmB, sa + Plan::kABytes + h * 64 * 128, &full_bar[s], kb * 128,
-                            gate_row + (h & 1) * p.swiglu_i + (h >> 1) * 64, policy_b);
+                tma_load_2d(&tmB, sa + Plan::kABytes + h * (BN / 4) * 128, &full_bar[s], kb * 128,
+                            gate_row + (h & 1) * p.swiglu_i + (h >> 1) * (BN / 4), policy_b);
             } else if constexpr (SWIGLU) {
               // gate rows 128·n .. and up rows I + 128·n .. (B's tensor map box is 128 rows)
               const int gate_row = tile.g * p.N + tile.n_blk * 128;
@@ -763,7 +764,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       __syncwarp();
       // The first column of this warp (as a row of B: fused SwiGLU puts the up rows at I + 128·n).
       auto first_col = [&](int n_blk) -> int {
-        if constexpr (kGated) return n_blk * 128;   // the gate's scale block; the up scales are I/128 blocks on
+        if constexpr (kGated) return n_blk * (BN / 2);   // the gate's scale block; the up scales are I/128 blocks on
         return SWIGLU ? (cgrp ? p.swiglu_i : 0) + n_blk * 128 : n_blk * BN + cgrp * EPI_COLS;
       };
       // Only what the K loop needs is live across it; the rest of the tile is re-read afterwards.
@@ -810,7 +811,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         if (active) {
           const uint32_t taddr =
               tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(b * BN + cgrp * EPI_COLS);
-          float2 scale2 = make_float2(0.0f, 0.0f);
+          float2 scale2 = make_float2(0.0f, 0.0f), scale2b = scale2;   // of chunks c and c + 1
           // two 32-column loads in flight per wait; the buffer is released as soon as the last
           // pair has landed in registers, before its FMAs
 #pragma unroll
@@ -829,9 +830,11 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
               const float scale = sa_cur * sb_cur;
               scale2 = make_float2(scale, scale);
             }
-            if (kGated && c == 2) {   // columns 64..127 of the warp are up columns
+            scale2b = scale2;
+            if (kGated && c + 1 >= kChunks / 2) {   // the second half of the warp's columns are up columns
               const float scale = sa_cur * su_cur;
-              scale2 = make_float2(scale, scale);
+              scale2b = make_float2(scale, scale);
+              if (c >= kChunks / 2) scale2 = scale2b;
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -841,7 +844,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               acc2[(c + 1) * 16 + j] = __ffma2_rn(make_float2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1])),
-                                                  scale2, acc2[(c + 1) * 16 + j]);
+                                                  scale2b, acc2[(c + 1) * 16 + j]);
             }
           }
         } else {
@@ -1065,8 +1068,9 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       if (!__any_sync(0xffffffffu, write_row)) continue;   // no row of this warp is stored
       const bool use_tma = (MODE == kDense) || __all_sync(0xffffffffu, write_row);
       if constexpr (kGated) {
-        gated_epilogue<OUT_F32>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32, tile.n_blk * 128 + cgrp * 64,
-                                write_row, use_tma, staging, Plan::kStagingBox, store_count, lane);
+        gated_epilogue<OUT_F32, EPI_COLS / 2>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32,
+                                              tile.n_blk * (BN / 2) + cgrp * (EPI_COLS / 2), write_row, use_tma, staging,
+                                              Plan::kStagingBox, store_count, lane);
         continue;
       }
       if (!col_exists) continue;
@@ -1172,8 +1176,8 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         const int c4 = threadIdx.x % kVec;
         const int n = n_blk * BN + c4 * 4;
         if constexpr (kGated) {
-          gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
-                                        g, p.m_indices, p.status, kStatusBadGroup);
+          gated_cluster_reduce<OUT_F32, EPI_COLS / 2>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row,
+                                                      rows, n_blk, g, p.m_indices, p.status, kStatusBadGroup);
         } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {
           float4 tot = cluster_sum_v4(part + r * kRowBytes + c4 * 16, S);

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       if (!__any_sync(0xffffffffu, write_row)) continue;   // no row of this warp is stored
       const bool use_tma = (MODE == kDense) || __all_sync(0xffffffffu, write_row);
       if constexpr (kGated) {
-        gated_epilogue<OUT_F32>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32, tile.n_blk * 128 + cgrp * 64,
+        gated_epilogue<OUT_F32, 64>(ext, &tmD, p.D, p.swiglu_i, acc, tile.a_row + quad * 32, tile.n_blk * 128 + cgrp * 64,
                                 write_row, use_tma, staging, Plan::kStagingBox, store_count, lane);
         continue;
       }
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         const int c4 = threadIdx.x % kVec;
         const int n = n_blk * BN + c4 * 4;
         if constexpr (kGated) {
-          gated_cluster_reduce<OUT_F32>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
+          gated_cluster_reduce<OUT_F32, 64>(ext, p.D, p.swiglu_i, part, kRowBytes, S, rank, R::kEpiThreads, a_row, rows, n_blk,
                                         g, p.m_indices, p.status, kStatusBadGroup);
         } else
         for (int r = rank + (threadIdx.x / kVec) * S; r < rows; r += kRowsPerPass * S) {

@@ -41,7 +41,7 @@ cudaError_t launch_kgrouped(const LaunchArgs& a);
 // The masked form fused with SwiGLU (block_n 256, FP32-scale kernel); fp8_h: H as FP8 codes and
 // 1x128-group scales.
 cudaError_t launch_masked_swiglu(const LaunchArgs& a, bool fp8_h = false);
-// The gated projection (dense and contiguous forms, block_n 256), FP32 scales and block-scaled.
+// The gated projection (dense and contiguous forms), FP32 scales and block-scaled (block_n 256).
 cudaError_t launch_gated(const LaunchArgs& a);
 cudaError_t launch_bs_gated(const LaunchArgs& a);
 // The block-scaled kernel for packed UE8M0 scales (block_n is always 256).
