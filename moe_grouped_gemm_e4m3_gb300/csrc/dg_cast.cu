@@ -74,36 +74,47 @@ __device__ __forceinline__ void put_scale_last(void* base, size_t line, int kb, 
   }
 }
 
-__device__ __forceinline__ uint32_t codes4(const float* v, float f0, float f1, float f2, float f3) {
-  return e4m3x2_satfinite(__fmul_rn(v[0], f0), __fmul_rn(v[1], f1)) |
-         (e4m3x2_satfinite(__fmul_rn(v[2], f2), __fmul_rn(v[3], f3)) << 16);
-}
-
-__device__ __forceinline__ void put_codes8(uint8_t* p, const float (&v)[8], const float (&f)[8]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, f[0], f[1], f[2], f[3]), codes4(v + 4, f[4], f[5], f[6], f[7]));
-}
-
-__device__ __forceinline__ void put_codes8(uint8_t* p, const float (&v)[8], float f) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(codes4(v, f, f, f, f), codes4(v + 4, f, f, f, f));
-}
-
-// The maxima of eight lines over 16 lanes, lane c of them getting line c % 8: at each of three steps a lane
-// passes on the half of its lines that its partner keeps (8 shuffles; reducing line by line takes 32).
-__device__ __forceinline__ float max8_over_16(const float (&v)[8], int c) {
-  float a[4], b[2];
+// Eight codes of eight values, the products two a instruction (each rounded by itself).
+__device__ __forceinline__ void put_codes8(uint8_t* p, const float2 (&v)[4], const float2 (&f)[4]) {
+  uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float keep = c & 1 ? v[2 * k + 1] : v[2 * k], pass = c & 1 ? v[2 * k] : v[2 * k + 1];
-    a[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 1));
+    const float2 x = __fmul2_rn(v[k], f[k]);
+    w[k] = e4m3x2_satfinite(x.x, x.y);
   }
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+__device__ __forceinline__ void put_codes8(uint8_t* p, const float2 (&v)[4], float f) {
+  const float2 two = make_float2(f, f), all[4] = {two, two, two, two};
+  put_codes8(p, v, all);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float2 (&v)[4]) {
+  v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+  v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+  v[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+  v[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
+}
+
+// The maxima of LINES (a power of two) lines over 16 lanes, lane c of them getting line c % LINES: while there
+// are several, a lane passes on the half that its partner keeps (8 shuffles for eight lines; reducing line by
+// line takes 32).
+template <int LINES>
+__device__ __forceinline__ float max_over_16(const float (&v)[LINES], int c, int bit = 1) {
+  if constexpr (LINES == 1) {
+    float m = v[0];
+    for (; bit < 16; bit <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, bit));
+    return m;
+  } else {
+    float half[LINES / 2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float keep = c & 2 ? a[2 * k + 1] : a[2 * k], pass = c & 2 ? a[2 * k] : a[2 * k + 1];
-    b[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 2));
+    for (int k = 0; k < LINES / 2; ++k) {
+      const float keep = c & bit ? v[2 * k + 1] : v[2 * k], pass = c & bit ? v[2 * k] : v[2 * k + 1];
+      half[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, bit));
+    }
+    return max_over_16<LINES / 2>(half, c, bit << 1);
   }
-  const float keep = c & 4 ? b[1] : b[0], pass = c & 4 ? b[0] : b[1];
-  const float m = fmaxf(keep, __shfl_xor_sync(0xffffffffu, pass, 4));
-  return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
 }
 
 // Asynchronous copy of 16 bytes to this thread's own place in shared memory (zeros if !live). No other thread
@@ -139,24 +150,37 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
   const int Mb = (M + 127) / 128, Nb = (N + 127) / 128, ldm = (M + 3) / 4 * 4;
   const bool across = f.q_col || f.q_blk;   // anything beside rows
 
-  auto fetch = [&](int tile, int buf) {
+  // This thread's rows' indices (0 without m_indices): loaded a tile before the copies that need them are
+  // issued, and not looked at until then, so that nothing waits for them.
+  auto load_rows = [&](int tile, int (&idx)[kCastRows]) {
+#pragma unroll
+    for (int i = 0; i < kCastRows; ++i) {
+      const int row = tile / Nb % Mb * 128 + t / 16 + i * kCastStep;
+      idx[i] = m_indices && tile < tiles && row < M ? __ldg(m_indices + row) : 0;
+    }
+  };
+  auto fetch = [&](int tile, int buf, const int (&idx)[kCastRows]) {
     const int nb = tile % Nb, mb = tile / Nb % Mb, g = tile / Nb / Mb;
     const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
     const uint16_t* src = x + ((size_t)g * M + row0) * N + col;
 #pragma unroll
     for (int i = 0; i < kCastRows; ++i) {
-      const int row = row0 + i * kCastStep;
-      const bool live = row < M && col < N && (!m_indices || __ldg(m_indices + row) >= 0);
+      const bool live = row0 + i * kCastStep < M && col < N && idx[i] >= 0;
       copy_16(&sh.next[buf][i][t], live ? src + (size_t)i * kCastStep * N : x, live);
     }
   };
 
   int buf = 0;
-  if (blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  const int step = (int)gridDim.x;
+  int idx[kCastRows];
+  load_rows(blockIdx.x, idx);
+  fetch(blockIdx.x, 0, idx);
   commit_copies();
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, buf ^ 1);
+  load_rows((int)blockIdx.x + step, idx);
+  for (int tile = blockIdx.x; tile < tiles; tile += step, buf ^= 1) {
+    if (tile + step < tiles) fetch(tile + step, buf ^ 1, idx);
     commit_copies();
+    load_rows(tile + 2 * step, idx);
     wait_copies<1>();
     const int nb = tile % Nb, mb = tile / Nb % Mb, g = tile / Nb / Mb;
     const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
@@ -178,7 +202,7 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
       }
       float fac;
       uint32_t scale;
-      group_scale<UE>(max8_over_16(m, cg), fac, scale);   // of row cg % 8
+      group_scale<UE>(max_over_16(m, cg), fac, scale);   // of row cg % 8
       // the rows past M up to align4(M) get the filler
       const int row = row0 + cg * kCastStep;
       if (cg < 8 && row < ldm)
@@ -186,7 +210,7 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
 #pragma unroll
       for (int i = 0; i < kCastRows; ++i) {
         const float fi = __shfl_sync(0xffffffffu, fac, i, 16);
-        float v[8];
+        float2 v[4];
         unpack8(raw[i], v);
         if (row0 + i * kCastStep < M && col_live) put_codes8(f.q_row + off0 + (size_t)i * kCastStep * N, v, fi);
       }
@@ -225,12 +249,10 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
       if (lane == 0) sh.top[warp] = __uint_as_float(block);
     }
     __syncthreads();
-    float cf[8], bf = 0.0f;
-    {
-      const float4 a = *reinterpret_cast<const float4*>(&sh.factor[cg * 8]), b = *reinterpret_cast<const float4*>(&sh.factor[cg * 8 + 4]);
-      cf[0] = a.x; cf[1] = a.y; cf[2] = a.z; cf[3] = a.w;
-      cf[4] = b.x; cf[5] = b.y; cf[6] = b.z; cf[7] = b.w;
-    }
+    float2 cf[4];
+    float bf = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) cf[k] = *reinterpret_cast<const float2*>(&sh.factor[cg * 8 + 2 * k]);
     if (f.q_blk) {
       uint32_t scale;
       group_scale<UE>(fmaxf(fmaxf(sh.top[0], sh.top[1]), fmaxf(sh.top[2], sh.top[3])), bf, scale);
@@ -242,7 +264,7 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
 #pragma unroll
     for (int i = 0; i < kCastRows; ++i) {
       if (row0 + i * kCastStep >= M || !col_live) continue;
-      float v[8];
+      float2 v[4];
       unpack8(raw[i], v);
       const size_t off = off0 + (size_t)i * kCastStep * N;
       if (f.q_col) put_codes8(f.q_col + off, v, cf);
@@ -250,6 +272,19 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
     }
   }
   wait_copies<0>();
+}
+
+// 1/(1 + e^-x) from the hardware's base-2 exponential and reciprocal, subnormals flushed (1 + e^-x is at least
+// 1, and infinite, with the quotient 0, below about -88). Relative error below 1e-5 where |x| < 88.
+__device__ __forceinline__ float2 gate_sigmoid(float2 x) {
+  const float2 y = __fmul2_rn(x, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  float2 e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+  e = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+  return s;
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -286,12 +321,21 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
   const bool drop = d.threshold != 0;
   const Philox gen = drop ? Philox(d.rng) : Philox();
 
-  auto fetch = [&](int tile, int buf) {
+  // This thread's rows' indices (0 without m_indices): loaded a tile before the copies that need them are
+  // issued, and not looked at until then, so that nothing waits for them.
+  auto load_rows = [&](int tile, int (&idx)[kGateRows]) {
+#pragma unroll
+    for (int i = 0; i < kGateRows; ++i) {
+      const int row = tile / nI * 128 + t / 16 + i * kGateStep;
+      idx[i] = m_indices && tile < tiles && row < M ? __ldg(m_indices + row) : 0;
+    }
+  };
+  auto fetch = [&](int tile, int buf, const int (&idx)[kGateRows]) {
     const int row0 = tile / nI * 128 + t / 16, col = tile % nI * 128 + cg * 8;
 #pragma unroll
     for (int i = 0; i < kGateRows; ++i) {
       const int row = row0 + i * kGateStep;
-      const bool live = row < M && (!m_indices || __ldg(m_indices + row) >= 0);
+      const bool live = row < M && idx[i] >= 0;
       const size_t at = live ? (size_t)row * I + col : 0, at2 = live ? (size_t)row * 2 * I + col : 0;
       copy_16(&sh.next[buf][3 * i][t], dh + at, live);
       copy_16(&sh.next[buf][3 * i + 1][t], gu + at2, live);
@@ -300,48 +344,57 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
   };
 
   int buf = 0;
-  if (blockIdx.x < tiles) fetch(blockIdx.x, 0);
+  const int step = (int)gridDim.x;
+  int idx[kGateRows];
+  load_rows(blockIdx.x, idx);
+  fetch(blockIdx.x, 0, idx);
   commit_copies();
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    if (tile + (int)gridDim.x < tiles) fetch(tile + gridDim.x, buf ^ 1);
+  load_rows((int)blockIdx.x + step, idx);
+  for (int tile = blockIdx.x; tile < tiles; tile += step, buf ^= 1) {
+    if (tile + step < tiles) fetch(tile + step, buf ^ 1, idx);
     commit_copies();
+    load_rows(tile + 2 * step, idx);
     wait_copies<1>();
     const int nb = tile % nI, mb = tile / nI;
     const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
-    float v[2][kGateRows][8], h[BLOCKS ? kGateRows : 1][8];   // dG and dU; H
-    float line[8], cmax[2][8], hmax = 0.0f;                    // row maxima of dG, then of dU; column maxima
+    float2 v[2][kGateRows][4], h[BLOCKS ? kGateRows : 1][4];   // dG and dU; H
+    float line[2 * kGateRows], cmax[2][8], hmax = 0.0f;         // row maxima of dG, then of dU; column maxima
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int j = 0; j < 8; ++j) cmax[a][j] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kGateRows; ++i) {
-      float dt[8], g[8], u[8];
+      float2 dt[4], g[4], u[4];
       unpack8(sh.next[buf][3 * i][t], dt);
       unpack8(sh.next[buf][3 * i + 1][t], g);
       unpack8(sh.next[buf][3 * i + 2][t], u);
       uint4 w = make_uint4(0, 0, 0, 0);
       if (drop) {
         w = gen(((uint64_t)(row0 + i * kGateStep) * I + col) / 8);
-        dropout8(dt, w, d.threshold, d.scale);
+        dropout8(reinterpret_cast<float(&)[8]>(dt), w, d.threshold, d.scale);
       }
-      line[i] = line[4 + i] = 0.0f;
+      line[i] = line[kGateRows + i] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-g[j])), gs = g[j] * s;
-        const float dg = dt[j] * u[j] * s * (1.0f + g[j] * (1.0f - s)), du = dt[j] * gs;
-        v[0][i][j] = dg;
-        v[1][i][j] = du;
-        line[i] = fmaxf(line[i], fabsf(dg));
-        line[4 + i] = fmaxf(line[4 + i], fabsf(du));
-        cmax[0][j] = fmaxf(cmax[0][j], fabsf(dg));
-        cmax[1][j] = fmaxf(cmax[1][j], fabsf(du));
-        if constexpr (BLOCKS) h[i][j] = gs * u[j];
+      for (int k = 0; k < 4; ++k) {
+        const float2 s = gate_sigmoid(g[k]), gs = __fmul2_rn(g[k], s);
+        // dg = t·u·(s + gs·(1 - s)), du = t·gs
+        const float2 one = make_float2(1.0f, 1.0f), minus = make_float2(-1.0f, -1.0f);
+        v[0][i][k] = __fmul2_rn(__fmul2_rn(dt[k], u[k]), __ffma2_rn(gs, __ffma2_rn(s, minus, one), s));
+        v[1][i][k] = __fmul2_rn(dt[k], gs);
+        if constexpr (BLOCKS) h[i][k] = __fmul2_rn(gs, u[k]);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const float x = fabsf(v[a][i][k].x), y = fabsf(v[a][i][k].y);
+          line[a * kGateRows + i] = fmaxf(fmaxf(line[a * kGateRows + i], x), y);
+          cmax[a][2 * k] = fmaxf(cmax[a][2 * k], x);
+          cmax[a][2 * k + 1] = fmaxf(cmax[a][2 * k + 1], y);
+        }
       }
       if constexpr (BLOCKS) {
-        if (drop) dropout8(h[i], w, d.threshold, d.scale);
+        if (drop) dropout8(reinterpret_cast<float(&)[8]>(h[i]), w, d.threshold, d.scale);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) hmax = fmaxf(hmax, fabsf(h[i][j]));
+        for (int k = 0; k < 4; ++k) hmax = fmaxf(fmaxf(hmax, fabsf(h[i][k].x)), fabsf(h[i][k].y));
       }
     }
     const size_t off0 = (size_t)row0 * 2 * I + col;
@@ -349,15 +402,15 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
     if (f.q_row) {
       float fac;
       uint32_t scale;
-      group_scale<UE>(max8_over_16(line, cg), fac, scale);   // of row cg % 4, of dG (cg % 8 < 4) or dU
-      const int row = row0 + (cg & 3) * kGateStep;
-      if (cg < 8 && row < ldm)
-        put_scale_major<UE>(f.s_row, 0, nb + (cg >> 2) * nI, 2 * nI, ldm, row, row < M ? scale : (UE ? 127u : 0u));
+      group_scale<UE>(max_over_16(line, cg), fac, scale);   // lines: dG's rows, then dU's
+      const int row = row0 + cg % kGateRows * kGateStep;
+      if (cg < 2 * kGateRows && row < ldm)
+        put_scale_major<UE>(f.s_row, 0, nb + cg / kGateRows * nI, 2 * nI, ldm, row, row < M ? scale : (UE ? 127u : 0u));
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int i = 0; i < kGateRows; ++i) {
-          const float fi = __shfl_sync(0xffffffffu, fac, a * 4 + i, 16);
+          const float fi = __shfl_sync(0xffffffffu, fac, a * kGateRows + i, 16);
           if (row0 + i * kGateStep < M) put_codes8(f.q_row + off0 + (size_t)i * kGateStep * 2 * I + a * I, v[a][i], fi);
         }
     }
@@ -401,8 +454,9 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
     if (f.q_col) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const float4 p = *reinterpret_cast<const float4*>(&sh.factor[a][cg * 8]), q = *reinterpret_cast<const float4*>(&sh.factor[a][cg * 8 + 4]);
-        const float cf[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+        float2 cf[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cf[k] = *reinterpret_cast<const float2*>(&sh.factor[a][cg * 8 + 2 * k]);
 #pragma unroll
         for (int i = 0; i < kGateRows; ++i)
           if (row0 + i * kGateStep < M) put_codes8(f.q_col + off0 + (size_t)i * kGateStep * 2 * I + a * I, v[a][i], cf);

@@ -21,15 +21,7 @@ __device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 16-byte aligned, all eight present. (Plain loads: the output may be the input itself.)
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4*>(p), v);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+// 16-byte aligned, all eight present.
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]),
                                             round_bf16x2(v[4], v[5]), round_bf16x2(v[6], v[7]));
