@@ -239,7 +239,13 @@ struct Config {
   int raster_m;
 };
 
-Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false) {
+// gated: the gated projection, whose split-K exchange in clusters is priced anew (us: 0.8 + 0.2 a split for 64-column
+// tiles, 2.4 + 0.4 for 128-column ones, 1.4 + 0.4 block-scaled): the CTAs of a tile share the reduction, so it
+// grows slowly with the splits. With M = 333, 2I = 2304, K = 2064, block-scaled: 1/2/3/4/5 splits 15.6/13.8/12.6/12.9/13.1 us;
+// FP32 scales: 64-column tiles 1/2 splits 11.5/10.5, 128-column 3/5 splits 12.6/13.0. The plain calls keep their linear
+// term: another split count would change their bits.
+Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false,
+                     bool gated = false) {
   // Cost model calibrated on GB300 (sm_103a), times in microseconds per CTA:
   //  * compute: one K-block (BM=128, BK=128) costs ~0.55 (BN=256) or ~0.50 (BN=128: an N=128 MMA
   //    takes as long as an N=256 one, for half the work);
@@ -283,7 +289,9 @@ Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool 
       const double t_mem = (a_kb + b_kb) / (cta_gbs * 1e3);
       const double t_kb = t_compute > t_mem ? t_compute : t_mem;
       const double waves = (double)((units + num_sms - 1) / num_sms);
-      double t = waves * (kps * t_kb + kTileUs) + (se > 1 ? t_red * se : 0.0);
+      const double t_gated = block_scaled ? 1.4 + 0.4 * se : (cand_bn == 256 ? 2.4 + 0.4 * se : 0.8 + 0.2 * se);
+      const double t_exchange = gated && se <= kMaxClusterSplit ? t_gated : t_red * se;
+      double t = waves * (kps * t_kb + kTileUs) + (se > 1 ? t_exchange : 0.0);
       const double t_hbm = bytes / (kHbmGBs * 1e3);
       if (t < t_hbm) t = t_hbm;
       if (t < best_t - 1e-9) { best_t = t; best_s = se; bn = cand_bn; }
@@ -508,7 +516,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                                                dg::StreamArgs{stream, sms, pdl_setting()});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
-  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled);
+  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
   // (the gated kernels have the footprint of the plain ones: the same cluster capacities)
   if (!swiglu) fit_cluster_splits(cfg, mode, K, block_scaled, out_f32);
   const int d_cols = swiglu || gated ? N / 2 : N;   // width of D (fused SwiGLU: H has I = N/2 columns)
