@@ -187,6 +187,41 @@ def _check(status: int):
         raise DGError(status, load().dg_last_error_string().decode(errors="replace"))
 
 
+class _NoBind:
+    """Stands in for the short path where it is not built: every call goes through the checks below."""
+    gated = dense = contiguous = k_grouped = backward = cast = dropout = staticmethod(lambda *a: None)
+
+
+@functools.cache
+def _bind():
+    """The compiled short path (csrc/dg_bind.cpp): checks the arguments of a call and makes it, or returns None where
+    something is not as it should be; the checks below then say what."""
+    import importlib.machinery
+    import importlib.util
+
+    import torch
+    load()
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_dgbind", _build_mod.BIND)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_dgbind", _build_mod.BIND, loader=loader))
+        loader.exec_module(mod)
+    except (ImportError, OSError):
+        return _NoBind
+    same = mod.version() == torch.__version__.split("+")[0]
+    return mod if same and mod.load(_build_mod.LIB) else _NoBind
+
+
+# The variants of the entry points as the short path numbers them: bit 0 FP32 output, bit 1 packed UE8M0 scales.
+@functools.cache
+def _variant(name):
+    return (1 if name.endswith("_f32") else 0) + (2 if "_ue8m0" in name else 0)
+
+
+def _raw(stream):
+    """A stream as the short path takes it: None (the current one) or its number."""
+    return None if stream is None else int(getattr(stream, "cuda_stream", stream))
+
+
 # The helpers below run on every call, so each has a short path for well-formed arguments (a few attribute
 # reads, about 0.3 us a tensor) and leaves the words of an error to a second look.
 
@@ -303,6 +338,9 @@ def _d_types(f32: bool):
     return (torch.float32,) if f32 else (torch.bfloat16, torch.int16, torch.uint16)
 
 
+_NT = ("dg_fp8_gemm_nt", "dg_fp8_gemm_nt_f32", "dg_fp8_gemm_nt_ue8m0", "dg_fp8_gemm_nt_ue8m0_f32")
+
+
 def _dense_shapes(name, A, B):
     """(M, N, K) of a dense call: A [M, K], B [N, K] (or [1, N, K])."""
     a, b = _shape(A, "A"), _shape(B, "B")
@@ -327,6 +365,12 @@ def _check_scales_2d(name, sA, sB, M, N, K):
 
 
 def _dense(name, f32, A, sA, B, sB, D, stream):
+    if name in _NT and getattr(A, "ndim", 0) == 2 and getattr(B, "ndim", 0) == 2:
+        (M, K), N = A.shape, B.shape[0]
+        status = _bind().dense(_variant(name), A, sA, B, sB, D, M, N, K, _raw(stream))
+        if status is not None:
+            _check(status)
+            return D
     M, N, K = _dense_shapes(name, A, B)
     _check_scales_2d(name, sA, sB, M, N, K)
     q, st = _fp8_types(), _scale_types(name)
@@ -357,6 +401,10 @@ def dg_fp8_gemm_nt_noalloc(A, sA, B, sB, D, stream=None):
 
 
 def _contig(name, f32, A, sA, B, sB, m_indices, D, stream):
+    status = _bind().contiguous(_variant(name), A, sA, B, sB, m_indices, D, _raw(stream))
+    if status is not None:
+        _check(status)
+        return D
     a, b = _shape(A, "A"), _shape(B, "B")
     if len(a) != 2 or len(b) != 3:
         raise ValueError(f"contiguous layout: A must be [M_total, K] and B [G, N, K], got {list(a)} and {list(b)}")
@@ -439,10 +487,15 @@ def dg_fp8_gemm_nt_ue8m0_acc_f32(A, sA, B, sB, C, D, stream=None):
 
 # The layouts' names: the first letter says how A is stored (n: [M, K], t: [K, M]), the second how
 # B is stored (t: [N, K], n: [K, N]).
+_LAYOUT_VARIANTS = {"nn": 4, "tn": 8, "tt": 12}
 _LAYOUTS = {"nn": (False, True), "tn": (True, True), "tt": (True, False)}
 
 
 def _dense_layout(name, f32, A, sA, B, sB, D, M, N, K, stream):
+    status = _bind().dense(_variant(name) + _LAYOUT_VARIANTS[name[12:14]], A, sA, B, sB, D, M, N, K, _raw(stream))
+    if status is not None:
+        _check(status)
+        return D
     a_t, b_n = _LAYOUTS[name[len("dg_fp8_gemm_"):len("dg_fp8_gemm_") + 2]]
     M, N, K = int(M), int(N), int(K)
     nks, q, st = _scale_k(name, K), _fp8_types(), _scale_types(name)
@@ -508,6 +561,10 @@ def dg_fp8_gemm_tt_ue8m0_f32(A, sA, B, sB, D, M, N, K, stream=None):
 
 
 def _k_grouped(name, f32, A, sA, B, sB, k_offsets, D, stream):
+    status = _bind().k_grouped(_variant(name), A, sA, B, sB, k_offsets, D, _raw(stream))
+    if status is not None:
+        _check(status)
+        return D
     a, b, o = _shape(A, "A"), _shape(B, "B"), _shape(k_offsets, "k_offsets")
     if len(a) != 2 or len(b) != 2 or len(o) != 1 or o[0] < 1:
         raise ValueError(f"K-grouped: A must be [K_total, M], B [K_total, N], k_offsets [G + 1]; got "
@@ -564,8 +621,12 @@ def _bf16():
 
 
 def _gated(name, f32, A, sA, B, sB, m_indices, H, GU, rng, p, stream):
-    a, b = _shape(A, "A"), _shape(B, "B")
     grouped = "contiguous" in name
+    status = _bind().gated(_variant(name) + 4 * grouped, A, sA, B, sB, m_indices, H, GU, rng, p, _raw(stream))
+    if status is not None:
+        _check(status)
+        return H
+    a, b = _shape(A, "A"), _shape(B, "B")
     if len(a) != 2 or len(b) != (3 if grouped else 2):
         raise ValueError(f"gated projection: A must be [M, K] and B {'[G, 2I, K]' if grouped else '[2I, K]'}, "
                          f"got {list(a)} and {list(b)}")
@@ -631,6 +692,10 @@ def dg_fp8_grouped_contiguous_swiglu_ue8m0_f32(A, sA, B, sB, m_indices, H, GU=No
 
 
 def _contig_nn(name, f32, A, sA, B, sB, m_indices, D, stream):
+    status = _bind().contiguous(_variant(name) + 4, A, sA, B, sB, m_indices, D, _raw(stream))
+    if status is not None:
+        _check(status)
+        return D
     a, b = _shape(A, "A"), _shape(B, "B")
     if len(a) != 2 or len(b) != 3:
         raise ValueError(f"contiguous NN: A must be [M_total, K] and B [G, K, N], got {list(a)} and {list(b)}")
@@ -666,6 +731,10 @@ def dg_fp8_grouped_contiguous_nn_ue8m0_f32(A, sA, B, sB, m_indices, D, stream=No
 
 
 def _swiglu_backward(name, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream):
+    status = _bind().backward(_variant(name) >> 1, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, _raw(stream))
+    if status is not None:
+        _check(status)
+        return dGUr, dGUc
     h = _shape(dH, "dH")
     if len(h) != 2:
         raise ValueError(f"dH must be [M, I], got {list(h)}")
@@ -699,6 +768,10 @@ def dg_swiglu_backward_fp8_ue8m0(dH, GU, dGUr=None, sR=None, dGUc=None, sC=None,
 
 
 def _cast(name, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream):
+    status = _bind().cast(_variant(name) >> 1, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, _raw(stream))
+    if status is not None:
+        _check(status)
+        return
     x = _shape(X, "X")
     if len(x) not in (2, 3):
         raise ValueError(f"X must be [M, N] or [G, M, N], got {list(x)}")
@@ -731,6 +804,10 @@ def dg_dropout(X, Y, rng, p, R=None, stream=None):
     """Y = R + dropout(X) (R optional), bfloat16 or float32 tensors of one shape; Y may be X or R. rng is a CUDA
     int64 tensor {seed, offset}; the mask is a function of it, p and the flat index. Backward: the same
     call on the gradient, without R."""
+    status = _bind().dropout(X, R, Y, rng, p, _raw(stream))
+    if status is not None:
+        _check(status)
+        return Y
     f32 = getattr(X, "dtype", None) in _f32()
     dt, shape = _f32() if f32 else _bf16(), _shape(X, "X")
     pX, pR, pY, prng = _pointers((X, "X", dt, shape), (R, "R?", dt, shape), (Y, "Y", dt, shape), (rng, "rng?", _rng_types(), (2,)))

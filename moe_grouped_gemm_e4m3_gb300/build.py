@@ -1,16 +1,19 @@
 """Builds libdg.so (the sm_103a kernels and the C ABI of include/dg.h) in-tree with nvcc.
 
 The translation units are compiled in parallel (one per GEMM form plus the API layer) and linked
-into ``moe_grouped_gemm_e4m3_gb300/libdg.so``. Rebuilds only when a source or header is newer
-than the library. Usage: ``python -m moe_grouped_gemm_e4m3_gb300.build [--force]``.
+into ``moe_grouped_gemm_e4m3_gb300/libdg.so``. ``_dgbind.so``, the binding's short path, is compiled beside it with the
+host compiler against the installed torch's headers; if that fails, a message is printed and the binding
+works without it. Rebuilds only when a source or header is newer than the library. Usage: ``python -m moe_grouped_gemm_e4m3_gb300.build [--force]``.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdg.so")
+BIND = os.path.join(PKG, "_dgbind.so")
+BIND_SRC = os.path.join(CSRC, "dg_bind.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC,
@@ -47,7 +52,49 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _bind_current() -> bool:
+    newest = max(os.path.getmtime(BIND_SRC), os.path.getmtime(os.path.abspath(__file__)))
+    return os.path.exists(BIND) and os.path.getmtime(BIND) >= newest
+
+
+def _start_bind():
+    """The compilation of the binding's short path (None: no torch to compile against)."""
+    spec = importlib.util.find_spec("torch")
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if spec is None or not cxx:
+        return None
+    torch_dir = spec.submodule_search_locations[0]
+    inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(torch_dir, "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC"] + ["-I" + i for i in inc] + [BIND_SRC, "-o", tmp, "-L" + lib] + \
+        ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-Wl,-rpath," + lib]
+    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish_bind(started) -> None:
+    if started is None:
+        return
+    tmp, proc = started
+    out, _ = proc.communicate()
+    if proc.returncode == 0:
+        os.replace(tmp, BIND)
+    else:
+        sys.stderr.write("the binding's short path did not compile (calls will check their arguments in Python):\n" +
+                         out.decode(errors="replace")[-2000:])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    bind = None if not force and _bind_current() else _start_bind()
+    try:
+        return _build_lib(force, verbose)
+    finally:
+        _finish_bind(bind)
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

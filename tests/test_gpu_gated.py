@@ -488,3 +488,25 @@ def test_training_chain(dg, scales, grouped):
 def _captured(dg, b, out):
     _fn(dg, "dg_swiglu_backward_fp8", b.scales)(b.dH, b.GU, m_indices=b.m_indices, rng=b.rng, p=b.p, **out)
     return out
+
+
+def test_the_binding_s_two_paths_make_the_same_call(dg, monkeypatch):
+    """Arguments checked by the compiled short path and by Python: the same bits."""
+    prob, back = Problem(200, 128, 272, "fp32"), Backward(200, 128, "ue8m0", p=0.1)
+    x = torch.randn(200, 144, device="cuda").bfloat16()
+    rng = R.rng_tensor(SEED, OFFSET)
+
+    def calls():
+        out = list(prob.run(dg, False, p=0.1, rng=rng)) + list(back.run(dg).values())
+        q, s, y = torch.zeros(200, 144, dtype=torch.uint8, device="cuda"), torch.zeros(2, 200, device="cuda"), torch.empty_like(x)
+        dg.dg_cast_fp8(x, Xr=q, sR=s)
+        dg.dg_dropout(x, y, rng, 0.25, R=x)
+        d = torch.empty(200, 256, dtype=torch.bfloat16, device="cuda")
+        dg.dg_fp8_gemm_nt(prob.A, prob.sA, prob.B, prob.sB, d)
+        return out + [q, s, y, d]
+
+    first = calls()
+    assert dg._bind() is not dg._NoBind, "the short path is not built"
+    monkeypatch.setattr(dg, "_bind", lambda: dg._NoBind)
+    for a, b in zip(first, calls()):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
