@@ -552,7 +552,8 @@ dg_status dg_transform_sf_into_ue8m0_a(const float* sA, int32_t* sA_packed, int 
 dg_status dg_transform_sf_a_into_mn_major(const float* sA_rows, float* sA, int G, int M, int K, dg_stream_t stream);
 dg_status dg_transform_sf_into_ue8m0_b(const float* sB, int32_t* sB_packed, int G, int N, int K, dg_stream_t stream);
 
-/* Programmatic dependent launch for every GEMM call. With on != 0, each kernel is launched with
+/* Programmatic dependent launch for every GEMM call. (The elementwise calls of the gated block's training, and its
+   gated projection and contiguous NN product where they are at most one wave of tiles, are always launched this way.) With on != 0, each kernel is launched with
    programmatic stream serialization: it may start while the kernel ahead of it in the stream is
    still running, set up its shared memory, barriers and tensor memory, and then wait
    (griddepcontrol.wait) until that kernel has completed and its writes are visible, before it

@@ -513,7 +513,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   const int sms = effective_sms(*st);
   if (gated && mode == dg::kDense && rows <= dg::kFewTokens) {   // the weights' read is the whole cost
     const cudaError_t e = dg::launch_gated_few(A, sA, B, sB, D, gated->GU, gated->drop, rows, N / 2, K, out_f32, block_scaled,
-                                               dg::StreamArgs{stream, sms, pdl_setting()});
+                                               dg::StreamArgs{stream, sms, true});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
   Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
@@ -659,7 +659,10 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   a.out_f32 = out_f32;
   a.grid = cfg.grid;
   a.stream = stream;
-  a.pdl = pdl_setting();
+  // The gated projection and the contiguous NN form start early by themselves where they are at most one wave
+  // (333x2304x2064, back to back: 14.3 us in plain order, 12.6 so; 8192x4096x7168 over 8 experts, 7 waves: 215 and 221).
+  const bool one_wave = (long long)cfg.tiles * cfg.splits <= sms;
+  a.pdl = pdl_setting() || (one_wave && (gated || (mode == dg::kContiguous && b_mn)));
   if (print_configs()) {
     static const char* names[3] = {"dense", "contiguous", "masked"};
     std::fprintf(stderr, "[dg] %s%s%s%s rows=%d N=%d K=%d G=%d: BM=128 BN=%d stages=%d splits=%d%s grid=%d tiles=%d\n",
@@ -794,7 +797,10 @@ dg_status stream_args(dg_stream_t stream, dg::StreamArgs* out) {
   if (s != DG_OK) return s;
   out->stream = static_cast<cudaStream_t>(stream);
   out->sms = effective_sms(*st);
-  out->pdl = pdl_setting();
+  // Always launched for an early start: the kernels wait (griddepcontrol) before their first access to memory,
+  // and an elementwise call's launch is a good part of its time (64x2112 with residual, back to back: 4.1 us in plain
+  // order, 2.7 so; 8.7M FP32 14.2 and 11.4).
+  out->pdl = true;
   return DG_OK;
 }
 
