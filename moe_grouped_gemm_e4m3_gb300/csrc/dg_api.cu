@@ -516,7 +516,21 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
                                                dg::StreamArgs{stream, sms, true});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
-  Config cfg = choose_config(mode, rows, N, K, mode == dg::kDense ? 1 : G, sms, block_scaled, gated != nullptr);
+  const int groups = mode == dg::kDense ? 1 : G;
+  Config cfg = choose_config(mode, rows, N, K, groups, sms, block_scaled, gated != nullptr);
+  // A small gated projection with packed scales runs on the FP32-scale kernel's 64-column tiles, which read the
+  // words as they are, where those are chosen for FP32 scales and make one wave: the block-scaled kernel has
+  // 128-column tiles only. Measured (us, 64-column tiles / block-scaled): 333x2304x2064 10.3 / 12.6, 128x2048x2048 8.6 / 10.9,
+  // 32x1024x1024 6.2 / 7.1, 700x768x7168 13.3 / 15.2, 1000x1280x1360 9.8 / 12.8, 64x4096x7168 12.0 / 12.4, 500x1536x4096 13.1 / 12.7.
+  bool packed_on_fp32 = false;
+  if (gated && block_scaled) {
+    const Config narrow = choose_config(mode, rows, N, K, groups, sms, false, true);
+    if (narrow.block_n == 128 && (long long)narrow.tiles * narrow.splits <= sms) {
+      cfg = narrow;
+      packed_on_fp32 = true;
+      block_scaled = false;
+    }
+  }
   // (the gated kernels have the footprint of the plain ones: the same cluster capacities)
   if (!swiglu) fit_cluster_splits(cfg, mode, K, block_scaled, out_f32);
   const int d_cols = swiglu || gated ? N / 2 : N;   // width of D (fused SwiGLU: H has I = N/2 columns)
@@ -546,7 +560,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   p.num_n_blocks = swiglu ? d_cols / 128 : ceil_div(N, cfg.block_n);   // (gated: I over block_n/2 columns of H)
   p.swiglu_i = swiglu || gated ? d_cols : 0;
   p.flags = (a_mn ? dg::kFlagAMN : 0) | (b_mn ? dg::kFlagBMN : 0) | (accumulate ? dg::kFlagAccumulate : 0) |
-            wait_limit_flags();
+            (packed_on_fp32 ? dg::kFlagUe8m0 : 0) | wait_limit_flags();
   p.num_splits = cfg.splits;
   p.kb_per_split = cfg.kb_per_split;
   p.num_tiles = mode == dg::kMasked ? 0 : cfg.tiles;   // masked: counted on the device

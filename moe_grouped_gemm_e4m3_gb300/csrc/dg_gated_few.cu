@@ -14,7 +14,6 @@
 // kernel 12.8. From 17 tokens on (64 at 2I = 4096, K = 7168: 17 us) the tiled kernel takes over: 16 tokens cost 10.3
 // us here and 13.9 there, and each further 8 tokens read the activations once more per 16 weight rows.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "dg_launch.h"
@@ -59,13 +58,11 @@ __device__ __forceinline__ void mma_16x8x32(float (&c)[4], uint32_t a0, uint32_t
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The scale of K-block kb from its 32 bits: FP32, or byte kb % 4 of a packed word through the hardware's
-// E8M0 conversion (selects for the codes 0 and 255 cost 1.5 us of 8.4 at 1x4096x7168).
+// The scale of K-block kb from its 32 bits: FP32, or byte kb % 4 of a packed word.
 template <bool UE>
 __device__ __forceinline__ float scale_value(uint32_t bits, int kb) {
   if constexpr (!UE) return __uint_as_float(bits);
-  const __nv_bfloat162_raw v = __nv_cvt_e8m0x2_to_bf162raw((__nv_fp8x2_storage_t)((bits >> (8 * (kb & 3))) & 0xFFu));
-  return __uint_as_float((uint32_t)v.x << 16);
+  return ue8m0_value(bits >> (8 * (kb & 3)));
 }
 
 template <bool UE, bool OUT_F32, int NT>

@@ -98,6 +98,8 @@ constexpr int kFlagClusterSplit = 0x8;
 // which TMA multicasts into both CTAs' shared memory, so each SM pulls a third less from L2 per
 // K-block. Every MMA commit then releases the stage in both CTAs (empty barriers count 2).
 constexpr int kFlagPairB = 0x10;
+// The gated projection's 64-column tiles (BN = 128): the scales are packed UE8M0 words (kUe8m0Capable).
+constexpr int kFlagUe8m0 = 0x20;
 // The SWIGLU template argument: 0 no SwiGLU; kSwiglu H = silu(gate)·up stored as BF16/FP32;
 // kSwigluFp8 H quantised to FP8 for the down projection: each row's 128 columns of a tile (one 1x128
 // group) get the codes e4m3_rne(clamp(h · (448/amax), ±448)) and the dequantisation scale amax/448
@@ -446,6 +448,8 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
   constexpr bool kGated = SWIGLU == kSwigluGated;
   constexpr bool kClusterCapable = (MODE == kDense || MODE == kContiguous) && (!SWIGLU || kGated);
   constexpr int kChunks = EPI_COLS / 32;   // 32-column TMEM loads per epilogue thread and K-block
+  // whether this instantiation also reads its scales as packed UE8M0 words (the gated projection's small shapes)
+  constexpr bool kUe8m0Capable = kGated && BN == 128;
   constexpr uint32_t kTmemCols = NBUF * BN;
   static_assert(kTmemCols == 128 || kTmemCols == 256 || kTmemCols == 512, "TMEM allocation: power of two");
   constexpr uint32_t kIdesc = make_idesc_e4m3_f32(128, BN);
@@ -776,7 +780,8 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         row_live = row_in_tile < stash[6];
         const bool col_live = n_col < p.N;
         sa_ptr = p.sA + (MODE == kMasked ? (size_t)g * p.nkb * p.ldsa : 0) + stash[1] * 128 + row_in_tile;
-        sb_ptr = p.sB + ((size_t)(MODE == kKGrouped ? 0 : g) * p.nnb + (col_live ? n_col / 128 : 0)) * p.nkb;
+        const int sb_cols = kUe8m0Capable && (p.flags & kFlagUe8m0) ? (p.nkb + 3) / 4 : p.nkb;
+        sb_ptr = p.sB + ((size_t)(MODE == kKGrouped ? 0 : g) * p.nnb + (col_live ? n_col / 128 : 0)) * sb_cols;
         // Warps with no row or no column in range only keep the TMEM handshake going.
         active = col_live && __any_sync(0xffffffffu, row_live);
       }
@@ -788,12 +793,26 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       // step kb, before its wait, and moved into place at the end of it, so a global load has the
       // step's wait, TMEM loads and FMAs to land. (A K-grouped tile can have an empty K range: it
       // stores zeros and reads no scale.)
-      auto fetch_sa = [&](int kb) -> float {
-        return (active && row_live && kb < kb_end) ? __ldg(sa_ptr + (size_t)kb * p.ldsa) : 0.0f;
+      const bool ue = kUe8m0Capable && (p.flags & kFlagUe8m0);
+      const int nkq = (p.nkb + 3) / 4;
+      // (packed: the word that holds K-block kb, its byte picked at the use)
+      auto e8m0 = [&](const float* words, size_t at, int kb) -> float {
+        return ue8m0_value(__ldg(reinterpret_cast<const uint32_t*>(words) + at) >> (8 * (kb & 3)));
       };
-      auto fetch_sb = [&](int kb) -> float { return (active && kb < kb_end) ? __ldg(sb_ptr + kb) : 0.0f; };
+      auto fetch_sa = [&](int kb) -> float {
+        if (!(active && row_live && kb < kb_end)) return 0.0f;
+        if (kUe8m0Capable && ue) return e8m0(sa_ptr, (size_t)(kb / 4) * p.ldsa, kb);
+        return __ldg(sa_ptr + (size_t)kb * p.ldsa);
+      };
+      auto fetch_sb = [&](int kb) -> float {
+        if (!(active && kb < kb_end)) return 0.0f;
+        if (kUe8m0Capable && ue) return e8m0(sb_ptr, (size_t)(kb / 4), kb);
+        return __ldg(sb_ptr + kb);
+      };
       auto fetch_su = [&](int kb) -> float {   // gated: the up columns' scale
-        return (active && kb < kb_end) ? __ldg(sb_ptr + (size_t)(p.swiglu_i / 128) * p.nkb + kb) : 0.0f;
+        if (!(active && kb < kb_end)) return 0.0f;
+        if (kUe8m0Capable && ue) return e8m0(sb_ptr, (size_t)(p.swiglu_i / 128) * nkq + kb / 4, kb);
+        return __ldg(sb_ptr + (size_t)(p.swiglu_i / 128) * p.nkb + kb);
       };
       float sa_cur = fetch_sa(kb_begin), sb_cur = fetch_sb(kb_begin);
       float su_cur = 0.0f, su_nxt = 0.0f;

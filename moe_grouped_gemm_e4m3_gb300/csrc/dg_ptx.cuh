@@ -151,6 +151,13 @@ __device__ __forceinline__ uint32_t e4m3x2_satfinite(float first, float second) 
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(first, second), __NV_SATFINITE, __NV_E4M3);
 }
 
+// The value of the E8M0 code in a word's low byte: 2^(code - 127), through the hardware's conversion (code 0
+// is a subnormal, 255 NaN; selects for the two cost 1.5 us of 8.4 in the few-token gated projection).
+__device__ __forceinline__ float ue8m0_value(uint32_t word) {
+  const __nv_bfloat162_raw v = __nv_cvt_e8m0x2_to_bf162raw((__nv_fp8x2_storage_t)(word & 0xFFu));
+  return __uint_as_float((uint32_t)v.x << 16);
+}
+
 // Largest cluster the split-K exchange uses (the portable cluster size).
 constexpr int kMaxClusterCtas = 8;
 

@@ -128,14 +128,15 @@ class Problem:
 
 @pytest.mark.parametrize("scales", SCALES)
 @pytest.mark.parametrize("M,I,K", [(1, 128, 16), (1, 256, 1040), (3, 384, 144), (8, 128, 7168), (9, 256, 528), (16, 128, 80), (17, 128, 144), (64, 128, 640), (127, 128, 128),
-                                   (128, 256, 272), (129, 128, 1024), (300, 384, 528), (257, 1024, 2064)])
+                                   (128, 256, 272), (129, 128, 1024), (300, 384, 528), (257, 1024, 2064), (300, 1920, 3600)])   # the last: 128-column tiles, K split
 def test_dense(dg, M, I, K, scales):
     Problem(M, I, K, scales).check(dg)
 
 
 @pytest.mark.parametrize("scales", SCALES)
 @pytest.mark.parametrize("sizes,I,K", [([0, 1, 127, 128], 128, 272), ([130, 0, 64], 256, 144), ([5], 384, 1040),
-                                       ([300, 7, 0, 0, 129], 128, 512)])
+                                       ([300, 7, 0, 0, 129], 128, 512),
+                                       ([700, 0, 1300, 100], 1024, 272), ([140, 0, 40], 1920, 3600)])   # 128-column tiles
 def test_contiguous(dg, sizes, I, K, scales):
     Problem(None, I, K, scales, sizes=sizes, holes=[2] if sizes[0] > 4 else []).check(dg)
 
@@ -148,6 +149,8 @@ def test_dropout_in_the_epilogue(dg, scales, p):
     Problem(40, 256, 1040, scales).check(dg, p)           # K split in a cluster
     Problem(300, 128, 272, scales).check(dg, p)
     Problem(None, 128, 272, scales, sizes=[100, 0, 200], holes=[50]).check(dg, p)
+    Problem(None, 1024, 272, scales, sizes=[700, 0, 1300, 100], holes=[50]).check(dg, p)
+    Problem(300, 1920, 3600, scales).check(dg, p)
 
 
 @pytest.mark.parametrize("scales", SCALES)
@@ -190,7 +193,8 @@ def test_bad_group_index_is_flagged(dg, scales):
 
 @pytest.mark.parametrize("scales", SCALES)
 def test_timeout_and_recovery(dg, scales):
-    for prob in (Problem(300, 256, 1024, scales), Problem(20, 256, 2048, scales), Problem(None, 128, 256, scales, sizes=[100, 60])):
+    for prob in (Problem(300, 256, 1024, scales), Problem(300, 1920, 3600, scales), Problem(1280, 2048, 272, scales),
+                 Problem(20, 256, 2048, scales), Problem(None, 128, 256, scales, sizes=[100, 60])):
         ref, _ = prob.run(dg, False)
         prev = dg.dg_set_wait_limit_us(0)
         try:
