@@ -290,6 +290,8 @@ def run_ours(args, rank, world, local):
 
     torch.cuda.set_device(local)
     dg.load()
+    # plain stream order: a launch bounded by events must not start inside the flush before it
+    dg.dg_set_pdl(os.environ.get("DG_PDL", "0") not in ("", "0"))
     pg = None
     if world > 1:
         import torch.distributed as tdist
@@ -734,6 +736,8 @@ def run_all_configs(args):
     import dg_inputs
     import moe_grouped_gemm_e4m3_gb300 as dg
     dg.load()
+    # plain stream order: a launch bounded by events must not start inside the flush before it
+    dg.dg_set_pdl(os.environ.get("DG_PDL", "0") not in ("", "0"))
     peaks = load_peaks()
     fp8_peak = 2.0 * peaks["bf16_tflops"]
     dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()

@@ -552,21 +552,21 @@ dg_status dg_transform_sf_into_ue8m0_a(const float* sA, int32_t* sA_packed, int 
 dg_status dg_transform_sf_a_into_mn_major(const float* sA_rows, float* sA, int G, int M, int K, dg_stream_t stream);
 dg_status dg_transform_sf_into_ue8m0_b(const float* sB, int32_t* sB_packed, int G, int N, int K, dg_stream_t stream);
 
-/* Programmatic dependent launch for every GEMM call. (The elementwise calls of the gated block's training, and its
-   gated projection and contiguous NN product where they are at most one wave of tiles, are always launched this way.) With on != 0, each kernel is launched with
-   programmatic stream serialization: it may start while the kernel ahead of it in the stream is
-   still running, set up its shared memory, barriers and tensor memory, and then wait
-   (griddepcontrol.wait) until that kernel has completed and its writes are visible, before it
-   reads any input. Each kernel also signals, once its own setup is done, that the next kernel may
-   start (griddepcontrol.launch_dependents). Back-to-back calls on one stream then hide part of
-   each launch's setup. A kernel that follows one of these in the stream starts early only if it
-   was itself launched for it. Results are the same bits either way. on = 0 (the default; the
-   environment variable DG_PDL=1 sets the initial value to on) launches in plain stream order.
-   Returns the previous value (0 or 1). The pages name a PDL switch among the library's utilities,
-   set_pdl / get_pdl ("DeepGEMM: İnce ölçeklendirmeyle temiz ve verimli FP8 GEMM çekirdekleri",
+/* Programmatic dependent launch. A kernel launched with programmatic stream serialization may start while the
+   kernel ahead of it in the stream is still running, set up its shared memory, barriers and tensor memory, and
+   then wait (griddepcontrol.wait) until that kernel has completed and its writes are visible, before it
+   reads any input. Each kernel also signals, once its own setup is done, that the next kernel may start
+   (griddepcontrol.launch_dependents). Back-to-back calls on one stream then hide part of each launch's
+   setup. A kernel that follows one of these in the stream starts early only if it was itself launched for it.
+   Results are the same bits either way.
+   on > 0: every GEMM and elementwise call is launched so; on = 0: every call in plain stream order; on < 0 (the
+   default): the calls of at most one wave of tiles, and the elementwise ones, where it gains most. The
+   environment variable DG_PDL=1 or 0 sets the initial value to on or off. Returns the previous value, 1 for on
+   and 0 for off or the default. The pages name a PDL switch among the library's utilities, set_pdl / get_pdl
+   ("DeepGEMM: İnce ölçeklendirmeyle temiz ve verimli FP8 GEMM çekirdekleri",
    tr.news.hada.io/topic?id=19459, § "Yardımcı fonksiyonlar ve ortam değişkenleri"). */
 int dg_set_pdl(int on);
-/* The current setting of dg_set_pdl (0 or 1). */
+/* Whether every call is launched so: 1, or 0 (off, or the default). */
 int dg_get_pdl(void);
 
 /* Split-K inside thread-block clusters (dense and contiguous forms, either scale form). When a call

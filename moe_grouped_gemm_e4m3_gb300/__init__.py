@@ -968,11 +968,12 @@ def dg_set_pair_b(on: bool) -> bool:
     return bool(load().dg_set_pair_b(1 if on else 0))
 
 
-def dg_set_pdl(on: bool) -> bool:
-    """Launch every GEMM with programmatic dependent launch (it may start before the previous kernel
-    in the stream ends, and waits for that kernel's results before reading its inputs), or not (the
-    default). Returns the previous value; results are bit-identical either way."""
-    return bool(load().dg_set_pdl(1 if on else 0))
+def dg_set_pdl(on) -> bool:
+    """Launch every call with programmatic dependent launch (it may start before the previous kernel in the stream
+    ends, and waits for that kernel's results before reading its inputs): True always, False never, None (the
+    default) where a call is elementwise or at most one wave of tiles. Returns whether it was always on; results
+    are bit-identical either way."""
+    return bool(load().dg_set_pdl(-1 if on is None else (1 if on else 0)))
 
 
 def dg_get_pdl() -> bool:

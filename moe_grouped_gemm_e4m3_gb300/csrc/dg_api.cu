@@ -61,23 +61,32 @@ bool cluster_split_setting() {
   return v != 0;
 }
 
-// Pairs of CTAs sharing B tiles through TMA multicast (dense and contiguous, FP32 scales, BN = 256,
-// no split-K): off unless DG_PAIR_B=1 or dg_set_pair_b(1). Measured on GB300, the FP32-scale kernel
-// is bound by its per-K-block TMEM round trip, not by the L2 feed that pairing relieves, and paired
-// launches lose the tail split: 4096x7168x16384 397 us single, 419 us paired.
-// Programmatic dependent launch: off unless DG_PDL=1 or dg_set_pdl(1).
+// Programmatic dependent launch: 0 never, 1 always (DG_PDL, dg_set_pdl), or by default where a launch is at
+// most one wave of tiles or elementwise. Between kernels in plain stream order the GPU took 2 us steps back to back: the
+// gated projection of 333x2304x2064 14.3 us in plain order and 12.6 started early, the backward of 200x1024x1024 (three
+// calls) 23.6 and 17.3. Over several waves it gains nothing (8192x4096x7168 over 8 experts 215 and 221).
+enum Pdl : int { kPdlOff = 0, kPdlOn = 1, kPdlShort = 2 };
 std::atomic<int> g_pdl{-1};
-bool pdl_setting() {
+int pdl_setting() {
   int v = g_pdl.load();
   if (v < 0) {
     const char* e = std::getenv("DG_PDL");
     int expected = -1;
-    g_pdl.compare_exchange_strong(expected, (e && std::atoi(e) != 0) ? 1 : 0);
+    g_pdl.compare_exchange_strong(expected, !e ? kPdlShort : (std::atoi(e) != 0 ? kPdlOn : kPdlOff));
     v = g_pdl.load();
   }
-  return v != 0;
+  return v;
+}
+// Whether a launch of this many units of work on this many SMs may start early.
+bool early_start(long long units, int sms) {
+  const int v = pdl_setting();
+  return v == kPdlOn || (v == kPdlShort && units <= sms);
 }
 
+// Pairs of CTAs sharing B tiles through TMA multicast (dense and contiguous, FP32 scales, BN = 256,
+// no split-K): off unless DG_PAIR_B=1 or dg_set_pair_b(1). Measured on GB300, the FP32-scale kernel
+// is bound by its per-K-block TMEM round trip, not by the L2 feed that pairing relieves, and paired
+// launches lose the tail split: 4096x7168x16384 397 us single, 419 us paired.
 std::atomic<int> g_pair_b{-1};
 bool pair_b_setting() {
   int v = g_pair_b.load();
@@ -513,7 +522,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   const int sms = effective_sms(*st);
   if (gated && mode == dg::kDense && rows <= dg::kFewTokens) {   // the weights' read is the whole cost
     const cudaError_t e = dg::launch_gated_few(A, sA, B, sB, D, gated->GU, gated->drop, rows, N / 2, K, out_f32, block_scaled,
-                                               dg::StreamArgs{stream, sms, true});
+                                               dg::StreamArgs{stream, sms, early_start(0, sms)});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
   const int groups = mode == dg::kDense ? 1 : G;
@@ -673,10 +682,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   a.out_f32 = out_f32;
   a.grid = cfg.grid;
   a.stream = stream;
-  // The gated projection and the contiguous NN form start early by themselves where they are at most one wave
-  // (333x2304x2064, back to back: 14.3 us in plain order, 12.6 so; 8192x4096x7168 over 8 experts, 7 waves: 215 and 221).
-  const bool one_wave = (long long)cfg.tiles * cfg.splits <= sms;
-  a.pdl = pdl_setting() || (one_wave && (gated || (mode == dg::kContiguous && b_mn)));
+  a.pdl = early_start((long long)cfg.tiles * cfg.splits, sms);
   if (print_configs()) {
     static const char* names[3] = {"dense", "contiguous", "masked"};
     std::fprintf(stderr, "[dg] %s%s%s%s rows=%d N=%d K=%d G=%d: BM=128 BN=%d stages=%d splits=%d%s grid=%d tiles=%d\n",
@@ -783,7 +789,7 @@ dg_status run_k_grouped(bool out_f32, const uint8_t* A, const void* sA, const ui
   a.out_f32 = out_f32;
   a.grid = tiles < sms ? tiles : sms;
   a.stream = stream;
-  a.pdl = pdl_setting();
+  a.pdl = early_start(tiles, sms);
   if (print_configs())
     std::fprintf(stderr, "[dg] k-grouped%s%s G=%d M=%d N=%d K_total=%d: BM=128 BN=%d grid=%d tiles=%d\n",
                  block_scaled ? "/ue8m0" : "", out_f32 ? "/f32" : "", G, M, N, K_total, bn, a.grid, tiles);
@@ -811,10 +817,7 @@ dg_status stream_args(dg_stream_t stream, dg::StreamArgs* out) {
   if (s != DG_OK) return s;
   out->stream = static_cast<cudaStream_t>(stream);
   out->sms = effective_sms(*st);
-  // Always launched for an early start: the kernels wait (griddepcontrol) before their first access to memory,
-  // and an elementwise call's launch is a good part of its time (64x2112 with residual, back to back: 4.1 us in plain
-  // order, 2.7 so; 8.7M FP32 14.2 and 11.4).
-  out->pdl = true;
+  out->pdl = early_start(0, out->sms);   // (the kernels wait with griddepcontrol before their first access)
   return DG_OK;
 }
 
@@ -1309,12 +1312,12 @@ int dg_set_pair_b(int on) {
 }
 
 int dg_set_pdl(int on) {
-  const int prev = pdl_setting() ? 1 : 0;
-  g_pdl.store(on ? 1 : 0);
+  const int prev = pdl_setting() == kPdlOn ? 1 : 0;
+  g_pdl.store(on < 0 ? kPdlShort : (on ? kPdlOn : kPdlOff));
   return prev;
 }
 
-int dg_get_pdl(void) { return pdl_setting() ? 1 : 0; }
+int dg_get_pdl(void) { return pdl_setting() == kPdlOn ? 1 : 0; }
 
 int dg_set_cluster_split(int on) {
   const int prev = cluster_split_setting() ? 1 : 0;

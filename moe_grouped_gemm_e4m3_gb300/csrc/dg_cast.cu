@@ -296,42 +296,67 @@ __device__ __forceinline__ float2 gate_sigmoid(float2 x) {
 // columns 8·(t % 16).. of the tile's rows i·32 + t/16, i < 4. Persistent, with the next tile's inputs
 // copied ahead as above: one CTA of 512 threads an SM, since dG and dU stay in registers between their
 // maxima and their codes.
-constexpr int kGateThreads = 512, kGateRows = 4, kGateStep = 32;
+//
+// SPLIT > 1: a tile's rows are shared by a cluster of SPLIT CTAs (one tile a cluster), which exchange their
+// column maxima through distributed shared memory. For few tiles, where one CTA's arithmetic on a whole tile is most of
+// the call: 200x512 rows 5.6 us with SPLIT = 1.
+constexpr int kGateThreads = 512;
 
+template <int SPLIT>
+struct GatePlan {
+  static constexpr int kRows = 4 / SPLIT, kStep = 32;   // rows a thread, this many apart
+};
+
+template <int SPLIT>
 struct GateShared {
-  uint4 next[2][3 * kGateRows][kGateThreads];
+  uint4 next[2][3 * GatePlan<SPLIT>::kRows][kGateThreads];
   float part[2][kGateThreads / 32][128];   // each warp's column maxima of dG and dU
   float factor[2][128];
   float h_top[kGateThreads / 32];
   float h_factor;
+  float cta_top[2][128], cta_h_top;        // SPLIT > 1: this CTA's maxima, read by its peers
 };
 
-template <bool UE, bool BLOCKS>
+// The largest of a float at the same place of every CTA of a cluster of SPLIT.
+template <int SPLIT>
+__device__ __forceinline__ float cluster_max(const float* mine) {
+  uint32_t v[SPLIT], top = 0;
+#pragma unroll
+  for (int r = 0; r < SPLIT; ++r) v[r] = ld_cluster_u32(cluster_map(smem_u32(mine), (uint32_t)r));
+#pragma unroll
+  for (int r = 0; r < SPLIT; ++r) top = max(top, v[r]);   // magnitudes: ordered as integers
+  return __uint_as_float(top);
+}
+
+template <bool UE, bool BLOCKS, int SPLIT>
 __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const uint16_t* __restrict__ dh,
                                                                           const uint16_t* __restrict__ gu,
                                                                           const int32_t* __restrict__ m_indices,
                                                                           const Dropout d, const CastForms f,
                                                                           const CastForms f_h, int M, int I, int tiles) {
+  constexpr int kGateRows = GatePlan<SPLIT>::kRows, kGateStep = GatePlan<SPLIT>::kStep;
   extern __shared__ __align__(16) uint8_t smem[];
-  GateShared& sh = *reinterpret_cast<GateShared*>(smem);
+  GateShared<SPLIT>& sh = *reinterpret_cast<GateShared<SPLIT>*>(smem);
   griddep_wait();
   griddep_launch_dependents();
   const int t = threadIdx.x, cg = t % 16, warp = t / 32, lane = t % 32;
   const int nI = I / 128, Mb = (M + 127) / 128, ldm = (M + 3) / 4 * 4;
   const bool drop = d.threshold != 0;
   const Philox gen = drop ? Philox(d.rng) : Philox();
+  const int rank = SPLIT > 1 ? (int)(blockIdx.x % SPLIT) : 0, tile0 = (int)blockIdx.x / SPLIT;
+  const int t_row = rank * kGateRows * kGateStep + t / 16;   // this thread's first row in a tile
 
   // This thread's rows' indices (0 without m_indices): loaded a tile before the copies that need them are
   // issued, and not looked at until then, so that nothing waits for them.
   auto load_rows = [&](int tile, int (&idx)[kGateRows]) {
 #pragma unroll
     for (int i = 0; i < kGateRows; ++i) {
-      const int row = tile / nI * 128 + t / 16 + i * kGateStep;
+      const int row = tile / nI * 128 + t_row + i * kGateStep;
       idx[i] = m_indices && tile < tiles && row < M ? __ldg(m_indices + row) : 0;
     }
   };
   auto fetch = [&](int tile, int buf, const int (&idx)[kGateRows]) {
-    const int row0 = tile / nI * 128 + t / 16, col = tile % nI * 128 + cg * 8;
+    const int row0 = tile / nI * 128 + t_row, col = tile % nI * 128 + cg * 8;
 #pragma unroll
     for (int i = 0; i < kGateRows; ++i) {
       const int row = row0 + i * kGateStep;
@@ -344,19 +369,19 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
   };
 
   int buf = 0;
-  const int step = (int)gridDim.x;
+  const int step = (int)gridDim.x / SPLIT;
   int idx[kGateRows];
-  load_rows(blockIdx.x, idx);
-  fetch(blockIdx.x, 0, idx);
+  load_rows(tile0, idx);
+  fetch(tile0, 0, idx);
   commit_copies();
-  load_rows((int)blockIdx.x + step, idx);
-  for (int tile = blockIdx.x; tile < tiles; tile += step, buf ^= 1) {
+  load_rows(tile0 + step, idx);
+  for (int tile = tile0; tile < tiles; tile += step, buf ^= 1) {
     if (tile + step < tiles) fetch(tile + step, buf ^ 1, idx);
     commit_copies();
     load_rows(tile + 2 * step, idx);
     wait_copies<1>();
     const int nb = tile % nI, mb = tile / nI;
-    const int row0 = mb * 128 + t / 16, col = nb * 128 + cg * 8;
+    const int row0 = mb * 128 + t_row, col = nb * 128 + cg * 8;
     float2 v[2][kGateRows][4], h[BLOCKS ? kGateRows : 1][4];   // dG and dU; H
     float line[2 * kGateRows], cmax[2][8], hmax = 0.0f;         // row maxima of dG, then of dU; column maxima
 #pragma unroll
@@ -431,23 +456,35 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
       if (lane == 0) sh.h_top[warp] = __uint_as_float(top);
     }
     __syncthreads();   // (every thread has read the previous tile's factors by then)
+    const bool h_warp = BLOCKS && warp == 8;
+    float top = 0.0f;
+    if (t < 256) {
+#pragma unroll
+      for (int w = 0; w < kGateThreads / 32; ++w) top = fmaxf(top, sh.part[t / 128][w][t % 128]);
+    } else if (h_warp) {
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lane < kGateThreads / 32 ? sh.h_top[lane] : 0.0f)));
+    }
+    if constexpr (SPLIT > 1) {
+      if (t < 256) sh.cta_top[t / 128][t % 128] = top;
+      else if (h_warp && lane == 0) sh.cta_h_top = top;
+      cluster_sync_all();
+      if (t < 256) top = cluster_max<SPLIT>(&sh.cta_top[t / 128][t % 128]);
+      else if (h_warp) top = cluster_max<SPLIT>(&sh.cta_h_top);
+    }
     if (t < 256) {
       const int a = t / 128, c = t % 128;
-      float top = 0.0f, fac;
-#pragma unroll
-      for (int w = 0; w < kGateThreads / 32; ++w) top = fmaxf(top, sh.part[a][w][c]);
+      float fac;
       uint32_t scale;
       group_scale<UE>(top, fac, scale);
       sh.factor[a][c] = fac;
-      if (f.q_col) put_scale_major<UE>(f.s_col, 0, mb, Mb, 2 * I, a * I + nb * 128 + c, scale);
-    } else if (BLOCKS && warp == 8) {
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(lane < kGateThreads / 32 ? sh.h_top[lane] : 0.0f));
+      if (f.q_col && rank == 0) put_scale_major<UE>(f.s_col, 0, mb, Mb, 2 * I, a * I + nb * 128 + c, scale);
+    } else if (h_warp) {
       float fac;
       uint32_t scale;
-      group_scale<UE>(__uint_as_float(top), fac, scale);
+      group_scale<UE>(top, fac, scale);
       if (lane == 0) {
         sh.h_factor = fac;
-        put_scale_last<UE>(f_h.s_blk_t, nb, mb, Mb, scale);
+        if (rank == 0) put_scale_last<UE>(f_h.s_blk_t, nb, mb, Mb, scale);
       }
     }
     __syncthreads();
@@ -470,6 +507,8 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
     }
   }
   wait_copies<0>();
+  // no CTA of a cluster leaves while a peer may still read its maxima
+  if (SPLIT > 1 && (f.q_col || BLOCKS)) cluster_sync_all();
 }
 
 template <typename Kernel>
@@ -495,15 +534,15 @@ cudaError_t launch_cast_as(const uint16_t* x, const int32_t* m_indices, const Ca
                       N, tiles);
 }
 
-template <bool UE, bool BLOCKS>
+template <bool UE, bool BLOCKS, int SPLIT>
 cudaError_t launch_backward_as(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices, const Dropout& d,
                                const CastForms& dgu, const CastForms& h, int M, int I, const StreamArgs& s) {
   static bool done[64] = {};
-  const cudaError_t e = allow_smem(swiglu_backward_kernel<UE, BLOCKS>, sizeof(GateShared), done);
+  const cudaError_t e = allow_smem(swiglu_backward_kernel<UE, BLOCKS, SPLIT>, sizeof(GateShared<SPLIT>), done);
   if (e != cudaSuccess) return e;
-  const int tiles = (M + 127) / 128 * (I / 128);
-  return launch_plain(swiglu_backward_kernel<UE, BLOCKS>, tiles < s.sms ? tiles : s.sms, kGateThreads, sizeof(GateShared), s, dh,
-                      gu, m_indices, d, dgu, h, M, I, tiles);
+  const int tiles = (M + 127) / 128 * (I / 128), most = s.sms / SPLIT;
+  return launch_plain(swiglu_backward_kernel<UE, BLOCKS, SPLIT>, (tiles < most ? tiles : most) * SPLIT, kGateThreads,
+                      sizeof(GateShared<SPLIT>), s, dh, gu, m_indices, d, dgu, h, M, I, tiles);
 }
 
 }  // namespace
@@ -516,9 +555,17 @@ cudaError_t launch_cast(const uint16_t* x, const int32_t* m_indices, const CastF
 cudaError_t launch_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices,
                                    const Dropout& d, const CastForms& dgu, const CastForms& h, int M, int I,
                                    bool ue8m0, const StreamArgs& s) {
-  auto go = [&](auto kernel) { return kernel(dh, gu, m_indices, d, dgu, h, M, I, s); };
-  if (h.q_blk) return ue8m0 ? go(launch_backward_as<true, true>) : go(launch_backward_as<false, true>);
-  return ue8m0 ? go(launch_backward_as<true, false>) : go(launch_backward_as<false, false>);
+  auto go = [&](auto launch, const StreamArgs& with) { return launch(dh, gu, m_indices, d, dgu, h, M, I, with); };
+  // few tiles: four CTAs on each, while every cluster gets SMs of its own
+  const long long tiles = ((long long)M + 127) / 128 * (I / 128);
+  if (4 * tiles <= s.sms) {
+    StreamArgs four = s;
+    four.cluster = 4;
+    if (h.q_blk) return ue8m0 ? go(launch_backward_as<true, true, 4>, four) : go(launch_backward_as<false, true, 4>, four);
+    return ue8m0 ? go(launch_backward_as<true, false, 4>, four) : go(launch_backward_as<false, false, 4>, four);
+  }
+  if (h.q_blk) return ue8m0 ? go(launch_backward_as<true, true, 1>, s) : go(launch_backward_as<false, true, 1>, s);
+  return ue8m0 ? go(launch_backward_as<true, false, 1>, s) : go(launch_backward_as<false, false, 1>, s);
 }
 
 }  // namespace dg

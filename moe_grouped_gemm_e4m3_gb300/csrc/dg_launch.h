@@ -58,12 +58,13 @@ cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int 
                              cudaStream_t stream);
 // A's scales row-major [G][M][nkb] -> MN-major [G][nkb][ldsa] (rows m >= M zero).
 cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, cudaStream_t stream);
-// What the elementwise kernels' launches need: the stream, the SMs they may fill, and whether they may
-// start before the previous kernel of the stream ends (dg_set_pdl).
+// What the elementwise kernels' launches need: the stream, the SMs they may fill, whether they may start
+// before the previous kernel of the stream ends (they wait for it with griddepcontrol), and the cluster size.
 struct StreamArgs {
   cudaStream_t stream;
   int sms;
   bool pdl;
+  int cluster = 1;
 };
 // Y = R + dropout(X) over n elements, BF16 or FP32; r may be null (dg_dropout.cu).
 cudaError_t launch_dropout(const void* x, const void* r, void* y, bool f32, const Dropout& d, long long n,
@@ -101,11 +102,22 @@ cudaError_t launch_plain(void (*kernel)(Params...), int grid, int threads, size_
   cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = s.stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = s.pdl ? 1 : 0;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (s.cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)s.cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (s.pdl) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
