@@ -666,6 +666,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       // buffers and stages, so the order in which the two threads issue them does not matter;
       // each commit covers only its own thread's MMAs.
       const uint32_t me = (uint32_t)(warp - R::kMmaWarp);
+      const bool lead = elect_one();
       const bool a_mn = (p.flags & kFlagAMN) != 0, b_mn = (p.flags & kFlagBMN) != 0;
       const uint32_t a_addr0 = smem_u32(smem);
       const uint64_t adesc0 = a_mn ? make_sw128_mnmajor_desc(a_addr0, 128 * 128) : make_sw128_kmajor_desc(a_addr0);
@@ -683,23 +684,24 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         const uint32_t nk = (uint32_t)(tile.kb1 - tile.kb0);
-        // Lane 0 runs this issuer's K-blocks of the tile on its own (no warp-wide step per K-block).
-        int ok = 1;
-        if (lane == 0) {
-          for (uint32_t g = acc_it + ((me - acc_it) & 1u); g < acc_it + nk; g += 2) {
-            const int s = (int)(g % STAGES);
-            const uint32_t ph = (g / STAGES) & 1;
-            const int b = (int)(g % NBUF);
-            const uint32_t aph = (g / NBUF) & 1;
-            // the stage's data first (normally there long before), then the TMEM buffer, whose
-            // release by the epilogue is the round trip this wait is on
-            ok = mbar_wait(&full_bar[s], ph, abort_flag, p.status, p.flags) &&
-                 mbar_wait(&tempty_bar[b], aph ^ 1, abort_flag, p.status, p.flags);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t soff = (uint64_t)((s * Plan::kStageBytes) >> 4);
-            const uint64_t adesc = adesc0 + soff, bdesc = bdesc0 + soff;
-            const uint32_t d_tmem = tmem_base + (uint32_t)(b * BN);
+        // The whole warp walks the K-blocks and one elected lane issues, so that the operands' values are the same in
+        // every lane and sit in uniform registers, where the MMA takes them from.
+        bool ok = true;
+        for (uint32_t g = acc_it + ((me - acc_it) & 1u); g < acc_it + nk; g += 2) {
+          const int s = (int)(g % STAGES);
+          const uint32_t ph = (g / STAGES) & 1;
+          const int b = (int)(g % NBUF);
+          const uint32_t aph = (g / NBUF) & 1;
+          // the stage's data first (normally there long before), then the TMEM buffer, whose
+          // release by the epilogue is the round trip this wait is on
+          ok = mbar_wait(&full_bar[s], ph, abort_flag, p.status, p.flags) &&
+               mbar_wait(&tempty_bar[b], aph ^ 1, abort_flag, p.status, p.flags);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t soff = (uint64_t)((s * Plan::kStageBytes) >> 4);
+          const uint64_t adesc = adesc0 + soff, bdesc = bdesc0 + soff;
+          const uint32_t d_tmem = tmem_base + (uint32_t)(b * BN);
+          if (lead) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               mma_e4m3(d_tmem, adesc + a_step * k, bdesc + b_step * k, idesc, k > 0 ? 1u : 0u);
@@ -709,15 +711,15 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
             else
               mma_commit(&empty_bar[s]);
             mma_commit(&tfull_bar[b]);
-            last_b = b;
-            last_ph = aph;
           }
+          last_b = b;
+          last_ph = aph;
         }
         acc_it += nk;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lane == 0 && last_b >= 0) {
+      if (!alive && lead && last_b >= 0) {
         // Abandoned: wait for the MMAs this thread issued before TMEM is freed.
         const uint32_t a = smem_u32(&tfull_bar[last_b]);
         const uint64_t t0 = global_timer_ns();

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       // ---------------------------------------------------------------- block-scaled MMA issuer
       uint32_t it = 0, sf_it = 0, tile_it = 0;
       bool alive = true, issued_any = false;
+      const bool lead = elect_one();
       // An operand stored MN-major (the NN/TN/TT layouts) is read with an MN-major descriptor: one
       // K=32 step is +32 rows of 128 bytes (+256 in the >>4 address field) instead of +32 bytes.
       const bool a_mn = (p.flags & kFlagAMN) != 0, b_mn = (p.flags & kFlagBMN) != 0;
@@ -248,8 +249,10 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
         const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
-        int ok = 1;
-        if (lane == 0) {
+        // The whole warp walks the K-blocks and one elected lane issues, so that the operands' values are the same in
+        // every lane and sit in uniform registers, where the MMA takes them from.
+        bool ok = true;
+        {
           // the epilogue has loaded the previous tile's accumulator
           ok = mbar_wait(acc_empty_bar, (tile_it & 1) ^ 1, abort_flag, p.status, p.flags);
           tc_fence_after();
@@ -275,27 +278,30 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
             const uint32_t idesc = idesc_with_sf_id(idesc_layout, (uint32_t)(kb & 3));
             const uint32_t sfa = tmem_base + kSfCol0 + slot * kSfSlotCols;
             const uint32_t sfb = sfa + kSfbOff;
+            const bool last_of_word = (kb & 3) == 3 || kb + 1 == tile.kb1;
+            if (lead) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              // K-major: +32 bytes along K inside the 128-byte swizzled row (+2 in the >>4 field)
-              mma_e4m3_block_scaled(tmem_base, adesc + a_step * k, bdesc + b_step * k, idesc, sfa, sfb,
-                                    (kb > tile.kb0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k) {
+                // K-major: +32 bytes along K inside the 128-byte swizzled row (+2 in the >>4 field)
+                mma_e4m3_block_scaled(tmem_base, adesc + a_step * k, bdesc + b_step * k, idesc, sfa, sfb,
+                                      (kb > tile.kb0 || k > 0) ? 1u : 0u);
+              }
+              mma_commit(&empty_bar[s]);
+              if (last_of_word) mma_commit(&sf_empty_bar[slot]);   // the slot is free once these MMAs are done
             }
             issued_any = true;
-            mma_commit(&empty_bar[s]);
-            if ((kb & 3) == 3 || kb + 1 == tile.kb1) {
-              mma_commit(&sf_empty_bar[slot]);   // the slot is free once these MMAs are done
+            if (last_of_word) {
               ++sf_it;
               cur_quad = -1;
             }
           }
-          if (ok) mma_commit(acc_full_bar);
+          if (ok && lead) mma_commit(acc_full_bar);
         }
         ++tile_it;
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lane == 0 && issued_any) {
+      if (!alive && lead && issued_any) {
         // Abandoned: wait for the MMAs already issued before TMEM is freed.
         mma_commit(drain_bar);
         const uint32_t a = smem_u32(drain_bar);

@@ -28,6 +28,13 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
+// Whether this is the elected lane of the converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+  return is != 0;
+}
+
 // ---------------------------------------------------------------------------------------------
 // mbarrier
 
