@@ -557,6 +557,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       int issued_phase[STAGES];
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) issued_phase[s] = -1;
+      const bool lead = elect_one();
       // L2 hints: A tiles evict last (re-read by every n-block of the tiles in flight). With more
       // than one 128-row block, B tiles evict first: they stream past each m-block group, and A
       // then stays in L2. Measured: dense 4096x7168x16384 (A and B 64 + 117 MB) 385 -> 363 us
@@ -571,14 +572,14 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         const int b_row = (MODE == kKGrouped ? 0 : tile.g * p.N) + tile.n_blk * BN;
-        // Lane 0 runs the tile's K loop on its own (no warp-wide step per K-block).
-        int ok = 1;
-        if (lane == 0) {
-          for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
-            const int s = it % STAGES;
-            const uint32_t ph = (it / STAGES) & 1;
-            ok = mbar_wait(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
-            if (!ok) break;
+        // (warp-wide, one lane issuing, as the MMAs below)
+        bool ok = true;
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1;
+          ok = mbar_wait(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
+          if (!ok) break;
+          if (lead) {
             uint8_t* sa = smem + s * Plan::kStageBytes;
             mbar_arrive_expect_tx(&full_bar[s], Plan::kStageBytes);
             if (p.flags & kFlagAMN)   // A stored [K, M]: the box is 128 K-rows x 128 M-bytes
@@ -621,13 +622,15 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
             } else {
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, b_row, policy_b);
             }
-            issued_phase[s] = (int)ph;
           }
+#pragma unroll
+          for (int i = 0; i < STAGES; ++i)
+            if (i == s) issued_phase[i] = (int)ph;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lane == 0) {
+      if (!alive && lead) {
         // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
         for (int s = 0; s < STAGES; ++s) {
           if (issued_phase[s] < 0) continue;
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
           }
         }
       }
-      if (pair && lane == 0) {
+      if (pair && lead) {
         if (alive) {
           // Both CTAs' MMAs have released this CTA's last stages: the peer's last commits have
           // arrived on this CTA's barriers (and its copies into this CTA landed before them).

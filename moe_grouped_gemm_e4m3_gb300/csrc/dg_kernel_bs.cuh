@@ -187,19 +187,20 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) issued_phase[s] = -1;
       const uint64_t policy = l2_policy_evict_last();
+      const bool lead = elect_one();
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
         const Tile tile = decode_tile<BN, MODE, kGated>(p, sc, t, lane);
         if (tile.skip) continue;
         // (K-grouped: B [K_total, N] is shared by the groups, and A's M coordinate is the m-block's)
         const int b_row = (MODE == kKGrouped ? 0 : tile.g * p.N) + tile.n_blk * BN;
         const int a_m = MODE == kKGrouped ? tile.m_blk * 128 : tile.a_row;
-        int ok = 1;
-        if (lane == 0) {
-          for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {
-            const int s = it % STAGES;
-            const uint32_t ph = (it / STAGES) & 1;
-            ok = mbar_wait(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
-            if (!ok) break;
+        bool ok = true;
+        for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {   // (warp-wide, one lane issuing, as the MMAs below)
+          const int s = it % STAGES;
+          const uint32_t ph = (it / STAGES) & 1;
+          ok = mbar_wait(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
+          if (!ok) break;
+          if (lead) {
             uint8_t* sa = smem + s * Plan::kStageBytes;
             mbar_arrive_expect_tx(&full_bar[s], Plan::kStageBytes);
             if (p.flags & kFlagAMN)   // A stored [K, M]: the box is 128 K-rows x 128 M-bytes
@@ -220,13 +221,15 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
             } else {
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, b_row, policy);
             }
-            issued_phase[s] = (int)ph;
           }
+#pragma unroll
+          for (int i = 0; i < STAGES; ++i)
+            if (i == s) issued_phase[i] = (int)ph;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lane == 0) {
+      if (!alive && lead) {
         // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
         for (int s = 0; s < STAGES; ++s) {
           if (issued_phase[s] < 0) continue;

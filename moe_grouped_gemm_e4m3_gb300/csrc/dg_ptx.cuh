@@ -67,6 +67,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
   return ok != 0;
 }
 
+// As mbar_try_wait, but never parks the thread: the phase is complete now, or not.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bound of the drain waits on an abandoned path (the copies and MMAs already in flight): they do
 // not use the caller's limit below, so that in-flight work is always waited for.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -90,12 +103,14 @@ constexpr int kWaitLimitShift = 8;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                           int flags) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t limit_ns = (uint64_t)((uint32_t)flags >> kWaitLimitShift) * 1000ull;
+  const uint32_t limit_us = (uint32_t)flags >> kWaitLimitShift;
+  // (a limit of 0 gives up at once on a phase that is not already complete: a try_wait could park a whole warp until
+  // it is)
+  if (limit_us != 0 ? mbar_try_wait(a, parity) : mbar_test_wait(a, parity)) return true;
+  const uint64_t limit_ns = (uint64_t)limit_us * 1000ull;
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    // (a limit of 0 gives up at once on a phase that is not already complete)
-    if (limit_ns != 0) {
+    if (limit_us != 0) {
 #pragma unroll 1
       for (int i = 0; i < 32; ++i)
         if (mbar_try_wait(a, parity)) return true;
