@@ -64,7 +64,7 @@ bool cluster_split_setting() {
 // Programmatic dependent launch: 0 never, 1 always (DG_PDL, dg_set_pdl), or by default where a launch is at
 // most one wave of tiles or elementwise. Between kernels in plain stream order the GPU took 2 us steps back to back: the
 // gated projection of 333x2304x2064 14.3 us in plain order and 12.6 started early, the backward of 200x1024x1024 (three
-// calls) 23.6 and 17.3. Over several waves it gains nothing (8192x4096x7168 over 8 experts 215 and 221).
+// calls) 23.6 and 16.7. Over several waves it gains nothing (8192x4096x7168 over 8 experts 215 us and 221).
 enum Pdl : int { kPdlOff = 0, kPdlOn = 1, kPdlShort = 2 };
 std::atomic<int> g_pdl{-1};
 int pdl_setting() {

@@ -18,7 +18,8 @@
 //
 // One CTA takes a 128x128 tile at a time, which holds whole groups of every form: the input is read once
 // into registers, and the maxima along rows (shuffles within 16 lanes), columns and the block (shared
-// memory) come from there. Bound by HBM: 2 bytes read and 1 byte written per form and element.
+// memory) come from there. Bound by HBM: 2 bytes read and 1 byte written per form and element
+// (8192x7168, three forms: 52 us back to back, 5.7 TB/s; issue slots 72% busy, two thirds of it products and conversions).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -299,7 +300,7 @@ __device__ __forceinline__ float2 gate_sigmoid(float2 x) {
 //
 // SPLIT > 1: a tile's rows are shared by a cluster of SPLIT CTAs (one tile a cluster), which exchange their
 // column maxima through distributed shared memory. For few tiles, where one CTA's arithmetic on a whole tile is most of
-// the call: 200x512 rows 5.6 us with SPLIT = 1.
+// the call: 200x512 rows 5.6 us with SPLIT = 1, 4.3 with 4.
 constexpr int kGateThreads = 512;
 
 template <int SPLIT>
