@@ -250,7 +250,7 @@ struct Config {
 
 // gated: the gated projection, whose split-K exchange in clusters is priced anew (us: 0.8 + 0.2 a split for 64-column
 // tiles, 2.4 + 0.4 for 128-column ones, 1.4 + 0.4 block-scaled): the CTAs of a tile share the reduction, so it
-// grows slowly with the splits. With M = 333, 2I = 2304, K = 2064, block-scaled: 1/2/3/4/5 splits 15.6/13.8/12.6/12.9/13.1 us;
+// grows slowly with the splits. With M = 333, 2I = 2304, K = 2064, block-scaled: 1/2/3/4/5 splits 14.8/13.0/11.8/11.9/12.0 us;
 // FP32 scales: 64-column tiles 1/2 splits 11.5/10.5, 128-column 3/5 splits 12.6/13.0. The plain calls keep their linear
 // term: another split count would change their bits.
 Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false,
@@ -529,8 +529,9 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   Config cfg = choose_config(mode, rows, N, K, groups, sms, block_scaled, gated != nullptr);
   // A small gated projection with packed scales runs on the FP32-scale kernel's 64-column tiles, which read the
   // words as they are, where those are chosen for FP32 scales and make one wave: the block-scaled kernel has
-  // 128-column tiles only. Measured (us, 64-column tiles / block-scaled): 333x2304x2064 10.3 / 12.6, 128x2048x2048 8.6 / 10.9,
-  // 32x1024x1024 6.2 / 7.1, 700x768x7168 13.3 / 15.2, 1000x1280x1360 9.8 / 12.8, 64x4096x7168 12.0 / 12.4, 500x1536x4096 13.1 / 12.7.
+  // 128-column tiles only. Measured (us, 64-column tiles / block-scaled): 333x2304x2064 10.0 / 11.8, 128x2048x2048 8.5 / 9.4,
+  // 32x1024x1024 5.4 / 6.3, 700x768x7168 13.0 / 13.4, 1000x1280x1360 9.3 / 12.1, 40x2816x6000 8.6 / 9.8; the other way at 64x4096x7168
+  // 11.5 / 11.1 and 500x1536x4096 12.6 / 11.9.
   bool packed_on_fp32 = false;
   if (gated && block_scaled) {
     const Config narrow = choose_config(mode, rows, N, K, groups, sms, false, true);

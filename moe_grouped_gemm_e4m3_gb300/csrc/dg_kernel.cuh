@@ -553,9 +553,6 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       uint32_t it = 0;
       bool alive = true;
-      int issued_phase[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued_phase[s] = -1;
       const bool lead = elect_one();
       // L2 hints: A tiles evict last (re-read by every n-block of the tiles in flight). With more
       // than one 128-row block, B tiles evict first: they stream past each m-block group, and A
@@ -622,20 +619,17 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, b_row, policy_b);
             }
           }
-#pragma unroll
-          for (int i = 0; i < STAGES; ++i)
-            if (i == s) issued_phase[i] = (int)ph;
         }
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
       if (!alive && lead) {
         // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
-        for (int s = 0; s < STAGES; ++s) {
-          if (issued_phase[s] < 0) continue;
+        for (uint32_t s = 0; s < (uint32_t)STAGES && s < it; ++s) {   // `it` loads were issued
+          const uint32_t phase = ((it - 1 - (it - 1 - s) % STAGES) / STAGES) & 1;   // of the last into stage s
           const uint32_t a = smem_u32(&full_bar[s]);
           const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(a, (uint32_t)issued_phase[s]) && global_timer_ns() - t0 < kWaitLimitNs) {
+          while (!mbar_try_wait(a, phase) && global_timer_ns() - t0 < kWaitLimitNs) {
           }
         }
       }
@@ -643,11 +637,11 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         if (alive) {
           // Both CTAs' MMAs have released this CTA's last stages: the peer's last commits have
           // arrived on this CTA's barriers (and its copies into this CTA landed before them).
-          for (int s = 0; s < STAGES; ++s) {
-            if (issued_phase[s] < 0) continue;
+          for (uint32_t s = 0; s < (uint32_t)STAGES && s < it; ++s) {   // `it` loads were issued
+            const uint32_t phase = ((it - 1 - (it - 1 - s) % STAGES) / STAGES) & 1;   // of the last into stage s
             const uint32_t a = smem_u32(&empty_bar[s]);
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(a, (uint32_t)issued_phase[s]) && global_timer_ns() - t0 < kWaitLimitNs) {
+            while (!mbar_try_wait(a, phase) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
           }
         } else {

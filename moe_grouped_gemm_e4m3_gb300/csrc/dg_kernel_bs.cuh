@@ -183,9 +183,6 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       uint32_t it = 0;
       bool alive = true;
-      int issued_phase[STAGES];
-#pragma unroll
-      for (int s = 0; s < STAGES; ++s) issued_phase[s] = -1;
       const uint64_t policy = l2_policy_evict_last();
       const bool lead = elect_one();
       for (int t = blockIdx.x; alive && t < total_tiles; t += gridDim.x) {
@@ -222,20 +219,17 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
               tma_load_2d(&tmB, sa + Plan::kABytes, &full_bar[s], kb * 128, b_row, policy);
             }
           }
-#pragma unroll
-          for (int i = 0; i < STAGES; ++i)
-            if (i == s) issued_phase[i] = (int)ph;
         }
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
       if (!alive && lead) {
         // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
-        for (int s = 0; s < STAGES; ++s) {
-          if (issued_phase[s] < 0) continue;
+        for (uint32_t s = 0; s < (uint32_t)STAGES && s < it; ++s) {   // `it` loads were issued
+          const uint32_t phase = ((it - 1 - (it - 1 - s) % STAGES) / STAGES) & 1;   // of the last into stage s
           const uint32_t a = smem_u32(&full_bar[s]);
           const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(a, (uint32_t)issued_phase[s]) && global_timer_ns() - t0 < kWaitLimitNs) {
+          while (!mbar_try_wait(a, phase) && global_timer_ns() - t0 < kWaitLimitNs) {
           }
         }
       }

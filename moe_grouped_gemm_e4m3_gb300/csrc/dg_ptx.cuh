@@ -103,14 +103,12 @@ constexpr int kWaitLimitShift = 8;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status,
                                           int flags) {
   const uint32_t a = smem_u32(bar);
-  const uint32_t limit_us = (uint32_t)flags >> kWaitLimitShift;
-  // (a limit of 0 gives up at once on a phase that is not already complete: a try_wait could park a whole warp until
-  // it is)
-  if (limit_us != 0 ? mbar_try_wait(a, parity) : mbar_test_wait(a, parity)) return true;
-  const uint64_t limit_ns = (uint64_t)limit_us * 1000ull;
+  // (test_wait, which never parks the thread: a limit of 0 gives up at once on a phase that is not complete yet)
+  if (mbar_test_wait(a, parity)) return true;
+  const uint64_t limit_ns = (uint64_t)((uint32_t)flags >> kWaitLimitShift) * 1000ull;
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    if (limit_us != 0) {
+    if (limit_ns != 0) {
 #pragma unroll 1
       for (int i = 0; i < 32; ++i)
         if (mbar_try_wait(a, parity)) return true;
