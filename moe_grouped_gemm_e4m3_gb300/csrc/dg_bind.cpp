@@ -6,7 +6,9 @@
 // function here takes the entry point's arguments, makes the same checks as the Python path (type, shape,
 // device, contiguity of every tensor) and calls the library. Where anything is not as it should be it
 // returns None and calls nothing: the Python path then looks again and raises the error. So there is one set
-// of error messages, and without this module everything works, more slowly.
+// of error messages, and without this module everything works, more slowly. Torch's accessors throw (the sizes of
+// a nested tensor, the data of a fake one, the current stream without a driver): every function is called through
+// `guarded`, which makes that a None as well, so that no C++ exception reaches the interpreter.
 //
 // Host code only; compiled against the headers of the torch installation that it runs with (version()).
 #include <Python.h>
@@ -116,7 +118,7 @@ bool variant(Check& c, PyObject* o, int most, int* v) {
 }
 
 // gated(variant, A, sA, B, sB, m_indices or None (dense), H, GU, rng, p, stream); variant + 4: contiguous
-PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* gated(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int v;
   if (n != 11 || !variant(c, a[0], 8, &v)) return not_here();
@@ -139,7 +141,7 @@ PyObject* gated(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // dense(variant + 4 · layout (nt, nn, tn, tt), A, sA, B, sB, D, M, N, K, stream)
-PyObject* dense(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* dense(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int v;
   if (n != 10 || !variant(c, a[0], 16, &v)) return not_here();
@@ -158,7 +160,7 @@ PyObject* dense(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // contiguous(variant + 4 · (B stored [G, K, N]), A, sA, B, sB, m_indices, D, stream)
-PyObject* contiguous(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* contiguous(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int v;
   if (n != 8 || !variant(c, a[0], 8, &v)) return not_here();
@@ -178,7 +180,7 @@ PyObject* contiguous(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // k_grouped(variant, A, sA, B, sB, k_offsets, D, stream)
-PyObject* k_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* k_grouped(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int v;
   if (n != 8 || !variant(c, a[0], 4, &v)) return not_here();
@@ -197,7 +199,7 @@ PyObject* k_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // backward(ue8m0, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream)
-PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* backward(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int ue;
   if (n != 13 || !variant(c, a[0], 2, &ue)) return not_here();
@@ -218,7 +220,7 @@ PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // cast(ue8m0, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream), of one matrix [M, N]
-PyObject* cast(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* cast(PyObject* const* a, Py_ssize_t n) {
   Check c;
   int ue;
   if (n != 11 || !variant(c, a[0], 2, &ue)) return not_here();
@@ -238,7 +240,7 @@ PyObject* cast(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // dropout(X, R, Y, rng, p, stream)
-PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* dropout(PyObject* const* a, Py_ssize_t n) {
   Check c;
   const at::Tensor* x = n == 6 && g_loaded ? tensor(a[0]) : nullptr;
   if (!x || !x->defined() || x->layout() != at::kStrided) return not_here();
@@ -250,6 +252,17 @@ PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[5]);
   if (!c.ok) return not_here();
   return PyLong_FromLong(g_dropout[f32](px, pr, py, rng, p, x->numel(), s));
+}
+
+// The function as Python calls it: an exception of torch's is one more "not here".
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return F(a, n);
+  } catch (...) {
+    PyErr_Clear();
+    return not_here();
+  }
 }
 
 template <typename F>
@@ -283,7 +296,7 @@ PyObject* load(PyObject*, PyObject* path) {
 // The version of torch whose headers this was compiled against.
 PyObject* version(PyObject*, PyObject*) { return PyUnicode_FromString(TORCH_VERSION); }
 
-#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FAST(gated), FAST(dense), FAST(contiguous), FAST(k_grouped), FAST(backward), FAST(cast), FAST(dropout),
                            {"load", load, METH_O, nullptr}, {"version", version, METH_NOARGS, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_dgbind", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
