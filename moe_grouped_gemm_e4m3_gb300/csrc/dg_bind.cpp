@@ -3,8 +3,8 @@
 //
 // A step of a small layer runs kernels of a few microseconds, and a call's checks in Python (five attributes
 // of every tensor) cost as much: cast of 64x7168 rows 7.4 us of host time a call, 3.0 of them the library's. Each
-// function here takes the entry point's arguments, makes the same checks as the Python path (type, shape,
-// device, contiguity of every tensor) and calls the library. Where anything is not as it should be it
+// function here takes the entry point's arguments, makes the same checks as the Python path (of every tensor
+// its type, its shape, that it is a CUDA tensor and that it is contiguous) and calls the library. Where anything is not as it should be it
 // returns None and calls nothing: the Python path then looks again and raises the error. So there is one set
 // of error messages, and without this module everything works, more slowly. Torch's accessors throw (the sizes of
 // a nested tensor, the data of a fake one, the current stream without a driver): every function is called through
@@ -98,6 +98,22 @@ struct Check {
 
 PyObject* not_here() { Py_RETURN_NONE; }
 
+// The call itself, with the interpreter's lock released, as ctypes does: a launch waits when the stream's queue is full, and
+// a first call may allocate.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F, typename... Args>
+PyObject* status_of(F f, Args... args) {
+  int status;
+  {
+    Unlocked u;
+    status = f(args...);
+  }
+  return PyLong_FromLong(status);
+}
+
 using P = void*;
 // The library's entry points, by variant: bit 0 FP32 output, bit 1 packed UE8M0 scales.
 int (*g_gated[4])(P, P, P, P, P, P, P, double, int, int, int, P);
@@ -136,8 +152,8 @@ PyObject* gated(PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[10]);
   const int m = c.size(M), nn = c.size(N), k = c.size(K), g = c.size(G);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(grouped ? g_gated_grouped[v & 3](A, sA, B, sB, idx, H, GU, rng, p, m, nn, k, g, s)
-                                 : g_gated[v & 3](A, sA, B, sB, H, GU, rng, p, m, nn, k, s));
+  return grouped ? status_of(g_gated_grouped[v & 3], A, sA, B, sB, idx, H, GU, rng, p, m, nn, k, g, s)
+                 : status_of(g_gated[v & 3], A, sA, B, sB, H, GU, rng, p, m, nn, k, s);
 }
 
 // dense(variant + 4 · layout (nt, nn, tn, tt), A, sA, B, sB, D, M, N, K, stream)
@@ -156,7 +172,7 @@ PyObject* dense(PyObject* const* a, Py_ssize_t n) {
   P D = c.ptr(a[5], f32 ? kF32 : kBf16, {M, N});
   P s = c.stream(a[9]);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_dense[layout][v & 3](A, sA, B, sB, D, m, nn, k, s));
+  return status_of(g_dense[layout][v & 3], A, sA, B, sB, D, m, nn, k, s);
 }
 
 // contiguous(variant + 4 · (B stored [G, K, N]), A, sA, B, sB, m_indices, D, stream)
@@ -176,7 +192,7 @@ PyObject* contiguous(PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[7]);
   const int m = c.size(M), nn = c.size(N), k = c.size(K), g = c.size(G);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_contiguous[b_n][v & 3](A, sA, B, sB, idx, D, m, nn, k, g, s));
+  return status_of(g_contiguous[b_n][v & 3], A, sA, B, sB, idx, D, m, nn, k, g, s);
 }
 
 // k_grouped(variant, A, sA, B, sB, k_offsets, D, stream)
@@ -195,7 +211,7 @@ PyObject* k_grouped(PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[7]);
   const int m = c.size(M), nn = c.size(N), k = c.size(K), g = c.size(G);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_kgrouped[v](A, sA, B, sB, off, D, g, m, nn, k, s));
+  return status_of(g_kgrouped[v], A, sA, B, sB, off, D, g, m, nn, k, s);
 }
 
 // backward(ue8m0, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, p, stream)
@@ -216,7 +232,7 @@ PyObject* backward(PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[12]);
   const int m = c.size(M), i = c.size(I);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_backward[ue](dh, gu, idx, rng, p, qr, sr, qc, sc, hb, sh, m, i, s));
+  return status_of(g_backward[ue], dh, gu, idx, rng, p, qr, sr, qc, sc, hb, sh, m, i, s);
 }
 
 // cast(ue8m0, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream), of one matrix [M, N]
@@ -236,7 +252,7 @@ PyObject* cast(PyObject* const* a, Py_ssize_t n) {
   P s = c.stream(a[10]);
   const int m = c.size(M), nn = c.size(N);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_cast[ue](x, idx, qr, sr, qc, sc, qb, sb, sbt, 1, m, nn, s));
+  return status_of(g_cast[ue], x, idx, qr, sr, qc, sc, qb, sb, sbt, 1, m, nn, s);
 }
 
 // dropout(X, R, Y, rng, p, stream)
@@ -251,7 +267,7 @@ PyObject* dropout(PyObject* const* a, Py_ssize_t n) {
   const double p = c.real(a[4]);
   P s = c.stream(a[5]);
   if (!c.ok) return not_here();
-  return PyLong_FromLong(g_dropout[f32](px, pr, py, rng, p, x->numel(), s));
+  return status_of(g_dropout[f32], px, pr, py, rng, p, x->numel(), s);
 }
 
 // The function as Python calls it: an exception of torch's is one more "not here".

@@ -58,3 +58,50 @@ except (RuntimeError, ValueError, TypeError) as e:
     print("raised", type(e).__name__)
 """)
     assert p.returncode == 0 and "raised" in p.stdout, p.stdout[-2000:]
+
+
+@pytest.fixture(scope="module")
+def against_a_stand_in(tmp_path_factory):
+    """The short path loaded with a library whose entry points return whether the caller holds the interpreter's lock."""
+    import importlib.machinery
+    import importlib.util
+    import shutil
+
+    from moe_grouped_gemm_e4m3_gb300 import build
+    d = tmp_path_factory.mktemp("stand_in")
+    src, lib, bind = d / "stand_in.c", d / "libstandin.so", d / "_dgbind.so"
+    src.write_text("int PyGILState_Check(void);\n" + "".join(f"int {n}() {{ return PyGILState_Check(); }}\n" for n in dg.EXPORTED_SYMBOLS))
+    subprocess.run([os.environ.get("CC") or "gcc", "-std=c11", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    dg._bind()                                   # torch's libraries are loaded
+    shutil.copy(build.BIND, bind)                # a file of its own: its entry points are not the binding's
+    loader = importlib.machinery.ExtensionFileLoader("_dgbind", str(bind))
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_dgbind", str(bind), loader=loader))
+    loader.exec_module(mod)
+    assert mod.load(str(lib))
+    return mod
+
+
+def _shell(dtype, *shape):
+    """A tensor that says it is on the GPU and has no memory (nothing reads it here)."""
+    import torch
+
+    class Shell(torch.Tensor):
+        @classmethod
+        def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+            raise AssertionError(f"{func} on a tensor without memory")
+
+    return torch.Tensor._make_wrapper_subclass(Shell, shape, dtype=getattr(torch, dtype), device="cuda")
+
+
+def test_the_interpreter_runs_on_during_a_call(against_a_stand_in):
+    """A launch can wait for a full queue; other threads of Python must not wait with it."""
+    u8, bf, f32, i32 = ((lambda *s, d=d: _shell(d, *s)) for d in ("uint8", "bfloat16", "float32", "int32"))
+    a, sa, b, sb, d = u8(256, 256), f32(2, 256), u8(256, 256), f32(2, 2), bf(256, 256)
+    bg, sbg, idx, h, dk = u8(2, 256, 256), f32(2, 2, 2), i32(256), bf(256, 128), bf(2, 256, 256)
+    m = against_a_stand_in
+    calls = [m.dense(0, a, sa, b, sb, d, 256, 256, 256, 0), m.contiguous(0, a, sa, bg, sbg, idx, d, 0),
+             m.contiguous(4, a, sa, bg, sbg, idx, d, 0), m.k_grouped(0, a, sa, b, sb, i32(3), dk, 0),
+             m.gated(0, a, sa, b, sb, None, h, None, None, 0.0, 0), m.gated(4, a, sa, bg, sbg, idx, h, None, None, 0.0, 0),
+             m.backward(0, h, d, a, sa, None, None, None, None, None, None, 0.0, 0),
+             m.cast(0, d, a, sa, None, None, None, None, None, None, 0), m.dropout(d, None, d, None, 0.0, 0)]
+    assert calls == [0] * len(calls), calls      # (None: declined; 1: called with the lock held)
