@@ -201,13 +201,18 @@ def _bind():
 
     import torch
     load()
+    if not _build_mod.bind_tried():   # torch or Python changed since; without a compiler the calls are checked in Python
+        try:
+            _build_mod.build()
+        except (RuntimeError, OSError):
+            pass
     try:
         loader = importlib.machinery.ExtensionFileLoader("_dgbind", _build_mod.BIND)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_dgbind", _build_mod.BIND, loader=loader))
         loader.exec_module(mod)
     except (ImportError, OSError):
         return _NoBind
-    same = mod.version() == torch.__version__.split("+")[0]
+    same = mod.version() == torch.__version__.split("+")[0]   # (a process that outlived an upgrade on disk, or no compiler to follow it)
     return mod if same and mod.load(_build_mod.LIB) else _NoBind
 
 

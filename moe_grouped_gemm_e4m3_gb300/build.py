@@ -3,13 +3,15 @@
 The translation units are compiled in parallel (one per GEMM form plus the API layer) and linked
 into ``moe_grouped_gemm_e4m3_gb300/libdg.so``. ``_dgbind.so``, the binding's short path, is compiled beside it with the
 host compiler against the installed torch's headers; if that fails, a message is printed and the binding
-works without it. Rebuilds only when a source or header is newer than the library. Usage: ``python -m moe_grouped_gemm_e4m3_gb300.build [--force]``.
+works without it. Rebuilds only when a source or header is newer than the library, and ``_dgbind.so`` also when torch or
+Python is no longer the version it was compiled for. Usage: ``python -m moe_grouped_gemm_e4m3_gb300.build [--force]``.
 """
 from __future__ import annotations
 
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -23,6 +25,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdg.so")
 BIND = os.path.join(PKG, "_dgbind.so")
 BIND_SRC = os.path.join(CSRC, "dg_bind.cpp")
+BIND_KEY = os.path.join(BUILD_DIR, "dgbind.key")   # what the last compilation of _dgbind.so, good or not, was for
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC,
@@ -52,18 +55,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec is not None else None
+
+
+def _bind_key() -> str:
+    """The installed torch and Python, without importing torch (and its CUDA libraries)."""
+    try:
+        with open(os.path.join(_torch_dir() or "", "version.py")) as f:
+            found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        found = None
+    return f"torch {found.group(1) if found else None} {sys.implementation.cache_tag}"
+
+
+def bind_tried() -> bool:
+    """Whether _dgbind.so was compiled, or failed to, from this source for this torch and Python."""
+    if not os.path.exists(BIND_KEY):
+        return False
+    with open(BIND_KEY) as f:
+        same = f.read() == _bind_key()
+    return same and os.path.getmtime(BIND_KEY) >= max(os.path.getmtime(BIND_SRC), os.path.getmtime(os.path.abspath(__file__)))
+
+
 def _bind_current() -> bool:
-    newest = max(os.path.getmtime(BIND_SRC), os.path.getmtime(os.path.abspath(__file__)))
-    return os.path.exists(BIND) and os.path.getmtime(BIND) >= newest
+    return os.path.exists(BIND) and bind_tried()
 
 
 def _start_bind():
-    """The compilation of the binding's short path (None: no torch to compile against)."""
-    spec = importlib.util.find_spec("torch")
+    """The compilation of the binding's short path (None: no torch to compile against, or no compiler)."""
+    torch_dir = _torch_dir()
     cxx = os.environ.get("CXX") or shutil.which("g++")
-    if spec is None or not cxx:
+    if torch_dir is None or not cxx:
         return None
-    torch_dir = spec.submodule_search_locations[0]
     inc = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
@@ -71,17 +96,20 @@ def _start_bind():
     tmp = BIND + f".tmp{os.getpid()}"
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC"] + ["-I" + i for i in inc] + [BIND_SRC, "-o", tmp, "-L" + lib] + \
         ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl", "-Wl,-rpath," + lib]
-    return tmp, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    return tmp, _bind_key(), subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 def _finish_bind(started) -> None:
     if started is None:
         return
-    tmp, proc = started
+    tmp, key, proc = started
     out, _ = proc.communicate()
     if proc.returncode == 0:
         os.replace(tmp, BIND)
-    else:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BIND_KEY, "w") as f:
+        f.write(key)
+    if proc.returncode != 0:
         sys.stderr.write("the binding's short path did not compile (calls will check their arguments in Python):\n" +
                          out.decode(errors="replace")[-2000:])
 

@@ -105,3 +105,15 @@ def test_the_interpreter_runs_on_during_a_call(against_a_stand_in):
              m.backward(0, h, d, a, sa, None, None, None, None, None, None, 0.0, 0),
              m.cast(0, d, a, sa, None, None, None, None, None, None, 0), m.dropout(d, None, d, None, 0.0, 0)]
     assert calls == [0] * len(calls), calls      # (None: declined; 1: called with the lock held)
+
+
+def test_another_torch_asks_for_another_short_path(tmp_path, monkeypatch):
+    """The short path is compiled against torch's headers: an upgraded torch, whose files keep older dates, makes it stale."""
+    import importlib.util
+    import types
+
+    from moe_grouped_gemm_e4m3_gb300 import build
+    assert dg._bind() is not dg._NoBind and build._bind_current()
+    (tmp_path / "version.py").write_text("__version__ = '99.0.0+cu999'\n")
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name: types.SimpleNamespace(submodule_search_locations=[str(tmp_path)]))
+    assert not build._bind_current()
