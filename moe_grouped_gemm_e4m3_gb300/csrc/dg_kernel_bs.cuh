@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         for (int kb = tile.kb0; kb < tile.kb1; ++kb, ++it) {   // (warp-wide, one lane issuing, as the MMAs below)
           const int s = it % STAGES;
           const uint32_t ph = (it / STAGES) & 1;
-          ok = mbar_wait(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
+          ok = mbar_wait_warp(&empty_bar[s], ph ^ 1, abort_flag, p.status, p.flags);
           if (!ok) break;
           if (lead) {
             uint8_t* sa = smem + s * Plan::kStageBytes;
@@ -257,15 +257,15 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         // form spilled into this loop (64 rows, 2I = 7168, K = 16384: 36 us instead of 27; 4096x4096x7168 88 and 86).
         const int kb1 = __shfl_sync(0xffffffffu, tile.kb1, 0);
         // the epilogue has loaded the previous tile's accumulator
-        bool ok = mbar_wait(acc_empty_bar, (tile_it & 1) ^ 1, abort_flag, p.status, p.flags);
+        bool ok = mbar_wait_warp(acc_empty_bar, (tile_it & 1) ^ 1, abort_flag, p.status, p.flags);
         tc_fence_after();
         uint32_t accumulate = 0;
         for (int kb = __shfl_sync(0xffffffffu, tile.kb0, 0); ok && kb < kb1;) {   // the K-blocks of one scale word
           const int word_end = min((kb & ~3) + 4, kb1);
-          ok = mbar_wait(&sf_full_bar[slot], sf_ph, abort_flag, p.status, p.flags);
+          ok = mbar_wait_warp(&sf_full_bar[slot], sf_ph, abort_flag, p.status, p.flags);
           const uint32_t sfa = tmem_base + kSfCol0 + slot * kSfSlotCols;
           for (; ok && kb < word_end; ++kb) {
-            if (!ready) ok = mbar_wait(&full_bar[s], ph, abort_flag, p.status, p.flags);
+            if (!ready) ok = mbar_wait_warp(&full_bar[s], ph, abort_flag, p.status, p.flags);
             if (!ok) break;
             tc_fence_after();
             const uint64_t soff = (uint64_t)(s * (Plan::kStageBytes >> 4));
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       bool alive = true;
       auto post = [&](const Tile& tl, int end) -> bool {
         const uint32_t ds = desc_it % Plan::kDescSlots;
-        if (!mbar_wait(&desc_empty_bar[ds], ((desc_it / Plan::kDescSlots) & 1) ^ 1, abort_flag, p.status, p.flags))
+        if (!mbar_wait_warp(&desc_empty_bar[ds], ((desc_it / Plan::kDescSlots) & 1) ^ 1, abort_flag, p.status, p.flags))
           return false;
         if (lane == 0) {
           volatile int* d = desc_ring + ds * 8;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
           const uint32_t b0 = __ldg(sfb_ptr + quad);
           const uint32_t b1 = has_nb1 ? __ldg(sfb1_ptr + quad) : 0x7F7F7F7Fu;
           const uint32_t slot = sf_it % SLOTS;
-          if (!mbar_wait(&sf_empty_bar[slot], ((sf_it / SLOTS) & 1) ^ 1, abort_flag, p.status, p.flags)) {
+          if (!mbar_wait_warp(&sf_empty_bar[slot], ((sf_it / SLOTS) & 1) ^ 1, abort_flag, p.status, p.flags)) {
             alive = false;
             break;
           }
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       bool active, empty_k = false;
       {
         const uint32_t ds = desc_it % Plan::kDescSlots;
-        if (!mbar_wait(&desc_full_bar[ds], (desc_it / Plan::kDescSlots) & 1, abort_flag, p.status, p.flags)) {
+        if (!mbar_wait_warp(&desc_full_bar[ds], (desc_it / Plan::kDescSlots) & 1, abort_flag, p.status, p.flags)) {
           alive = false;
           break;
         }
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       uint32_t accu[EPI_COLS];
       float* const acc = reinterpret_cast<float*>(accu);
 
-      if (!mbar_wait(acc_full_bar, tile_it & 1, abort_flag, p.status, p.flags)) { alive = false; break; }
+      if (!mbar_wait_warp(acc_full_bar, tile_it & 1, abort_flag, p.status, p.flags)) { alive = false; break; }
       ++tile_it;
       tc_fence_after();
       if (active) {
