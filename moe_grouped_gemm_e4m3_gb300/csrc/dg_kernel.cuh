@@ -623,8 +623,9 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lead) {
-        // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
+      if (lead) {
+        // Let the loads issued land before the CTA's shared memory goes away: where a consumer gave up, nobody
+        // else waits for them. (Otherwise they landed long before the CTA's last store.)
         for (uint32_t s = 0; s < (uint32_t)STAGES && s < it; ++s) {   // `it` loads were issued
           const uint32_t phase = ((it - 1 - (it - 1 - s) % STAGES) / STAGES) & 1;   // of the last into stage s
           const uint32_t a = smem_u32(&full_bar[s]);
@@ -715,8 +716,9 @@ __global__ void __launch_bounds__(Roles<BN, EPI_COLS>::kThreads, 1)
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lead && last_b >= 0) {
-        // Abandoned: wait for the MMAs this thread issued before TMEM is freed.
+      if (lead && last_b >= 0) {
+        // Wait for the MMAs this thread issued before TMEM is freed and the CTA's shared memory goes away: where an
+        // epilogue warp gave up, nobody else waits for the last ones.
         const uint32_t a = smem_u32(&tfull_bar[last_b]);
         const uint64_t t0 = global_timer_ns();
         while (!mbar_try_wait(a, last_ph) && global_timer_ns() - t0 < kWaitLimitNs) {

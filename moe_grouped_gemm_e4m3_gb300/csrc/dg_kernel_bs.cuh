@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
   uint64_t* acc_empty_bar = acc_full_bar + 1;      // every epilogue warp has loaded it
   uint64_t* epi_arrive_bar = acc_empty_bar + 1;    // split-K: all epilogue warps published a partial
   uint64_t* epi_release_bar = epi_arrive_bar + 1;  // split-K: the arrival count has been taken
-  uint64_t* drain_bar = epi_release_bar + 1;       // abandon path: the MMAs issued have completed
+  uint64_t* drain_bar = epi_release_bar + 1;       // at the end: the MMAs issued have completed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Plan::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Plan::kMiscOff + 4);
   volatile int* last_flag = reinterpret_cast<volatile int*>(smem + Plan::kMiscOff + 8);
@@ -223,8 +223,9 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lead) {
-        // Abandoned: let the loads already issued land before the CTA's shared memory goes away.
+      if (lead) {
+        // Let the loads issued land before the CTA's shared memory goes away: where a consumer gave up, nobody
+        // else waits for them.
         for (uint32_t s = 0; s < (uint32_t)STAGES && s < it; ++s) {   // `it` loads were issued
           const uint32_t phase = ((it - 1 - (it - 1 - s) % STAGES) / STAGES) & 1;   // of the last into stage s
           const uint32_t a = smem_u32(&full_bar[s]);
@@ -295,8 +296,9 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         __syncwarp();
         if (!ok) { alive = false; break; }
       }
-      if (!alive && lead && issued_any) {
-        // Abandoned: wait for the MMAs already issued before TMEM is freed.
+      if (lead && issued_any) {
+        // Wait for the MMAs issued before TMEM is freed and the CTA's shared memory goes away: where an epilogue warp
+        // gave up, nobody else waits for the last ones.
         mma_commit(drain_bar);
         const uint32_t a = smem_u32(drain_bar);
         const uint64_t t0 = global_timer_ns();

@@ -1,4 +1,4 @@
-"""Waits that run out in the middle of a launch: a warp ends them with one verdict.
+"""Waits that run out in the middle of a launch: a warp ends them with one verdict, and what is in flight lands first.
 
 With limits of a few microseconds some waits of a launch are satisfied and others give up, at any K-block and in any
 role, and the lanes of a warp read the timer on both sides of the limit. Whatever happens, the launch has to end by
@@ -118,3 +118,25 @@ def test_waits_that_give_up_midway_end_the_launch(dg, form, ue):
         torch.cuda.synchronize()
         assert dg.dg_get_device_status() == 0
         assert torch.equal(out.view(torch.int8), ref.view(torch.int8)), f"the call after limits of {limit} us differs"
+
+
+@pytest.mark.parametrize("ue", [False, True], ids=["fp32", "ue8m0"])
+def test_a_limit_of_zero_with_every_load_already_issued(dg, ue):
+    """Two K-blocks a tile: the producer has issued all its loads, and waits for nothing, when the others give up."""
+    call, out = _dense(dg, ue, 128, 2112, 256)
+    call()
+    torch.cuda.synchronize()
+    assert dg.dg_get_device_status() == 0
+    ref = out.clone()
+    for _ in range(20):
+        prev = dg.dg_set_wait_limit_us(0)
+        try:
+            call()
+            assert dg.dg_get_device_status() == dg.DG_DEV_TIMEOUT
+        finally:
+            dg.dg_set_wait_limit_us(prev)
+        out.view(torch.int8).fill_(-1)
+        call()
+        torch.cuda.synchronize()
+        assert dg.dg_get_device_status() == 0
+        assert torch.equal(out.view(torch.int8), ref.view(torch.int8))
