@@ -561,12 +561,12 @@ dg_status dg_transform_sf_into_ue8m0_b(const float* sB, int32_t* sB_packed, int 
    Results are the same bits either way.
    on > 0: every GEMM and elementwise call is launched so; on = 0: every call in plain stream order; on < 0 (the
    default): the calls of at most one wave of tiles, and the elementwise ones, where it gains most. The
-   environment variable DG_PDL=1 or 0 sets the initial value to on or off. Returns the previous value, 1 for on
-   and 0 for off or the default. The pages name a PDL switch among the library's utilities, set_pdl / get_pdl
+   environment variable DG_PDL=1 or 0 sets the initial value to on or off. Returns the previous value: 1 for on,
+   0 for off, -1 for the default; passing it back restores it. The pages name a PDL switch among the library's utilities, set_pdl / get_pdl
    ("DeepGEMM: İnce ölçeklendirmeyle temiz ve verimli FP8 GEMM çekirdekleri",
    tr.news.hada.io/topic?id=19459, § "Yardımcı fonksiyonlar ve ortam değişkenleri"). */
 int dg_set_pdl(int on);
-/* Whether every call is launched so: 1, or 0 (off, or the default). */
+/* The current setting: 1, 0 or -1, as dg_set_pdl returns it. */
 int dg_get_pdl(void);
 
 /* Split-K inside thread-block clusters (dense and contiguous forms, either scale form). When a call

@@ -973,16 +973,21 @@ def dg_set_pair_b(on: bool) -> bool:
     return bool(load().dg_set_pair_b(1 if on else 0))
 
 
-def dg_set_pdl(on) -> bool:
+def _pdl(v):
+    return None if v < 0 else bool(v)
+
+
+def dg_set_pdl(on):
     """Launch every call with programmatic dependent launch (it may start before the previous kernel in the stream
     ends, and waits for that kernel's results before reading its inputs): True always, False never, None (the
-    default) where a call is elementwise or at most one wave of tiles. Returns whether it was always on; results
-    are bit-identical either way."""
-    return bool(load().dg_set_pdl(-1 if on is None else (1 if on else 0)))
+    default) where a call is elementwise or at most one wave of tiles. Returns the previous setting, in the same
+    three values, so that passing it back restores it; results are bit-identical either way."""
+    return _pdl(load().dg_set_pdl(-1 if on is None else (1 if on else 0)))
 
 
-def dg_get_pdl() -> bool:
-    return bool(load().dg_get_pdl())
+def dg_get_pdl():
+    """The current setting: True, False or None, as dg_set_pdl takes it."""
+    return _pdl(load().dg_get_pdl())
 
 
 def dg_set_tail_splits(n: int) -> int:

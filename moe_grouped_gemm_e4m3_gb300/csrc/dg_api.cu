@@ -1312,13 +1312,16 @@ int dg_set_pair_b(int on) {
   return prev;
 }
 
+int dg_get_pdl(void) {
+  const int v = pdl_setting();
+  return v == kPdlShort ? -1 : v;
+}
+
 int dg_set_pdl(int on) {
-  const int prev = pdl_setting() == kPdlOn ? 1 : 0;
+  const int prev = dg_get_pdl();
   g_pdl.store(on < 0 ? kPdlShort : (on ? kPdlOn : kPdlOff));
   return prev;
 }
-
-int dg_get_pdl(void) { return pdl_setting() == kPdlOn ? 1 : 0; }
 
 int dg_set_cluster_split(int on) {
   const int prev = cluster_split_setting() ? 1 : 0;
