@@ -511,21 +511,17 @@ long long dg_set_wait_limit_us(long long us);
    152 SMs. */
 int dg_set_tail_splits(int n);
 
-/* Pairs of CTAs sharing B tiles (dense and contiguous calls with FP32 scales and K-major operands,
-   BN = 256, no split-K, at least 256 rows). The CTAs run as clusters of two over pairs of 128-row
-   blocks that use the same B tile: each CTA loads its own A tile and half of the B tile, which TMA
-   multicasts into both CTAs' shared memory, so each SM pulls a third less operand data from L2 per
-   K-block. A contiguous pair whose two blocks belong to different groups loads each group's B tile
-   separately. Results are bit-identical with pairing on or off; only the schedule changes, and a
+/* Pairs of CTAs on the same B tiles (dense and contiguous calls with FP32 scales and K-major operands,
+   BN = 256, no split-K, at least 256 rows). The CTAs walk pairs of 128-row blocks two by two and ask for
+   the B tiles of a pair at the same time. Each CTA loads its own copy, the second from L2; no copy is shared
+   between SMs. In the contiguous form each CTA takes its own block's group. Results are
+   bit-identical with pairing on or off; only the schedule changes, and a
    paired launch has no tail split. dg_query_config reports a paired configuration as block_m 256.
    Pairing is off by default: on = 1 switches it on, on = 0 off; the environment variable
    DG_PAIR_B=1 sets it on initially. Returns the previous setting. Measured on GB300, pairing does
    not shorten the kernel's period per K-block: that is set by the hand-off MMA -> promotion -> MMA
-   through the tensor memory, and each SM still receives the whole B tile. Pairing also loses the
-   tail split (4096x7168x16384: 397 us single, 419 us paired; under a sustained load the paired
-   launch draws less power and runs about 4% higher in clock, but needs about 8% more cycles).
-   The pages say only that the design moves its operands with TMA ("DeepSeek AI libera DeepGEMM…",
-   7minutos.es, § "Detalles y beneficios técnicos"); sharing them through multicast is this
+   through the tensor memory (4096x4096x7168: 107 us single, 110 paired; 4096x7168x2048: 58 us either way). The pages say only that the design moves its operands with
+   TMA ("DeepSeek AI libera DeepGEMM…", 7minutos.es, § "Detalles y beneficios técnicos"); this schedule is this
    implementation's choice. */
 int dg_set_pair_b(int on);
 

@@ -968,8 +968,8 @@ def dg_set_wait_limit_us(us: int) -> int:
 
 
 def dg_set_pair_b(on: bool) -> bool:
-    """Allow or forbid (default) pairs of CTAs that share B tiles through TMA multicast. Returns the
-    previous value; results are bit-identical either way."""
+    """Allow or forbid (default) walking the tiles by pairs of CTAs that ask for the same B tiles at the same time. Returns
+    the previous value; results are bit-identical either way."""
     return bool(load().dg_set_pair_b(1 if on else 0))
 
 

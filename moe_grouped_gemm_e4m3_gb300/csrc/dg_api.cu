@@ -83,10 +83,10 @@ bool early_start(long long units, int sms) {
   return v == kPdlOn || (v == kPdlShort && units <= sms);
 }
 
-// Pairs of CTAs sharing B tiles through TMA multicast (dense and contiguous, FP32 scales, BN = 256,
-// no split-K): off unless DG_PAIR_B=1 or dg_set_pair_b(1). Measured on GB300, the FP32-scale kernel
-// is bound by its per-K-block TMEM round trip, not by the L2 feed that pairing relieves, and paired
-// launches lose the tail split: 4096x7168x16384 397 us single, 419 us paired.
+// Pairs of CTAs on the same B tiles (dense and contiguous, FP32 scales, BN = 256, no split-K): off unless
+// DG_PAIR_B=1 or dg_set_pair_b(1). The FP32-scale kernel is bound by its per-K-block TMEM round trip, not by
+// the L2 feed, and paired launches lose the tail split: 4096x4096x7168 107 us single and 110 paired, 4096x7168x2048 58
+// either way.
 std::atomic<int> g_pair_b{-1};
 bool pair_b_setting() {
   int v = g_pair_b.load();
@@ -363,14 +363,14 @@ bool use_cluster_split(const Config& c, int mode, bool out_f32, bool block_scale
          cluster_capacity(mode, c.block_n, out_f32, c.splits, block_scaled) >= c.tiles;
 }
 
-// Whether a call with this configuration runs as pairs of CTAs sharing B (kFlagPairB): dense or
+// Whether a call with this configuration runs as pairs of CTAs on the same B tiles (kFlagPairB): dense or
 // contiguous with FP32 scales and K-major operands, BN = 256, no split-K, at least two 128-row
-// blocks, and clusters of 2 can be resident. Returns the resident clusters of 2 (0: no pairing).
-int pair_clusters(const Config& c, int mode, int rows, bool out_f32, bool block_scaled, bool swiglu, bool mn_layout) {
+// blocks. Returns the pairs that `sms` SMs hold (0: no pairing).
+int pairs_resident(const Config& c, int mode, int rows, int sms, bool block_scaled, bool swiglu, bool mn_layout) {
   if (!pair_b_setting() || block_scaled || swiglu || mn_layout) return 0;
   if ((mode != dg::kDense && mode != dg::kContiguous) || c.block_n != 256 || c.splits != 1 || ceil_div(rows, 128) < 2)
     return 0;
-  return cluster_capacity(mode, 256, out_f32, 2, false);
+  return sms / 2;
 }
 
 // Read on every call (a debugging aid), so that a process can switch it on and off.
@@ -596,18 +596,17 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   // distributed shared memory (no workspace, no counters) when every tile's cluster can be resident
   // at once and each CTA gets exactly one work unit.
   const bool cluster = use_cluster_split(cfg, mode, out_f32, block_scaled, swiglu);
-  // Pairs of CTAs share B tiles (kFlagPairB): the persistent units are pairs of 128-row blocks by
-  // BN columns, walked by clusters of 2; no tail split.
-  const int pair_cap = cluster ? 0 : pair_clusters(cfg, mode, rows, out_f32, block_scaled, swiglu || gated, a_mn || b_mn);
+  // Pairs of CTAs on the same B tiles (kFlagPairB): the persistent units are pairs of 128-row blocks by
+  // BN columns, walked by two CTAs each; no tail split.
+  const int pair_cap = cluster ? 0 : pairs_resident(cfg, mode, rows, sms, block_scaled, swiglu || gated, a_mn || b_mn);
   const bool pair = pair_cap > 0;
   if (pair) {
     const int m_pairs = ceil_div(ceil_div(rows, 128), 2);
     const long long units = (long long)m_pairs * ceil_div(N, cfg.block_n);
     p.flags |= dg::kFlagPairB;
-    p.num_tiles = (int)units;
+    p.num_tiles = 2 * (int)units;
     p.raster_m = (int16_t)(m_pairs < 8 ? m_pairs : 8);
     p.tail_splits = 1;
-    a.cluster = 2;
     cfg.grid = 2 * (int)(units < pair_cap ? units : pair_cap);
   }
   if (cluster) {
@@ -648,7 +647,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
     return s;
   }
   // rows of B's boxes: the gated tile's quarters (FP32 scales), or gate and up halves
-  const int b_box = gated && !block_scaled ? cfg.block_n / 4 : (swiglu || gated ? 128 : (pair ? cfg.block_n / 2 : cfg.block_n));
+  const int b_box = gated && !block_scaled ? cfg.block_n / 4 : (swiglu || gated ? 128 : cfg.block_n);
   if (b_mn) {   // B stored [K, N]: N contiguous, boxes of 128 N-bytes x 128 K-rows
     if ((s = encode_2d(&a.tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, B, (uint64_t)b_rows, (uint64_t)b_ks, (uint64_t)b_rows, 128,
                        128, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, "B")) != DG_OK)
@@ -688,7 +687,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
     static const char* names[3] = {"dense", "contiguous", "masked"};
     std::fprintf(stderr, "[dg] %s%s%s%s rows=%d N=%d K=%d G=%d: BM=128 BN=%d stages=%d splits=%d%s grid=%d tiles=%d\n",
                  names[mode], block_scaled ? "/ue8m0" : "", swiglu || gated ? "/swiglu" : "", out_f32 ? "/f32" : "", rows, N, K,
-                 p.G, cfg.block_n, cfg.stages, cfg.splits, cluster ? " (cluster)" : (pair ? " (pairs sharing B)" : ""),
+                 p.G, cfg.block_n, cfg.stages, cfg.splits, cluster ? " (cluster)" : (pair ? " (pairs on B)" : ""),
                  cfg.grid, cfg.tiles);
   }
   cudaError_t e;
@@ -1394,7 +1393,7 @@ dg_status query_config(int mode, int M, int N, int K, int G, int* cfg, bool bloc
   if (st) {
     fit_cluster_splits(c, mode, K, block_scaled, false);
     const int cap = use_cluster_split(c, mode, false, block_scaled, false)
-                        ? 0 : pair_clusters(c, mode, M, false, block_scaled, false, false);
+                        ? 0 : pairs_resident(c, mode, M, sms, block_scaled, false, false);
     if (cap > 0) {   // pairs of CTAs: 256 rows (two CTAs of 128) by BN columns per unit
       const long long units = (long long)ceil_div(ceil_div(M, 128), 2) * ceil_div(N, c.block_n);
       c.grid = 2 * (int)(units < cap ? units : cap);
