@@ -475,8 +475,8 @@ int dg_get_tma_aligned_size(int x, int elem_bytes);
    Source: get_mk_alignment_for_contiguous_layout, same page and section. */
 int dg_get_mk_alignment_for_contiguous_layout(void);
 
-/* Cap on the SMs the kernels use (0 restores the device's SM count; the environment variable
-   DG_NUM_SMS sets the initial cap). Source: set_num_sms / get_num_sms, same page and section.
+/* Cap on the SMs the kernels use: under it no launch, of any call, has more CTAs than this many (0 restores
+   the device's SM count; the environment variable DG_NUM_SMS sets the initial cap). Source: set_num_sms / get_num_sms, same page and section.
    dg_get_num_sms() returns the cap in force for the current device. */
 void dg_set_num_sms(int n);
 int dg_get_num_sms(void);
@@ -556,7 +556,8 @@ dg_status dg_transform_sf_into_ue8m0_b(const float* sB, int32_t* sB_packed, int 
    setup. A kernel that follows one of these in the stream starts early only if it was itself launched for it.
    Results are the same bits either way.
    on > 0: every GEMM and elementwise call is launched so; on = 0: every call in plain stream order; on < 0 (the
-   default): the calls of at most one wave of tiles, and the elementwise ones, where it gains most. The
+   default): the calls of at most one wave of tiles, and the elementwise ones, where it gains most, and none while
+   dg_set_num_sms caps the SMs (a kernel that starts early takes SMs beside the one ahead of it). The
    environment variable DG_PDL=1 or 0 sets the initial value to on or off. Returns the previous value: 1 for on,
    0 for off, -1 for the default; passing it back restores it. The pages name a PDL switch among the library's utilities, set_pdl / get_pdl
    ("DeepGEMM: İnce ölçeklendirmeyle temiz ve verimli FP8 GEMM çekirdekleri",

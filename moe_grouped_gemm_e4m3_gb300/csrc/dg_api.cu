@@ -77,10 +77,11 @@ int pdl_setting() {
   }
   return v;
 }
-// Whether a launch of this many units of work on this many SMs may start early.
-bool early_start(long long units, int sms) {
+// Whether a launch of this many units of work may start early. Not by default where the SMs are capped: its CTAs would take
+// further SMs beside those of the launch ahead of it.
+bool early_start(long long units, const dg::SmLimit& sms) {
   const int v = pdl_setting();
-  return v == kPdlOn || (v == kPdlShort && units <= sms);
+  return v == kPdlOn || (v == kPdlShort && !sms.capped && units <= sms.sms);
 }
 
 // Pairs of CTAs on the same B tiles (dense and contiguous, FP32 scales, BN = 256, no split-K): off unless
@@ -233,6 +234,11 @@ dg_status device_state(DeviceState** out) {
 int effective_sms(const DeviceState& st) {
   const int cap = num_sms_cap();
   return (cap > 0 && cap < st.sm_count) ? cap : st.sm_count;
+}
+
+dg::SmLimit sm_limit(const DeviceState& st) {
+  const int sms = effective_sms(st);
+  return {sms, sms < st.sm_count};
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -522,7 +528,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   const int sms = effective_sms(*st);
   if (gated && mode == dg::kDense && rows <= dg::kFewTokens) {   // the weights' read is the whole cost
     const cudaError_t e = dg::launch_gated_few(A, sA, B, sB, D, gated->GU, gated->drop, rows, N / 2, K, out_f32, block_scaled,
-                                               dg::StreamArgs{stream, sms, early_start(0, sms)});
+                                               dg::StreamArgs{stream, sm_limit(*st), early_start(0, sm_limit(*st))});
     return e == cudaSuccess ? DG_OK : fail_cuda(e, "kernel launch");
   }
   const int groups = mode == dg::kDense ? 1 : G;
@@ -682,7 +688,7 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   a.out_f32 = out_f32;
   a.grid = cfg.grid;
   a.stream = stream;
-  a.pdl = early_start((long long)cfg.tiles * cfg.splits, sms);
+  a.pdl = early_start((long long)cfg.tiles * cfg.splits, sm_limit(*st));
   if (print_configs()) {
     static const char* names[3] = {"dense", "contiguous", "masked"};
     std::fprintf(stderr, "[dg] %s%s%s%s rows=%d N=%d K=%d G=%d: BM=128 BN=%d stages=%d splits=%d%s grid=%d tiles=%d\n",
@@ -789,7 +795,7 @@ dg_status run_k_grouped(bool out_f32, const uint8_t* A, const void* sA, const ui
   a.out_f32 = out_f32;
   a.grid = tiles < sms ? tiles : sms;
   a.stream = stream;
-  a.pdl = early_start(tiles, sms);
+  a.pdl = early_start(tiles, sm_limit(*st));
   if (print_configs())
     std::fprintf(stderr, "[dg] k-grouped%s%s G=%d M=%d N=%d K_total=%d: BM=128 BN=%d grid=%d tiles=%d\n",
                  block_scaled ? "/ue8m0" : "", out_f32 ? "/f32" : "", G, M, N, K_total, bn, a.grid, tiles);
@@ -816,8 +822,8 @@ dg_status stream_args(dg_stream_t stream, dg::StreamArgs* out) {
   const dg_status s = device_state(&st);
   if (s != DG_OK) return s;
   out->stream = static_cast<cudaStream_t>(stream);
-  out->sms = effective_sms(*st);
-  out->pdl = early_start(0, out->sms);   // (the kernels wait with griddepcontrol before their first access)
+  out->limit = sm_limit(*st);
+  out->pdl = early_start(0, out->limit);   // (the kernels wait with griddepcontrol before their first access)
   return DG_OK;
 }
 
@@ -1016,7 +1022,7 @@ dg_status dg_transform_sf_into_ue8m0_a(const float* sA, int32_t* sA_packed, int 
   dg_status s = device_state(&st);
   if (s != DG_OK) return s;
   const int nkb = ceil_div(K, 128), ldsa = dg_get_tma_aligned_size(M, 4);
-  const cudaError_t e = dg::launch_sf_pack_a(sA, sA_packed, G, nkb, ldsa, st->status, effective_sms(*st),
+  const cudaError_t e = dg::launch_sf_pack_a(sA, sA_packed, G, nkb, ldsa, st->status, sm_limit(*st),
                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "UE8M0 packing (A) launch");
 }
@@ -1030,7 +1036,7 @@ dg_status dg_transform_sf_a_into_mn_major(const float* sA_rows, float* sA, int G
   dg_status s = device_state(&st);
   if (s != DG_OK) return s;
   const cudaError_t e = dg::launch_sf_a_to_mn_major(sA_rows, sA, G, M, ceil_div(K, 128), dg_get_tma_aligned_size(M, 4),
-                                                     static_cast<cudaStream_t>(stream));
+                                                     sm_limit(*st), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "scale transpose launch");
 }
 
@@ -1043,7 +1049,7 @@ dg_status dg_transform_sf_into_ue8m0_b(const float* sB, int32_t* sB_packed, int 
   if (s != DG_OK) return s;
   const int nkb = ceil_div(K, 128);
   const long long rows = (long long)G * ceil_div(N, 128);
-  const cudaError_t e = dg::launch_sf_pack_b(sB, sB_packed, rows, nkb, st->status, effective_sms(*st),
+  const cudaError_t e = dg::launch_sf_pack_b(sB, sB_packed, rows, nkb, st->status, sm_limit(*st),
                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "UE8M0 packing (B) launch");
 }

@@ -530,7 +530,7 @@ cudaError_t launch_cast_as(const uint16_t* x, const int32_t* m_indices, const Ca
   static bool done[64] = {};
   const cudaError_t e = allow_smem(cast_kernel<UE>, sizeof(CastShared), done);
   if (e != cudaSuccess) return e;
-  const int tiles = G * ((M + 127) / 128) * ((N + 127) / 128), most = kCastCtas * s.sms;
+  const int tiles = G * ((M + 127) / 128) * ((N + 127) / 128), most = (int)s.limit.ctas(kCastCtas);
   return launch_plain(cast_kernel<UE>, tiles < most ? tiles : most, kCastThreads, sizeof(CastShared), s, x, m_indices, f, M,
                       N, tiles);
 }
@@ -541,7 +541,7 @@ cudaError_t launch_backward_as(const uint16_t* dh, const uint16_t* gu, const int
   static bool done[64] = {};
   const cudaError_t e = allow_smem(swiglu_backward_kernel<UE, BLOCKS, SPLIT>, sizeof(GateShared<SPLIT>), done);
   if (e != cudaSuccess) return e;
-  const int tiles = (M + 127) / 128 * (I / 128), most = s.sms / SPLIT;
+  const int tiles = (M + 127) / 128 * (I / 128), most = s.limit.sms / SPLIT;
   return launch_plain(swiglu_backward_kernel<UE, BLOCKS, SPLIT>, (tiles < most ? tiles : most) * SPLIT, kGateThreads,
                       sizeof(GateShared<SPLIT>), s, dh, gu, m_indices, d, dgu, h, M, I, tiles);
 }
@@ -559,7 +559,7 @@ cudaError_t launch_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const
   auto go = [&](auto launch, const StreamArgs& with) { return launch(dh, gu, m_indices, d, dgu, h, M, I, with); };
   // few tiles: four CTAs on each, while every cluster gets SMs of its own
   const long long tiles = ((long long)M + 127) / 128 * (I / 128);
-  if (4 * tiles <= s.sms) {
+  if (4 * tiles <= s.limit.sms) {
     StreamArgs four = s;
     four.cluster = 4;
     if (h.q_blk) return ue8m0 ? go(launch_backward_as<true, true, 4>, four) : go(launch_backward_as<false, true, 4>, four);

@@ -54,40 +54,47 @@ __device__ __forceinline__ void drop_and_add(float (&v)[8], const float (&add)[8
 }
 
 // VEC: X, R and Y are 16-byte aligned; otherwise every access is one element (any alignment that the
-// element type allows).
-template <typename T, bool VEC, bool RES, int GROUPS>
+// element type allows). CAPPED: a grid of fewer CTAs (dg_set_num_sms) that loops.
+template <typename T, bool VEC, bool RES, int GROUPS, bool CAPPED>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, const T* r, T* y, const Dropout d, long long n) {
   griddep_wait();
   griddep_launch_dependents();
   const Philox gen = d.threshold ? Philox(d.rng) : Philox();
-  const long long first = (long long)blockIdx.x * (kThreads * GROUPS) + threadIdx.x;
-  Eight<T> xs[GROUPS], rs[GROUPS];
-  if constexpr (VEC) {
+  auto pass = [&](long long first) {
+    Eight<T> xs[GROUPS], rs[GROUPS];
+    if constexpr (VEC) {
+#pragma unroll
+      for (int k = 0; k < GROUPS; ++k) {
+        const long long i = first + k * kThreads;
+        if (i * 8 + 8 > n) continue;
+        xs[k].load(x + i * 8);
+        if constexpr (RES) rs[k].load(r + i * 8);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < GROUPS; ++k) {
       const long long i = first + k * kThreads;
-      if (i * 8 + 8 > n) continue;
-      xs[k].load(x + i * 8);
-      if constexpr (RES) rs[k].load(r + i * 8);
+      if (i * 8 >= n) return;
+      float v[8], add[8];
+      if (VEC && i * 8 + 8 <= n) {
+        xs[k].values(v);
+        if constexpr (RES) rs[k].values(add);
+        drop_and_add<RES>(v, add, gen, i, d);
+        store8(y + i * 8, v);
+      } else {   // unaligned tensors, and the last, partial eight
+        const int live = (int)(n - i * 8 < 8 ? n - i * 8 : 8);
+        load8_part(x + i * 8, live, v);
+        if constexpr (RES) load8_part(r + i * 8, live, add);
+        drop_and_add<RES>(v, add, gen, i, d);
+        store8_part(y + i * 8, live, v);
+      }
     }
-  }
-#pragma unroll
-  for (int k = 0; k < GROUPS; ++k) {
-    const long long i = first + k * kThreads;
-    if (i * 8 >= n) return;
-    float v[8], add[8];
-    if (VEC && i * 8 + 8 <= n) {
-      xs[k].values(v);
-      if constexpr (RES) rs[k].values(add);
-      drop_and_add<RES>(v, add, gen, i, d);
-      store8(y + i * 8, v);
-    } else {   // unaligned tensors, and the last, partial eight
-      const int live = (int)(n - i * 8 < 8 ? n - i * 8 : 8);
-      load8_part(x + i * 8, live, v);
-      if constexpr (RES) load8_part(r + i * 8, live, add);
-      drop_and_add<RES>(v, add, gen, i, d);
-      store8_part(y + i * 8, live, v);
-    }
+  };
+  const long long first = (long long)blockIdx.x * (kThreads * GROUPS) + threadIdx.x;
+  if constexpr (CAPPED) {
+    for (long long i = first; i * 8 < n; i += (long long)gridDim.x * (kThreads * GROUPS)) pass(i);
+  } else {
+    pass(first);
   }
 }
 
@@ -96,12 +103,13 @@ cudaError_t launch_shape(const T* x, const T* r, T* y, const Dropout& d, long lo
   // several groups a thread once they still fill every SM four times over
   constexpr int kGroups = sizeof(T) == 2 ? 4 : 2;
   const long long eights = (n + 7) / 8;
-  auto go = [&](auto kernel, int groups) {
-    const long long per = (long long)kThreads * groups;
-    return launch_plain(kernel, (int)((eights + per - 1) / per), kThreads, 0, s, x, r, y, d, n);
+  auto go = [&](auto kernel, auto capped, int groups) {
+    const long long per = (long long)kThreads * groups, blocks = (eights + per - 1) / per, grid = s.limit.all(blocks);
+    return launch_plain(grid < blocks ? capped : kernel, (int)grid, kThreads, 0, s, x, r, y, d, n);
   };
-  if (VEC && eights >= 4LL * s.sms * kThreads * kGroups) return go(dropout_kernel<T, VEC, RES, kGroups>, kGroups);
-  return go(dropout_kernel<T, VEC, RES, 1>, 1);
+  if (VEC && eights >= 4LL * s.limit.sms * kThreads * kGroups)
+    return go(dropout_kernel<T, VEC, RES, kGroups, false>, dropout_kernel<T, VEC, RES, kGroups, true>, kGroups);
+  return go(dropout_kernel<T, VEC, RES, 1, false>, dropout_kernel<T, VEC, RES, 1, true>, 1);
 }
 
 template <typename T>

@@ -65,7 +65,8 @@ __device__ __forceinline__ float scale_value(uint32_t bits, int kb) {
   return ue8m0_value(bits >> (8 * (kb & 3)));
 }
 
-template <bool UE, bool OUT_F32, int NT>
+// CAPPED: fewer CTAs than groups of 8 columns (dg_set_num_sms), each taking several; a loop in the other form spills.
+template <bool UE, bool OUT_F32, int NT, bool CAPPED>
 __global__ void __launch_bounds__(FewPlan<NT>::kThreads, 2)
     gated_few_kernel(const uint8_t* __restrict__ A, const void* __restrict__ sA, const uint8_t* __restrict__ B,
                      const void* __restrict__ sB, void* H, uint16_t* GU, const Dropout drop, int M, int I, int K) {
@@ -75,88 +76,97 @@ __global__ void __launch_bounds__(FewPlan<NT>::kThreads, 2)
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane / 4, t = lane % 4;
   const int nkb = (K + 127) / 128, nkq = (nkb + 3) / 4, ldsa = (M + 3) / 4 * 4;
-  const int j0 = blockIdx.x * 8;
-  const int nb_gate = j0 / 128, nb_up = I / 128 + nb_gate;
-  const uint8_t* gate = B + (size_t)(j0 + g) * K;
-  const uint8_t* up = gate + (size_t)I * K;
+  auto columns = [&](int j0) {   // 8 columns of H
+    const int nb_gate = j0 / 128, nb_up = I / 128 + nb_gate;
+    const uint8_t* gate = B + (size_t)(j0 + g) * K;
+    const uint8_t* up = gate + (size_t)I * K;
 
-  float acc[NT][4] = {};
-  for (int kb0 = warp; kb0 < nkb; kb0 += kWarps * kBatch) {
-    uint4 w[kBatch][4], x[kBatch][NT][2];   // w: gate and up, 64-byte halves 0 and 1
-    uint32_t sg[kBatch], su[kBatch], sx[kBatch][NT][2];
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float acc[NT][4] = {};
+    for (int kb0 = warp; kb0 < nkb; kb0 += kWarps * kBatch) {
+      uint4 w[kBatch][4], x[kBatch][NT][2];   // w: gate and up, 64-byte halves 0 and 1
+      uint32_t sg[kBatch], su[kBatch], sx[kBatch][NT][2];
+      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int kb = kb0 + i * kWarps;
-      const bool some = kb < nkb;
+      for (int i = 0; i < kBatch; ++i) {
+        const int kb = kb0 + i * kWarps;
+        const bool some = kb < nkb;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = kb * 128 + c * 64 + t * 16;
-        const bool live = some && k < K;
-        w[i][c] = live ? load_stream(gate + k) : zero;
-        w[i][2 + c] = live ? load_stream(up + k) : zero;
+        for (int c = 0; c < 2; ++c) {
+          const int k = kb * 128 + c * 64 + t * 16;
+          const bool live = some && k < K;
+          w[i][c] = live ? load_stream(gate + k) : zero;
+          w[i][2 + c] = live ? load_stream(up + k) : zero;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            x[i][n][c] = live && n * 8 + g < M ? load_16(A + (size_t)(n * 8 + g) * K + k) : zero;
+        }
+        // (FP32 scales one a K-block, packed words one a four)
+        const int kq = UE ? kb / 4 : kb, ns = UE ? nkq : nkb;
+        const uint32_t *a = static_cast<const uint32_t*>(sA), *b = static_cast<const uint32_t*>(sB);
+        sg[i] = some ? load_4(b + (size_t)nb_gate * ns + kq) : 0u;
+        su[i] = some ? load_4(b + (size_t)nb_up * ns + kq) : 0u;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          x[i][n][c] = live && n * 8 + g < M ? load_16(A + (size_t)(n * 8 + g) * K + k) : zero;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int m = n * 8 + 2 * t + c;
+            sx[i][n][c] = some && m < M ? load_4(a + (size_t)kq * ldsa + m) : 0u;
+          }
       }
-      // (FP32 scales one a K-block, packed words one a four)
-      const int kq = UE ? kb / 4 : kb, ns = UE ? nkq : nkb;
-      const uint32_t *a = static_cast<const uint32_t*>(sA), *b = static_cast<const uint32_t*>(sB);
-      sg[i] = some ? load_4(b + (size_t)nb_gate * ns + kq) : 0u;
-      su[i] = some ? load_4(b + (size_t)nb_up * ns + kq) : 0u;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < kBatch; ++i) {
+        const int kb = kb0 + i * kWarps;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int m = n * 8 + 2 * t + c;
-          sx[i][n][c] = some && m < M ? load_4(a + (size_t)kq * ldsa + m) : 0u;
-        }
-    }
+        for (int n = 0; n < NT; ++n) {
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int kb = kb0 + i * kWarps;
+          for (int c = 0; c < 2; ++c) {
+            const uint4 &a = w[i][c], &b = w[i][2 + c], &v = x[i][n][c];
+            mma_16x8x32(part, a.x, b.x, a.y, b.y, v.x, v.y);
+            mma_16x8x32(part, a.z, b.z, a.w, b.w, v.z, v.w);
+          }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 &a = w[i][c], &b = w[i][2 + c], &v = x[i][n][c];
-          mma_16x8x32(part, a.x, b.x, a.y, b.y, v.x, v.y);
-          mma_16x8x32(part, a.z, b.z, a.w, b.w, v.z, v.w);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {   // rows g (gate: q = 0, 1) and g + 8 (up), tokens 2t and 2t + 1
-          const float s = scale_value<UE>(q < 2 ? sg[i] : su[i], kb), m = scale_value<UE>(sx[i][n][q & 1], kb);
-          acc[n][q] = fmaf(part[q], m * s, acc[n][q]);
+          for (int q = 0; q < 4; ++q) {   // rows g (gate: q = 0, 1) and g + 8 (up), tokens 2t and 2t + 1
+            const float s = scale_value<UE>(q < 2 ? sg[i] : su[i], kb), m = scale_value<UE>(sx[i][n][q & 1], kb);
+            acc[n][q] = fmaf(part[q], m * s, acc[n][q]);
+          }
         }
       }
     }
-  }
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) sums[warp][n][q][lane] = acc[n][q];
-  __syncthreads();
-  // thread -> (token, column): the column fastest, so that a token's 8 columns are stored together
-  for (int o = threadIdx.x; o < 8 * M; o += kWarps * 32) {
-    const int m = o / 8, j = o % 8, n = m / 8, from = j * 4 + (m % 8) / 2, q = m % 2;
-    float gs = 0.0f, us = 0.0f;
+      for (int q = 0; q < 4; ++q) sums[warp][n][q][lane] = acc[n][q];
+    __syncthreads();
+    // thread -> (token, column): the column fastest, so that a token's 8 columns are stored together
+    for (int o = threadIdx.x; o < 8 * M; o += kWarps * 32) {
+      const int m = o / 8, j = o % 8, n = m / 8, from = j * 4 + (m % 8) / 2, q = m % 2;
+      float gs = 0.0f, us = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      gs += sums[w][n][q][from];
-      us += sums[w][n][2 + q][from];
+      for (int w = 0; w < kWarps; ++w) {
+        gs += sums[w][n][q][from];
+        us += sums[w][n][2 + q][from];
+      }
+      if (GU) {
+        __nv_bfloat16* row = reinterpret_cast<__nv_bfloat16*>(GU) + (size_t)m * 2 * I;
+        row[j0 + j] = __float2bfloat16_rn(gs);
+        row[I + j0 + j] = __float2bfloat16_rn(us);
+      }
+      float h = silu_f32(gs) * us;
+      if (drop.threshold) h = dropout1(h, Philox(drop.rng)(((size_t)m * I + j0) / 8), j, drop.threshold, drop.scale);
+      if constexpr (OUT_F32)
+        static_cast<float*>(H)[(size_t)m * I + j0 + j] = h;
+      else
+        static_cast<__nv_bfloat16*>(H)[(size_t)m * I + j0 + j] = __float2bfloat16_rn(h);
     }
-    if (GU) {
-      __nv_bfloat16* row = reinterpret_cast<__nv_bfloat16*>(GU) + (size_t)m * 2 * I;
-      row[j0 + j] = __float2bfloat16_rn(gs);
-      row[I + j0 + j] = __float2bfloat16_rn(us);
+  };
+  if constexpr (CAPPED) {
+    for (int j0 = blockIdx.x * 8; j0 < I; j0 += gridDim.x * 8) {
+      columns(j0);
+      __syncthreads();   // the sums have been read
     }
-    float h = silu_f32(gs) * us;
-    if (drop.threshold) h = dropout1(h, Philox(drop.rng)(((size_t)m * I + j0) / 8), j, drop.threshold, drop.scale);
-    if constexpr (OUT_F32)
-      static_cast<float*>(H)[(size_t)m * I + j0 + j] = h;
-    else
-      static_cast<__nv_bfloat16*>(H)[(size_t)m * I + j0 + j] = __float2bfloat16_rn(h);
+  } else {
+    columns(blockIdx.x * 8);
   }
 }
 
@@ -164,15 +174,20 @@ __global__ void __launch_bounds__(FewPlan<NT>::kThreads, 2)
 
 cudaError_t launch_gated_few(const uint8_t* A, const void* sA, const uint8_t* B, const void* sB, void* H, uint16_t* GU,
                              const Dropout& drop, int M, int I, int K, bool out_f32, bool ue8m0, const StreamArgs& s) {
-  auto pick = [&](auto nt) {
+  const int grid = (int)s.limit.all(I / 8);
+  auto pick = [&](auto nt, auto capped) {
     constexpr int NT = decltype(nt)::value;
+    constexpr bool CAPPED = decltype(capped)::value;
     auto go = [&](auto kernel) {
-      return launch_plain(kernel, I / 8, FewPlan<NT>::kThreads, 0, s, A, sA, B, sB, H, GU, drop, M, I, K);
+      return launch_plain(kernel, grid, FewPlan<NT>::kThreads, 0, s, A, sA, B, sB, H, GU, drop, M, I, K);
     };
-    if (ue8m0) return out_f32 ? go(gated_few_kernel<true, true, NT>) : go(gated_few_kernel<true, false, NT>);
-    return out_f32 ? go(gated_few_kernel<false, true, NT>) : go(gated_few_kernel<false, false, NT>);
+    if (ue8m0) return out_f32 ? go(gated_few_kernel<true, true, NT, CAPPED>) : go(gated_few_kernel<true, false, NT, CAPPED>);
+    return out_f32 ? go(gated_few_kernel<false, true, NT, CAPPED>) : go(gated_few_kernel<false, false, NT, CAPPED>);
   };
-  return M <= 8 ? pick(std::integral_constant<int, 1>{}) : pick(std::integral_constant<int, 2>{});
+  auto pick_tokens = [&](auto capped) {
+    return M <= 8 ? pick(std::integral_constant<int, 1>{}, capped) : pick(std::integral_constant<int, 2>{}, capped);
+  };
+  return grid < I / 8 ? pick_tokens(std::true_type{}) : pick_tokens(std::false_type{});
 }
 
 }  // namespace dg

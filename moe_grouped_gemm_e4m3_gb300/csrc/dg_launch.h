@@ -50,19 +50,29 @@ cudaError_t launch_bs(const LaunchArgs& a, Mode mode);
 cudaError_t launch_bs_swiglu(const LaunchArgs& a);
 // The block-scaled K-grouped form (MN-major A and B).
 cudaError_t launch_bs_kgrouped(const LaunchArgs& a);
+// The CTAs that a launch may have on `sms` SMs with `per_sm` of them on each. Under dg_set_num_sms's cap it is one an SM:
+// the hardware deals CTAs out to every idle SM before it puts a second one on any.
+struct SmLimit {
+  int sms;
+  bool capped;
+  long long ctas(int per_sm) const { return capped ? sms : (long long)sms * per_sm; }
+  // as many as the work asks for, unless the SMs are capped
+  long long all(long long wanted) const { return capped && wanted > sms ? sms : wanted; }
+};
 // FP32 scale factors to packed UE8M0 words (dg_sf_transform.cu). A: [G][nkb][ldsa] ->
 // [G][ceil(nkb/4)][ldsa]; B: [rows][nkb] -> [rows][ceil(nkb/4)] (rows = G * nnb).
-cudaError_t launch_sf_pack_a(const float* sf, int32_t* out, int G, int nkb, int ldsa, int* status, int sms,
+cudaError_t launch_sf_pack_a(const float* sf, int32_t* out, int G, int nkb, int ldsa, int* status, SmLimit sms,
                              cudaStream_t stream);
-cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int nkb, int* status, int sms,
+cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int nkb, int* status, SmLimit sms,
                              cudaStream_t stream);
 // A's scales row-major [G][M][nkb] -> MN-major [G][nkb][ldsa] (rows m >= M zero).
-cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, cudaStream_t stream);
+cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, SmLimit sms,
+                                    cudaStream_t stream);
 // What the elementwise kernels' launches need: the stream, the SMs they may fill, whether they may start
 // before the previous kernel of the stream ends (they wait for it with griddepcontrol), and the cluster size.
 struct StreamArgs {
   cudaStream_t stream;
-  int sms;
+  SmLimit limit;
   bool pdl;
   int cluster = 1;
 };

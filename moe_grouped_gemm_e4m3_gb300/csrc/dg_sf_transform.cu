@@ -17,6 +17,7 @@
 // other value — not a power of two, negative, infinite or NaN — sets kStatusBadScale in the device
 // status word and packs as the code of the smallest power of two at or above its magnitude, clamped
 // to [0, 254] (127 for NaN).
+#include <climits>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -80,34 +81,38 @@ __global__ void sf_pack_b_kernel(const float* __restrict__ sf, int32_t* __restri
 }
 
 // Row-major A scales [G][M][nkb] -> MN-major [G][nkb][ldsa], rows m >= M zero: one 32x32 tile of the
-// (m, kb) plane per block of 32x8 threads, through shared memory so that both sides are coalesced.
+// (m, kb) plane at a time per block of 32x8 threads, through shared memory so that both sides are coalesced.
 __global__ void sf_a_to_mn_major_kernel(const float* __restrict__ in, float* __restrict__ out, int M, int nkb,
-                                        int ldsa) {
+                                        int ldsa, long long tiles) {
   __shared__ float tile[32][33];
-  const int g = blockIdx.z;
-  const int m0 = blockIdx.x * 32, k0 = blockIdx.y * 32;
-  const float* src = in + (size_t)g * M * nkb;
-  float* dst = out + (size_t)g * nkb * ldsa;
-  for (int r = threadIdx.y; r < 32; r += 8) {   // read rows m0 + r, columns k0 + threadIdx.x
-    const int m = m0 + r, kb = k0 + threadIdx.x;
-    tile[r][threadIdx.x] = (m < M && kb < nkb) ? src[(size_t)m * nkb + kb] : 0.0f;
-  }
-  __syncthreads();
-  for (int r = threadIdx.y; r < 32; r += 8) {   // write K-block k0 + r, rows m0 + threadIdx.x
-    const int kb = k0 + r, m = m0 + threadIdx.x;
-    if (kb < nkb && m < ldsa) dst[(size_t)kb * ldsa + m] = tile[threadIdx.x][r];
+  const int across = (ldsa + 31) / 32, down = (nkb + 31) / 32;
+  for (long long t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const long long g = t / across / down;
+    const int m0 = (int)(t % across) * 32, k0 = (int)(t / across % down) * 32;
+    const float* src = in + (size_t)g * M * nkb;
+    float* dst = out + (size_t)g * nkb * ldsa;
+    for (int r = threadIdx.y; r < 32; r += 8) {   // read rows m0 + r, columns k0 + threadIdx.x
+      const int m = m0 + r, kb = k0 + threadIdx.x;
+      tile[r][threadIdx.x] = (m < M && kb < nkb) ? src[(size_t)m * nkb + kb] : 0.0f;
+    }
+    __syncthreads();
+    for (int r = threadIdx.y; r < 32; r += 8) {   // write K-block k0 + r, rows m0 + threadIdx.x
+      const int kb = k0 + r, m = m0 + threadIdx.x;
+      if (kb < nkb && m < ldsa) dst[(size_t)kb * ldsa + m] = tile[threadIdx.x][r];
+    }
+    __syncthreads();
   }
 }
 
-int grid_for(long long words, int sms) {
+int grid_for(long long words, SmLimit sms) {
   const long long blocks = (words + 255) / 256;
-  const long long cap = 4LL * (sms > 0 ? sms : 1);
+  const long long cap = sms.ctas(4);
   return (int)(blocks < 1 ? 1 : (blocks < cap ? blocks : cap));
 }
 
 }  // namespace
 
-cudaError_t launch_sf_pack_a(const float* sf, int32_t* out, int G, int nkb, int ldsa, int* status, int sms,
+cudaError_t launch_sf_pack_a(const float* sf, int32_t* out, int G, int nkb, int ldsa, int* status, SmLimit sms,
                              cudaStream_t stream) {
   const long long words = (long long)G * ((nkb + 3) / 4) * ldsa;
   if (words == 0) return cudaSuccess;
@@ -115,14 +120,16 @@ cudaError_t launch_sf_pack_a(const float* sf, int32_t* out, int G, int nkb, int 
   return cudaGetLastError();
 }
 
-cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, cudaStream_t stream) {
-  if ((long long)G * ldsa * nkb == 0) return cudaSuccess;
-  const dim3 grid((unsigned)((ldsa + 31) / 32), (unsigned)((nkb + 31) / 32), (unsigned)G);
-  sf_a_to_mn_major_kernel<<<grid, dim3(32, 8), 0, stream>>>(in, out, M, nkb, ldsa);
+cudaError_t launch_sf_a_to_mn_major(const float* in, float* out, int G, int M, int nkb, int ldsa, SmLimit sms,
+                                    cudaStream_t stream) {
+  const long long tiles = (long long)G * ((ldsa + 31) / 32) * ((nkb + 31) / 32);
+  if (tiles == 0) return cudaSuccess;
+  const long long grid = sms.all(tiles < INT_MAX ? tiles : INT_MAX);
+  sf_a_to_mn_major_kernel<<<(unsigned)grid, dim3(32, 8), 0, stream>>>(in, out, M, nkb, ldsa, tiles);
   return cudaGetLastError();
 }
 
-cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int nkb, int* status, int sms,
+cudaError_t launch_sf_pack_b(const float* sf, int32_t* out, long long rows, int nkb, int* status, SmLimit sms,
                              cudaStream_t stream) {
   const long long words = rows * ((nkb + 3) / 4);
   if (words == 0) return cudaSuccess;
