@@ -271,6 +271,22 @@ def _shape(t, name):
     return t.shape
 
 
+def _size(v, name):
+    """An extent as the C entry points take it (ctypes would pass a larger one on modulo 2^32)."""
+    if v > 0x7FFFFFFF:
+        raise ValueError(f"{name} is {v}; the calls take extents below 2^31")
+    return v
+
+
+def _sizes(t, name):
+    """The shape of a tensor whose extents go to a C entry point."""
+    s = _shape(t, name)
+    for v in s:
+        if v > 0x7FFFFFFF:
+            _size(v, f"an extent of {name}")
+    return s
+
+
 def _expect(t, name, shape):
     """Raises ValueError unless tensor `t` has exactly `shape` (checked before any pointer is taken,
     so that a mis-shaped call never reaches a kernel, whose TMA boxes would read out of bounds)."""
@@ -348,7 +364,7 @@ _NT = ("dg_fp8_gemm_nt", "dg_fp8_gemm_nt_f32", "dg_fp8_gemm_nt_ue8m0", "dg_fp8_g
 
 def _dense_shapes(name, A, B):
     """(M, N, K) of a dense call: A [M, K], B [N, K] (or [1, N, K])."""
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 2:
         raise ValueError(f"A must be [M, K], got {list(a)}")
     if not (len(b) == 2 or (len(b) == 3 and b[0] == 1)):
@@ -363,7 +379,7 @@ def _dense_shapes(name, A, B):
 def _check_scales_2d(name, sA, sB, M, N, K):
     nks = _scale_k(name, K)
     _expect(sA, "sA", (nks, _align4(M)))
-    sb = _shape(sB, "sB")
+    sb = _sizes(sB, "sB")
     want = (_cdiv(N, 128), nks)
     if sb != want and sb != (1,) + want:
         raise ValueError(f"sB has shape {list(sb)}, expected {list(want)}")
@@ -410,7 +426,7 @@ def _contig(name, f32, A, sA, B, sB, m_indices, D, stream):
     if status is not None:
         _check(status)
         return D
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 2 or len(b) != 3:
         raise ValueError(f"contiguous layout: A must be [M_total, K] and B [G, N, K], got {list(a)} and {list(b)}")
     M, K = a
@@ -439,7 +455,7 @@ def dg_fp8_grouped_contiguous_f32(A, sA, B, sB, m_indices, D, stream=None):
 
 
 def _masked(name, f32, A, sA, B, sB, masked_m, D, stream):
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 3 or len(b) != 3:
         raise ValueError(f"masked layout: A must be [G, M_max, K] and B [G, N, K], got {list(a)} and {list(b)}")
     G, M_max, K = a
@@ -502,7 +518,7 @@ def _dense_layout(name, f32, A, sA, B, sB, D, M, N, K, stream):
         _check(status)
         return D
     a_t, b_n = _LAYOUTS[name[len("dg_fp8_gemm_"):len("dg_fp8_gemm_") + 2]]
-    M, N, K = int(M), int(N), int(K)
+    M, N, K = (_size(int(v), n) for v, n in ((M, "M"), (N, "N"), (K, "K")))
     nks, q, st = _scale_k(name, K), _fp8_types(), _scale_types(name)
     ptrs = _pointers((A, "A", q, (K, M) if a_t else (M, K)), (sA, "sA", st, (nks, _align4(M))),
                      (B, "B", q, (K, N) if b_n else (N, K)), (sB, "sB", st, (_cdiv(N, 128), nks)),
@@ -570,7 +586,7 @@ def _k_grouped(name, f32, A, sA, B, sB, k_offsets, D, stream):
     if status is not None:
         _check(status)
         return D
-    a, b, o = _shape(A, "A"), _shape(B, "B"), _shape(k_offsets, "k_offsets")
+    a, b, o = _sizes(A, "A"), _sizes(B, "B"), _sizes(k_offsets, "k_offsets")
     if len(a) != 2 or len(b) != 2 or len(o) != 1 or o[0] < 1:
         raise ValueError(f"K-grouped: A must be [K_total, M], B [K_total, N], k_offsets [G + 1]; got "
                          f"{list(a)}, {list(b)}, {list(o)}")
@@ -631,7 +647,7 @@ def _gated(name, f32, A, sA, B, sB, m_indices, H, GU, rng, p, stream):
     if status is not None:
         _check(status)
         return H
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 2 or len(b) != (3 if grouped else 2):
         raise ValueError(f"gated projection: A must be [M, K] and B {'[G, 2I, K]' if grouped else '[2I, K]'}, "
                          f"got {list(a)} and {list(b)}")
@@ -701,7 +717,7 @@ def _contig_nn(name, f32, A, sA, B, sB, m_indices, D, stream):
     if status is not None:
         _check(status)
         return D
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 2 or len(b) != 3:
         raise ValueError(f"contiguous NN: A must be [M_total, K] and B [G, K, N], got {list(a)} and {list(b)}")
     M, K = a
@@ -740,7 +756,7 @@ def _swiglu_backward(name, dH, GU, dGUr, sR, dGUc, sC, Hb, sHb, m_indices, rng, 
     if status is not None:
         _check(status)
         return dGUr, dGUc
-    h = _shape(dH, "dH")
+    h = _sizes(dH, "dH")
     if len(h) != 2:
         raise ValueError(f"dH must be [M, I], got {list(h)}")
     M, I = h
@@ -777,7 +793,7 @@ def _cast(name, X, Xr, sR, Xc, sC, Xb, sB, sBt, m_indices, stream):
     if status is not None:
         _check(status)
         return
-    x = _shape(X, "X")
+    x = _sizes(X, "X")
     if len(x) not in (2, 3):
         raise ValueError(f"X must be [M, N] or [G, M, N], got {list(x)}")
     M, N = x[-2:]
@@ -837,7 +853,7 @@ def dg_fp8_grouped_masked_swiglu_fp8(A, sA, B, sB, masked_m, Hq, sH, stream=None
     dequantisation scale amax/448 of each 1x128 group of each valid row; the A and sA layouts of
     dg_fp8_grouped_masked. Rows past masked_m are
     untouched in both."""
-    a, b = _shape(A, "A"), _shape(B, "B")
+    a, b = _sizes(A, "A"), _sizes(B, "B")
     if len(a) != 3 or len(b) != 3:
         raise ValueError(f"masked layout: A must be [G, M_max, K] and B [G, 2I, K], got {list(a)} and {list(b)}")
     G, M_max, K = a
@@ -872,7 +888,7 @@ def dg_transform_sf_into_ue8m0_a(sA, sA_packed, M, K, stream=None):
     -> packed UE8M0 words sA_packed [ceil(ceil(K/128)/4), align4(M)] (or [G, ...]) int32, on the GPU.
     A value that is not a power of two sets DG_DEV_BAD_SCALE (dg_get_device_status)."""
     import torch
-    s = _shape(sA, "sA")
+    s = _sizes(sA, "sA")
     if len(s) not in (2, 3):
         raise ValueError(f"sA must be [ceil(K/128), align4(M)] or [G, ceil(K/128), align4(M)], got {list(s)}")
     G = s[0] if len(s) == 3 else 1
@@ -887,7 +903,7 @@ def dg_transform_sf_a_into_mn_major(sA_rows, sA, M, K, stream=None):
     """A's FP32 scales row-major sA_rows [M, ceil(K/128)] (or [G, M, ceil(K/128)]) -> the MN-major
     layout of every call, sA [ceil(K/128), align4(M)] (or [G, ...]), padding rows zero, on the GPU."""
     import torch
-    s = _shape(sA_rows, "sA_rows")
+    s = _sizes(sA_rows, "sA_rows")
     if len(s) not in (2, 3):
         raise ValueError(f"sA_rows must be [M, ceil(K/128)] or [G, M, ceil(K/128)], got {list(s)}")
     G = s[0] if len(s) == 3 else 1
@@ -903,7 +919,7 @@ def dg_transform_sf_into_ue8m0_b(sB, sB_packed, N, K, stream=None):
     sB_packed [ceil(N/128), ceil(ceil(K/128)/4)] (or [G, ...]) int32, on the GPU. A value that is not a
     power of two sets DG_DEV_BAD_SCALE (dg_get_device_status)."""
     import torch
-    s = _shape(sB, "sB")
+    s = _sizes(sB, "sB")
     if len(s) not in (2, 3):
         raise ValueError(f"sB must be [ceil(N/128), ceil(K/128)] or [G, ceil(N/128), ceil(K/128)], got {list(s)}")
     G = s[0] if len(s) == 3 else 1
