@@ -5,11 +5,12 @@
 // computed in FP32 (product, then sum) and rounded once. R may be absent. The mask (dg_philox.cuh)
 // is a function of the seed, the offset and i, so the backward pass is the same call on dY without R.
 //
-// One counter serves eight consecutive elements (16 bytes of BF16, 32 of FP32). Bound by HBM. A large
-// tensor takes GROUPS such eights a thread, all loads ahead of the generator's arithmetic, and one
-// pass of the grid: with a resident grid that loops instead, 117M BF16 elements with a residual take 119 us, with
-// one pass 99.5 (7.1 TB/s) at 1 or 4 groups a thread; without the residual, where a thread has half the bytes in
-// flight, 87.6 at 1 group and 69.8 (6.7 TB/s) at 4.
+// One counter serves eight consecutive elements (16 bytes of BF16, 32 of FP32). Bound by HBM, in one pass of the grid: a
+// resident grid that loops takes 118 us where one pass takes 106 (117M BF16 elements with a residual, 6.7 TB/s), and 82 where it
+// takes 67 (59M FP32 without). A large tensor takes GROUPS such eights a thread, all loads ahead of the generator's
+// arithmetic, except BF16 with a residual, whose two loads a group are enough in flight (us at 1 group and at
+// several; 117M BF16 and 59M FP32 elements): BF16 without a residual 80 and 73, with one 106 and 112; FP32 67.8 and 67.4, with
+// one 98.9 and 97.9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -100,15 +101,16 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, const T* 
 
 template <typename T, bool VEC, bool RES>
 cudaError_t launch_shape(const T* x, const T* r, T* y, const Dropout& d, long long n, const StreamArgs& s) {
-  // several groups a thread once they still fill every SM four times over
+  // several groups a thread once they still fill every SM four times over (BF16 with a residual: one, see above)
   constexpr int kGroups = sizeof(T) == 2 ? 4 : 2;
   const long long eights = (n + 7) / 8;
   auto go = [&](auto kernel, auto capped, int groups) {
     const long long per = (long long)kThreads * groups, blocks = (eights + per - 1) / per, grid = s.limit.all(blocks);
     return launch_plain(grid < blocks ? capped : kernel, (int)grid, kThreads, 0, s, x, r, y, d, n);
   };
-  if (VEC && eights >= 4LL * s.limit.sms * kThreads * kGroups)
-    return go(dropout_kernel<T, VEC, RES, kGroups, false>, dropout_kernel<T, VEC, RES, kGroups, true>, kGroups);
+  if constexpr (VEC && !(RES && sizeof(T) == 2))
+    if (eights >= 4LL * s.limit.sms * kThreads * kGroups)
+      return go(dropout_kernel<T, VEC, RES, kGroups, false>, dropout_kernel<T, VEC, RES, kGroups, true>, kGroups);
   return go(dropout_kernel<T, VEC, RES, 1, false>, dropout_kernel<T, VEC, RES, 1, true>, 1);
 }
 
