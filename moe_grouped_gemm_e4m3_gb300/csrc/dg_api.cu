@@ -62,9 +62,9 @@ bool cluster_split_setting() {
 }
 
 // Programmatic dependent launch: 0 never, 1 always (DG_PDL, dg_set_pdl), or by default where a launch is at
-// most one wave of tiles or elementwise. Between kernels in plain stream order the GPU took 2 us steps back to back: the
-// gated projection of 333x2304x2064 14.3 us in plain order and 12.6 started early, the backward of 200x1024x1024 (three
-// calls) 23.6 and 16.7. Over several waves it gains nothing (8192x4096x7168 over 8 experts 215 us and 221).
+// most one wave of tiles or elementwise. Between kernels in plain stream order the GPU takes 2 us steps back to back: the
+// gated projection of 333x2304x2064 12.5 us in plain order and 10.6 started early, the backward of 200x1024x1024 (three
+// calls) 28.2 and 18.8. Over several waves it gains nothing (8192x4096x7168 over 8 experts 196 us and 200).
 enum Pdl : int { kPdlOff = 0, kPdlOn = 1, kPdlShort = 2 };
 std::atomic<int> g_pdl{-1};
 int pdl_setting() {
@@ -256,8 +256,8 @@ struct Config {
 
 // gated: the gated projection, whose split-K exchange in clusters is priced anew (us: 0.8 + 0.2 a split for 64-column
 // tiles, 2.4 + 0.4 for 128-column ones, 1.4 + 0.4 block-scaled): the CTAs of a tile share the reduction, so it
-// grows slowly with the splits. With M = 333, 2I = 2304, K = 2064, block-scaled: 1/2/3/4/5 splits 14.8/13.0/11.8/11.9/12.0 us;
-// FP32 scales: 64-column tiles 1/2 splits 11.5/10.5, 128-column 3/5 splits 12.6/13.0. The plain calls keep their linear
+// grows slowly with the splits. With M = 333, 2I = 2304, K = 2064, block-scaled: 1/2/3/4/5 splits 14.7/12.9/11.6/11.9/11.9 us;
+// FP32 scales: 64-column tiles 1/2 splits 10.7/9.6, 128-column 1/2/3/4/5 splits 15.0/13.1/11.9/12.0/12.1. The plain calls keep their linear
 // term: another split count would change their bits.
 Config choose_config(int mode, int rows, int N, int K, int G, int num_sms, bool block_scaled = false,
                      bool gated = false) {
@@ -535,9 +535,9 @@ dg_status run_gemm(int mode, bool out_f32, const uint8_t* A, const void* sA, con
   Config cfg = choose_config(mode, rows, N, K, groups, sms, block_scaled, gated != nullptr);
   // A small gated projection with packed scales runs on the FP32-scale kernel's 64-column tiles, which read the
   // words as they are, where those are chosen for FP32 scales and make one wave: the block-scaled kernel has
-  // 128-column tiles only. Measured (us, 64-column tiles / block-scaled): 333x2304x2064 10.0 / 11.8, 128x2048x2048 8.5 / 9.4,
-  // 32x1024x1024 5.4 / 6.3, 700x768x7168 13.0 / 13.4, 1000x1280x1360 9.3 / 12.1, 40x2816x6000 8.6 / 9.8; the other way at 64x4096x7168
-  // 11.5 / 11.1 and 500x1536x4096 12.6 / 11.9.
+  // 128-column tiles only. Measured (us, 64-column tiles / block-scaled): 333x2304x2064 10.2 / 11.6, 128x2048x2048 8.8 / 9.5,
+  // 32x1024x1024 5.3 / 6.2, 700x768x7168 13.4 / 13.7, 1000x1280x1360 9.3 / 12.0, 40x2816x6000 9.5 / 10.3, 64x4096x7168 12.8 / 13.2;
+  // the other way 500x1536x4096 12.8 / 12.2, and without GU 17x4096x7168 13.2 / 12.4 and 32x4096x7168 12.1 / 11.6.
   bool packed_on_fp32 = false;
   if (gated && block_scaled) {
     const Config narrow = choose_config(mode, rows, N, K, groups, sms, false, true);

@@ -10,9 +10,11 @@
 // use the same one). The K-block's partial is scaled by sA·sB into FP32
 // accumulators, as in the tiled kernels; the warps' sums are added in warp order through shared
 // memory (deterministic). mma.sync is below tcgen05's rate by far, but the tensor pipe idles here
-// either way: the bound is the weights' read. 1x4096x7168: 7.5 us, 3.9 TB/s, about 2 us of it the launch; the tiled
-// kernel 12.8. From 17 tokens on (64 at 2I = 4096, K = 7168: 17 us) the tiled kernel takes over: 16 tokens cost 10.3
-// us here and 13.9 there, and each further 8 tokens read the activations once more per 16 weight rows.
+// either way: the bound is the weights' read. 1x4096x7168: 7.8 us, 3.8 TB/s, about 2 us of it the launch; the tiled
+// kernel 12.9. Measured (us, here / tiled; 2I = 4096, K = 7168 and 2I = K = 2048): FP32 scales 8 tokens 7.9 / 12.8 and 2.7 / 6.3,
+// 16 tokens 10.3 / 13.7 and 3.0 / 6.3; packed scales 8 tokens 7.8 / 12.1 and 2.5 / 6.1, 16 tokens 10.6 / 12.2 and 3.0 / 6.3.
+// Each further 8 tokens read the activations once more per 16 weight rows and take as many accumulators again, so the tiled
+// kernel has the rest (17 tokens 12.9 and 6.3, packed 12.4 and 6.4).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
