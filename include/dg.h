@@ -427,6 +427,139 @@ dg_status dg_dropout_f32(const float* X, const float* R, float* Y, const uint64_
                          dg_stream_t stream);
 
 /*
+ * The operators around the experts' products: the norms at a block's boundary, the router, the experts' layer for a few
+ * tokens and products with four-bit weights. Additions of this library, like the training operators above.
+ *
+ * One decoding step of a layer:  dg_residual_norm (the last block's output joins the stream; the norm before this block comes
+ * out as E4M3 rows);  the router's logits by any product;  dg_route_topk;  dg_fp8_moe_swiglu.
+ */
+
+/*
+ * The norms before and after a block, with its gate and residual scale, in one pass over X [M,N] (the stream) and
+ * B [M,N] (the block's output, or NULL):
+ *     P = B·ra·w_after, ra = 1/sqrt(mean(B^2) + eps)   (or P = B where w_after is NULL)
+ *     R = X + gate[m]·scale[n]·P                       (gate [M], scale [N]: 1 where NULL; R = X without B)
+ *     Y = R·r·W, r = 1/sqrt(mean(R^2) + eps)           (nothing where W is NULL)
+ * in FP32. X, B, R, Y are BF16 bits or FP32; the vectors FP32. R [M,N] receives the stream, rounded once (NULL: not
+ * wanted); Y is formed from the unrounded R and rounded once. Yq, sY: Y as E4M3 rows with scales [ceil(N/128)][align4(M)],
+ * cast from the FP32 Y as dg_cast_fp8 casts its row form (entries m >= M 0, packed 127); N a multiple of 16 then.
+ * rstd [M] (r) and rstd_after [M] (ra): for the backward pass, or NULL. R and Y may each be X or B itself (not both the same);
+ * outputs may not overlap otherwise. N at most 16384; any alignment of the element type (rows of 16-byte multiples that start on
+ * 16 bytes are faster). A row of zeros with eps = 0 gives NaN, as the formula does.
+ */
+dg_status dg_residual_norm_bf16(const uint16_t* X, const uint16_t* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, uint16_t* R, uint16_t* Y, uint8_t* Yq, float* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream);
+dg_status dg_residual_norm_bf16_ue8m0(const uint16_t* X, const uint16_t* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, uint16_t* R, uint16_t* Y, uint8_t* Yq, int32_t* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream);
+dg_status dg_residual_norm_f32(const float* X, const float* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, float* R, float* Y, uint8_t* Yq, float* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream);
+dg_status dg_residual_norm_f32_ue8m0(const float* X, const float* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, float* R, float* Y, uint8_t* Yq, int32_t* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream);
+
+/*
+ * Its backward pass. dY [M,N] is Y's gradient and dR [M,N] the gradient that reaches R from behind (either may be NULL);
+ * R, rstd, rstd_after as the forward pass left them. With xh = R·rstd, bh = B·rstd_after (or B), P as above:
+ *     G = dR + rstd·(dY·W - xh·mean(dY·W·xh))    dX = G              dW = sum_m dY·xh
+ *     dgate = sum_n scale·P·G    dscale = sum_m gate·P·G    Q = gate·scale·G
+ *     dB = rstd_after·(Q·w_after - bh·mean(Q·w_after·bh)), dw_after = sum_m Q·bh   (without w_after: dB = Q)
+ * Outputs are written, not added to; each may be NULL. dX (also the gradient of the residual path) and dB are rounded once and
+ * may each be one of the inputs itself. dgate [M]; dW, dscale, dw_after [N] in FP32, summed in an order that depends on
+ * M and N alone (with M = 0 they are zero). workspace: device memory of at least
+ * dg_residual_norm_backward_workspace(M, N) bytes, 16-byte aligned, of this call alone until it has finished (needed only with
+ * dW, dscale or dw_after).
+ */
+dg_status dg_residual_norm_backward_bf16(const uint16_t* dY, const uint16_t* dR, const uint16_t* R, const uint16_t* B, const float* W,
+                                         const float* w_after, const float* gate, const float* scale, const float* rstd,
+                                         const float* rstd_after, uint16_t* dX, uint16_t* dB, float* dW, float* dw_after, float* dgate,
+                                         float* dscale, void* workspace, long long workspace_bytes, int M, int N,
+                                         dg_stream_t stream);
+dg_status dg_residual_norm_backward_f32(const float* dY, const float* dR, const float* R, const float* B, const float* W,
+                                         const float* w_after, const float* gate, const float* scale, const float* rstd,
+                                         const float* rstd_after, float* dX, float* dB, float* dW, float* dw_after, float* dgate,
+                                         float* dscale, void* workspace, long long workspace_bytes, int M, int N,
+                                         dg_stream_t stream);
+
+/*
+ * The router: the k experts of each token from its logits [T,E] (FP32 or BF16), in descending order.
+ *   score: softmax over the E logits, or each one's sigmoid. Selected are the k largest of score + bias[e] (bias NULL: of
+ *   the logits), ties to the lowest index; scores closer than FP32 tells apart are settled in FP64. A logit that is NaN or -inf
+ *   and a bias of -inf are never selected; a token with fewer than k others gets ids of -1 with weight 0 in the last places.
+ *   weights [T,k] = factor·score of the selected (without the bias), with renormalize divided by their sum + 1e-20.
+ * The ids [T,k] are those dg_fp8_moe_swiglu takes. E at most 1024, k at most min(E, 32).
+ */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+dg_status dg_route_topk_bf16(const uint16_t* logits, const float* bias, int32_t* ids, float* weights, int score, int renormalize,
+                            double factor, int T, int E, int k, dg_stream_t stream);
+dg_status dg_route_topk_f32(const float* logits, const float* bias, int32_t* ids, float* weights, int score, int renormalize,
+                            double factor, int T, int E, int k, dg_stream_t stream);
+/* The gradient of the logits from that of the weights, [T,k]; ids as selected (-1: skipped; the same one twice: both count), score,
+   renormalize and factor as in the forward call. Every element of dlogits [T,E] is written; it may be logits itself. The selection
+   and the bias have no gradient. */
+dg_status dg_route_topk_backward_bf16(const float* dweights, const uint16_t* logits, const int32_t* ids, uint16_t* dlogits, int score,
+                                     int renormalize, double factor, int T, int E, int k, dg_stream_t stream);
+dg_status dg_route_topk_backward_f32(const float* dweights, const float* logits, const int32_t* ids, float* dlogits, int score,
+                                     int renormalize, double factor, int T, int E, int k, dg_stream_t stream);
+
+/*
+ * The experts' feed-forward layer for a few tokens (a decoding step): for each token t and each of its experts e = topk_ids[t,j]
+ *     d = A[t]·W1[e]^T,  h = silu(d[0:I])·d[I:2I],  (q, s) = the E4M3 cast of h in groups of 128,
+ *     Y[t] = sum_j topk_weights[t,j]·(q·s)·W2[e]^T
+ * with FP32 sums; Y rounded once (or FP32). The cast is that of dg_fp8_grouped_masked_swiglu_fp8 (packed form: power-of-two
+ * scales), so the layer is the grouped calls' own chain without their 128-row tiles, gather and combination. Only the weights of
+ * experts that some token uses are read, each once for every 32 tokens: it is made for decoding, and from where most experts
+ * have tens of tokens the grouped calls are faster.
+ *   A [T,K] E4M3, sA as for dg_fp8_gemm_nt (packed: dg_fp8_gemm_nt_ue8m0)
+ *   W1 [E,2I,K]: I gate rows, then I up rows; W2 [E,N,I]; sW1 [E][2I/128][ceil(K/128)], sW2 [E][ceil(N/128)][I/128]
+ *       (packed: [E][2I/128][ceil(ceil(K/128)/4)] and so on, as everywhere)
+ *   _mxfp4: W1 [E,2I,K/2], W2 [E,N,I/2] hold E2M1 codes, the even k in the low half of a byte (OCP MX: values 0, .5, 1, 1.5, 2,
+ *       3, 4, 6 and a sign bit); sW1 [E][2I][K/32], sW2 [E][N][I/32] one E8M0 byte per 32 of a row (255: NaN). sA FP32.
+ *   topk_ids [T,k] int32: -1 is no expert (a token of those alone gets Y = 0); others outside [0, E) set DG_DEV_BAD_GROUP_INDEX
+ *       and count as none. The same expert twice adds up. topk_weights [T,k] FP32.
+ *   Y [T,N] BF16 bits or FP32.
+ *   workspace: device memory of at least dg_fp8_moe_workspace(T, k, I) bytes, 16-byte aligned, of this call alone until it has
+ *       finished. (Calls with workspaces of their own may overlap; calls that share one may not.)
+ * K a multiple of 16 (_mxfp4: 32), I of 128, N of 16; A, W1, W2 16-byte aligned. E at most 1024, k at most 32. The host reads no
+ * ids, so the call can be captured. The ids, weights, W1, W2 and their scales may not be written by work that runs beside the call.
+ */
+dg_status dg_fp8_moe_swiglu(const uint8_t* A, const float* sA, const uint8_t* W1, const float* sW1, const uint8_t* W2,
+                              const float* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+dg_status dg_fp8_moe_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* W1, const float* sW1, const uint8_t* W2,
+                              const float* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+dg_status dg_fp8_moe_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* W1, const int32_t* sW1, const uint8_t* W2,
+                              const int32_t* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+dg_status dg_fp8_moe_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* W1, const int32_t* sW1, const uint8_t* W2,
+                              const int32_t* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+dg_status dg_fp8_moe_swiglu_mxfp4(const uint8_t* A, const float* sA, const uint8_t* W1, const uint8_t* sW1, const uint8_t* W2,
+                              const uint8_t* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+dg_status dg_fp8_moe_swiglu_mxfp4_f32(const uint8_t* A, const float* sA, const uint8_t* W1, const uint8_t* sW1, const uint8_t* W2,
+                              const uint8_t* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream);
+
+/*
+ * Products with four-bit weights for a few tokens: D[M,N] = A·B^T, A [M,K] E4M3 with sA as for dg_fp8_gemm_nt, B [N,K/2] E2M1 codes
+ * and sB [N][K/32] E8M0 bytes as for dg_fp8_moe_swiglu_mxfp4. FP32 sums, D rounded once (or FP32). B is read once for every
+ * 32 rows of A. K a multiple of 32, N of 8; A and B 16-byte, sB 4-byte aligned.
+ */
+dg_status dg_fp8_mxfp4_gemm_nt(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, uint16_t* D, int M, int N,
+                               int K, dg_stream_t stream);
+dg_status dg_fp8_mxfp4_gemm_nt_f32(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, float* D, int M, int N,
+                               int K, dg_stream_t stream);
+
+/* Bytes of workspace of the calls above (a function of their sizes alone; 0 for empty problems). */
+long long dg_residual_norm_backward_workspace(int M, int N);
+long long dg_fp8_moe_workspace(int T, int k, int I);
+
+/*
  * Accumulating dense GEMM: D = C + A·Bᵀ, the full definition of fp8_gemm_nt ("DeepGEMM: İnce
  * ölçeklendirmeyle temiz ve verimli FP8 GEMM çekirdekleri", tr.news.hada.io/topic?id=19459,
  * § "GEMM arayüzü ve yerleşim kısıtları": the kernels are named after D = C + A @ B, and

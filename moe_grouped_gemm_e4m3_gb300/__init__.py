@@ -22,6 +22,12 @@ The names mirror the C ABI:
 * ``dg_fp8_grouped_contiguous_nn(A, sA, B, sB, m_indices, D)``  contiguous layout with B stored [G, K, N]
 * ``dg_cast_fp8(X, Xr=, sR=, Xc=, sC=, Xb=, sB=, sBt=, m_indices=)``  BF16 to E4M3 with 1x128, 128x1 and 128x128 scales
 * ``dg_dropout(X, Y, rng, p, R=)``  Y = R + dropout(X) from a counter-based generator, BF16 or FP32
+* ``dg_residual_norm(X, W, B=, w_after=, gate=, scale=, R=, Y=, Yq=, sY=, ...)``  the norms before and after a block with its gate
+  and residual scale; ``dg_residual_norm_backward`` its gradients
+* ``dg_route_topk(logits, ids, weights, bias=, ...)``  the k experts of each token; ``dg_route_topk_backward``
+* ``dg_fp8_moe_swiglu(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y)``  the experts' layer for a few tokens (``_ue8m0``,
+  ``_mxfp4``: four-bit weights)
+* ``dg_fp8_mxfp4_gemm_nt(A, sA, B, sB, D)``  few tokens by four-bit weights
 * ``*_ue8m0`` variants take power-of-two scales as packed UE8M0 int32 words (four K-groups per
   word, byte j = K-group 4q+j): sA int32 [ceil(ceil(K/128)/4), align4(rows)] (masked: leading G),
   sB int32 [G, ceil(N/128), ceil(ceil(K/128)/4)]. They run the block-scaled tensor-core kernel.
@@ -65,10 +71,16 @@ __all__ = [
     "dg_fp8_grouped_contiguous_nn_f32", "dg_fp8_grouped_contiguous_nn_ue8m0",
     "dg_fp8_grouped_contiguous_nn_ue8m0_f32", "dg_swiglu_backward_fp8", "dg_swiglu_backward_fp8_ue8m0",
     "dg_cast_fp8", "dg_cast_fp8_ue8m0", "dg_dropout",
+    "dg_residual_norm", "dg_residual_norm_ue8m0", "dg_residual_norm_backward", "dg_route_topk",
+    "dg_route_topk_backward", "dg_fp8_moe_swiglu", "dg_fp8_moe_swiglu_f32", "dg_fp8_moe_swiglu_ue8m0",
+    "dg_fp8_moe_swiglu_ue8m0_f32", "dg_fp8_moe_swiglu_mxfp4", "dg_fp8_moe_swiglu_mxfp4_f32", "dg_fp8_mxfp4_gemm_nt",
+    "dg_fp8_mxfp4_gemm_nt_f32", "dg_residual_norm_backward_workspace", "dg_fp8_moe_workspace", "DG_SCORE_SOFTMAX",
+    "DG_SCORE_SIGMOID",
 ]
 
 DG_OK, DG_ERR_INVALID_ARG, DG_ERR_ALIGNMENT, DG_ERR_UNSUPPORTED, DG_ERR_CUDA, DG_ERR_DEVICE_STATUS = range(6)
 DG_DEV_BAD_GROUP_INDEX, DG_DEV_BAD_MASKED_M, DG_DEV_TIMEOUT, DG_DEV_BAD_SCALE = 0x1, 0x2, 0x4, 0x8
+DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
 
 # Every symbol include/dg.h declares (checked against the built library by the CPU tests).
 EXPORTED_SYMBOLS = (
@@ -95,6 +107,12 @@ EXPORTED_SYMBOLS = (
     "dg_fp8_grouped_contiguous_nn_f32", "dg_fp8_grouped_contiguous_nn_ue8m0",
     "dg_fp8_grouped_contiguous_nn_ue8m0_f32", "dg_swiglu_backward_fp8", "dg_swiglu_backward_fp8_ue8m0",
     "dg_cast_fp8", "dg_cast_fp8_ue8m0", "dg_dropout_bf16", "dg_dropout_f32",
+    "dg_residual_norm_bf16", "dg_residual_norm_bf16_ue8m0", "dg_residual_norm_backward_bf16", "dg_route_topk_bf16",
+    "dg_route_topk_backward_bf16", "dg_residual_norm_f32", "dg_residual_norm_f32_ue8m0",
+    "dg_residual_norm_backward_f32", "dg_route_topk_f32", "dg_route_topk_backward_f32", "dg_fp8_moe_swiglu",
+    "dg_fp8_moe_swiglu_f32", "dg_fp8_moe_swiglu_ue8m0", "dg_fp8_moe_swiglu_ue8m0_f32", "dg_fp8_moe_swiglu_mxfp4",
+    "dg_fp8_moe_swiglu_mxfp4_f32", "dg_fp8_mxfp4_gemm_nt", "dg_fp8_mxfp4_gemm_nt_f32",
+    "dg_residual_norm_backward_workspace", "dg_fp8_moe_workspace",
 )
 
 
@@ -175,6 +193,24 @@ def load(build_if_missing: bool = True):
     for name in ("dg_dropout_bf16", "dg_dropout_f32"):
         f = getattr(lib, name)
         f.restype, f.argtypes = i32, [P, P, P, P, f64, ctypes.c_longlong, P]
+    i64 = ctypes.c_longlong
+    for t in ("bf16", "f32"):
+        for ue in ("", "_ue8m0"):
+            f = getattr(lib, f"dg_residual_norm_{t}{ue}")
+            f.restype, f.argtypes = i32, [P] * 6 + [f64] + [P] * 6 + [i32, i32, P]
+        f = getattr(lib, f"dg_residual_norm_backward_{t}")
+        f.restype, f.argtypes = i32, [P] * 17 + [i64, i32, i32, P]
+        for name in ("dg_route_topk", "dg_route_topk_backward"):
+            f = getattr(lib, f"{name}_{t}")
+            f.restype, f.argtypes = i32, [P] * 4 + [i32, i32, f64, i32, i32, i32, P]
+    for f32 in ("", "_f32"):
+        for form in ("", "_ue8m0", "_mxfp4"):
+            f = getattr(lib, f"dg_fp8_moe_swiglu{form}{f32}")
+            f.restype, f.argtypes = i32, [P] * 10 + [i64] + [i32] * 6 + [P]
+        f = getattr(lib, f"dg_fp8_mxfp4_gemm_nt{f32}")
+        f.restype, f.argtypes = i32, [P] * 5 + [i32] * 3 + [P]
+    lib.dg_residual_norm_backward_workspace.restype, lib.dg_residual_norm_backward_workspace.argtypes = i64, [i32, i32]
+    lib.dg_fp8_moe_workspace.restype, lib.dg_fp8_moe_workspace.argtypes = i64, [i32, i32, i32]
     for name in ("dg_query_config", "dg_query_config_ue8m0"):
         f = getattr(lib, name)
         f.restype, f.argtypes = i32, [i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)]
@@ -190,6 +226,7 @@ def _check(status: int):
 class _NoBind:
     """Stands in for the short path where it is not built: every call goes through the checks below."""
     gated = dense = contiguous = k_grouped = backward = cast = dropout = staticmethod(lambda *a: None)
+    norm = norm_backward = route = moe = mxfp4 = gated
 
 
 @functools.cache
@@ -835,6 +872,255 @@ def dg_dropout(X, Y, rng, p, R=None, stream=None):
     f = load().dg_dropout_f32 if f32 else load().dg_dropout_bf16
     _check(f(pX, pR, pY, prng, p, X.numel(), _stream(stream)))
     return Y
+
+
+def _pointers_here(*tensors):
+    """_pointers of tensors that all have to be on the current device, whose stream the call is launched on."""
+    ptrs = _pointers(*tensors)
+    device = _torch().cuda.current_device()
+    for t, name, _, _ in tensors:
+        if t is not None and t.device.index != device:
+            raise ValueError(f"{name.rstrip('?')} is on {t.device}, the current device is cuda:{device}")
+    return ptrs
+
+
+def _workspace(nbytes, given, stream):
+    """(the tensor that keeps it, its pointer, its bytes): the caller's, or memory of torch's allocator on the call's stream, where
+    whatever reuses it comes after the call (and which a graph being captured owns)."""
+    torch = _torch()
+    if given is not None:
+        return given, _ptr(given, "workspace", (torch.uint8,)), given.numel()
+    if stream is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    else:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_raw(stream))
+        with torch.cuda.stream(s):
+            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return t, t.data_ptr(), nbytes
+
+
+def _matrix(t, name):
+    s = _sizes(t, name)
+    if len(s) != 2:
+        raise ValueError(f"{name} must be a matrix, got {list(s)}")
+    return s
+
+
+def _stream_types(t, name):
+    """The element types of a residual stream like `t`: (suffix of the entry point, types)."""
+    f32 = getattr(t, "dtype", None) in _f32()
+    return ("_f32", _f32()) if f32 else ("_bf16", _bf16())
+
+
+def _norm(ue, X, W, B, w_after, gate, scale, eps, R, Y, Yq, sY, rstd, rstd_after, stream):
+    status = _bind().norm(ue, X, B, w_after, gate, scale, W, eps, R, Y, Yq, sY, rstd, rstd_after, _raw(stream))
+    if status is not None:
+        _check(status)
+        return
+    M, N = _matrix(X, "X")
+    kind, dt = _stream_types(X, "X")
+    tail = "_ue8m0" if ue else ""
+    f, x = _f32(), (M, N)
+    pX, pB, pwa, pg, ps, pW, *out = _pointers_here(
+        (X, "X", dt, x), (B, "B?", dt, x), (w_after, "w_after?", f, (N,)), (gate, "gate?", f, (M,)), (scale, "scale?", f, (N,)),
+        (W, "W?", f, (N,)), (R, "R?", dt, x), (Y, "Y?", dt, x), (Yq, "Yq?", _fp8_types(), x),
+        (sY, "sY?", _scale_types(tail), (_scale_k(tail, N), _align4(M))), (rstd, "rstd?", f, (M,)), (rstd_after, "rstd_after?", f, (M,)))
+    _check(getattr(load(), f"dg_residual_norm{kind}{tail}")(pX, pB, pwa, pg, ps, pW, eps, *out, M, N, _stream(stream)))
+
+
+def dg_residual_norm(X, W=None, B=None, w_after=None, gate=None, scale=None, R=None, Y=None, Yq=None, sY=None, rstd=None,
+                     rstd_after=None, eps=1e-6, stream=None):
+    """The norms at a block's boundary: R = X + gate[m]·scale·P with P = B·ra·w_after (the norm after the block; P = B without
+    w_after), and Y = R·r·W (the norm before the next block), ra and r the reciprocal roots of the mean squares plus eps.
+    X, B, R, Y bfloat16 or float32 [M, N]; W, w_after, scale float32 [N]; gate float32 [M]. Outputs, each optional: R (may be X
+    or B), Y, Yq with sY [ceil(N/128), align4(M)] (Y as E4M3 rows, A of the products), and rstd, rstd_after float32 [M] for the
+    backward pass."""
+    _norm(0, X, W, B, w_after, gate, scale, eps, R, Y, Yq, sY, rstd, rstd_after, stream)
+
+
+def dg_residual_norm_ue8m0(X, W=None, B=None, w_after=None, gate=None, scale=None, R=None, Y=None, Yq=None, sY=None, rstd=None,
+                           rstd_after=None, eps=1e-6, stream=None):
+    """dg_residual_norm with power-of-two scales packed as UE8M0 words: sY int32 [ceil(N/512), align4(M)]."""
+    _norm(1, X, W, B, w_after, gate, scale, eps, R, Y, Yq, sY, rstd, rstd_after, stream)
+
+
+def dg_residual_norm_backward_workspace(M, N):
+    """Bytes of workspace that dg_residual_norm_backward needs at most for [M, N]."""
+    return int(load().dg_residual_norm_backward_workspace(_size(M, "M"), _size(N, "N")))
+
+
+def dg_residual_norm_backward(dY=None, R=None, rstd=None, W=None, dR=None, B=None, rstd_after=None, w_after=None, gate=None,
+                              scale=None, dX=None, dB=None, dW=None, dw_after=None, dgate=None, dscale=None, workspace=None,
+                              stream=None):
+    """dg_residual_norm's gradients from dY (Y's) and dR (what reaches R from behind; either may be None) and the saved R, rstd and
+    rstd_after: dX, dB like X; dW, dw_after, dscale float32 [N]; dgate float32 [M]; each optional, written and not added to. dX
+    and dB may be one of the inputs themselves. workspace: a uint8 tensor of dg_residual_norm_backward_workspace(M, N) bytes;
+    None takes it from torch's allocator."""
+    status = _bind().norm_backward(dY, dR, R, B, W, w_after, gate, scale, rstd, rstd_after, dX, dB, dW, dw_after, dgate, dscale,
+                                   workspace, _raw(stream))
+    if status is not None:
+        _check(status)
+        return
+    first = dY if dY is not None else dR
+    M, N = _matrix(first, "dY" if dY is not None else "dR")
+    kind, dt = _stream_types(first, "dY")
+    f, x = _f32(), (M, N)
+    ptrs = _pointers_here(
+        (dY, "dY?", dt, x), (dR, "dR?", dt, x), (R, "R?", dt, x), (B, "B?", dt, x), (W, "W?", f, (N,)), (w_after, "w_after?", f, (N,)),
+        (gate, "gate?", f, (M,)), (scale, "scale?", f, (N,)), (rstd, "rstd?", f, (M,)), (rstd_after, "rstd_after?", f, (M,)),
+        (dX, "dX?", dt, x), (dB, "dB?", dt, x), (dW, "dW?", f, (N,)), (dw_after, "dw_after?", f, (N,)), (dgate, "dgate?", f, (M,)),
+        (dscale, "dscale?", f, (N,)))
+    need = dg_residual_norm_backward_workspace(M, N) if dW is not None or dw_after is not None or dscale is not None else 0
+    keep, pw, size = _workspace(need, workspace, stream)
+    _check(getattr(load(), f"dg_residual_norm_backward{kind}")(*ptrs, pw, size, M, N, _stream(stream)))
+
+
+_SCORES = {"softmax": DG_SCORE_SOFTMAX, "sigmoid": DG_SCORE_SIGMOID}
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score is {score!r}, expected one of {list(_SCORES)}")
+    return _SCORES[score]
+
+
+def dg_route_topk(logits, ids, weights, bias=None, score="softmax", renormalize=True, factor=1.0, stream=None):
+    """The k experts of each token from its logits (float32 or bfloat16 [T, E]): ids int32 [T, k] and weights float32 [T, k], in
+    descending order of score + bias (bias float32 [E], in the selection alone; ties to the lowest index). score: "softmax" over the
+    logits or "sigmoid". weights = factor·score of the selected, divided by their sum if renormalize. Logits of -inf or NaN and
+    biases of -inf are not selected (places left: id -1, weight 0)."""
+    how = _score(score)
+    status = _bind().route(0, logits, bias, ids, weights, how, bool(renormalize), factor, _raw(stream))
+    if status is not None:
+        _check(status)
+        return ids, weights
+    T, E = _matrix(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    kind, dt = _stream_types(logits, "logits")
+    ptrs = _pointers_here((logits, "logits", dt, (T, E)), (bias, "bias?", _f32(), (E,)), (ids, "ids", _i32(), (T, k)),
+                          (weights, "weights", _f32(), (T, k)))
+    _check(getattr(load(), f"dg_route_topk{kind}")(*ptrs, how, bool(renormalize), factor, T, E, k, _stream(stream)))
+    return ids, weights
+
+
+def dg_route_topk_backward(dweights, logits, ids, dlogits, score="softmax", renormalize=True, factor=1.0, stream=None):
+    """The gradient of dg_route_topk's logits, every element of dlogits [T, E] (the logits' type; may be logits itself), from that of
+    its weights, float32 [T, k], and the ids it selected; score, renormalize and factor as there."""
+    how = _score(score)
+    status = _bind().route(1, logits, dweights, ids, dlogits, how, bool(renormalize), factor, _raw(stream))
+    if status is not None:
+        _check(status)
+        return dlogits
+    T, E = _matrix(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    kind, dt = _stream_types(logits, "logits")
+    ptrs = _pointers_here((dweights, "dweights", _f32(), (T, k)), (logits, "logits", dt, (T, E)), (ids, "ids", _i32(), (T, k)),
+                          (dlogits, "dlogits", dt, (T, E)))
+    _check(getattr(load(), f"dg_route_topk_backward{kind}")(*ptrs, how, bool(renormalize), factor, T, E, k, _stream(stream)))
+    return dlogits
+
+
+@functools.cache
+def _bytes():
+    import torch
+    return (torch.uint8,)
+
+
+def dg_fp8_moe_workspace(T, k, I):
+    """Bytes of workspace that dg_fp8_moe_swiglu needs."""
+    return int(load().dg_fp8_moe_workspace(_size(T, "T"), _size(k, "k"), _size(I, "I")))
+
+
+# (form, FP32 output) of the expert layer's entry points, as the short path numbers them: bit 0 FP32 output, then the weights' form
+_MOE = {f"dg_fp8_moe_swiglu{form}{f32}": 2 * i + j for i, form in enumerate(("", "_ue8m0", "_mxfp4")) for j, f32 in enumerate(("", "_f32"))}
+
+
+def _moe(name, A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream):
+    status = _bind().moe(_MOE[name], A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, _raw(stream))
+    if status is not None:
+        _check(status)
+        return Y
+    T, K = _matrix(A, "A")
+    w1, w2, ids = _sizes(W1, "W1"), _sizes(W2, "W2"), _matrix(topk_ids, "topk_ids")
+    four = "_mxfp4" in name
+    if len(w1) != 3 or len(w2) != 3:
+        raise ValueError(f"W1 must be [E, 2I, K] and W2 [E, N, I], got {list(w1)} and {list(w2)}")
+    E, I, N, k = w1[0], w1[1] // 2, w2[1], ids[1]
+    per = 2 if four else 1   # values a byte
+    if w1[1] % 2 or w1[2] * per != K or K % per:
+        raise ValueError(f"W1 has shape {list(w1)}, expected [E, 2I, {K // per}]")
+    if w2[0] != E or w2[2] * per != I:
+        raise ValueError(f"W2 has shape {list(w2)}, expected [{E}, N, {I // per}]")
+    f, q, st = _f32(), _fp8_types(), _scale_types(name)
+    if four:
+        q1, st1, s1, s2 = _bytes(), _bytes(), (E, 2 * I, K // 32), (E, N, I // 32)
+    else:
+        q1, st1, s1, s2 = q, st, (E, _cdiv(2 * I, 128), _scale_k(name, K)), (E, _cdiv(N, 128), _scale_k(name, I))
+    ptrs = _pointers_here(
+        (A, "A", q, (T, K)), (sA, "sA", st, (_scale_k(name, K), _align4(T))), (W1, "W1", q1, w1), (sW1, "sW1", st1, s1), (W2, "W2", q1, w2),
+        (sW2, "sW2", st1, s2), (topk_ids, "topk_ids", _i32(), (T, k)), (topk_weights, "topk_weights", f, (T, k)),
+        (Y, "Y", _d_types(name.endswith("_f32")), (T, N)))
+    keep, pw, size = _workspace(dg_fp8_moe_workspace(T, k, I), workspace, stream)
+    _check(getattr(load(), name)(*ptrs, pw, size, T, k, E, K, I, N, _stream(stream)))
+    return Y
+
+
+def dg_fp8_moe_swiglu(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    """The experts' layer for a few tokens: Y[t] = sum_j topk_weights[t, j]·W2[e]·cast(silu(W1g[e]·A[t])·(W1u[e]·A[t])), e =
+    topk_ids[t, j] (-1: none). A [T, K] E4M3, W1 [E, 2I, K] (gate rows, then up rows), W2 [E, N, I], with the grouped calls' scales;
+    h is cast to E4M3 in groups of 128. workspace: a uint8 tensor of dg_fp8_moe_workspace(T, k, I) bytes; None takes it from
+    torch's allocator. Only the chosen experts' weights are read; the ids stay on the device."""
+    return _moe("dg_fp8_moe_swiglu", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def dg_fp8_moe_swiglu_f32(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    return _moe("dg_fp8_moe_swiglu_f32", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def dg_fp8_moe_swiglu_ue8m0(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    """dg_fp8_moe_swiglu with packed UE8M0 scales (h cast with power-of-two scales)."""
+    return _moe("dg_fp8_moe_swiglu_ue8m0", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def dg_fp8_moe_swiglu_ue8m0_f32(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    return _moe("dg_fp8_moe_swiglu_ue8m0_f32", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def dg_fp8_moe_swiglu_mxfp4(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    """dg_fp8_moe_swiglu with four-bit weights: W1 uint8 [E, 2I, K/2], W2 uint8 [E, N, I/2] (E2M1, the even k in a byte's low half),
+    sW1 uint8 [E, 2I, K/32], sW2 uint8 [E, N, I/32] (E8M0); A and sA as there."""
+    return _moe("dg_fp8_moe_swiglu_mxfp4", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def dg_fp8_moe_swiglu_mxfp4_f32(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace=None, stream=None):
+    return _moe("dg_fp8_moe_swiglu_mxfp4_f32", A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, stream)
+
+
+def _mxfp4(name, A, sA, B, sB, D, stream):
+    f32 = name.endswith("_f32")
+    status = _bind().mxfp4(int(f32), A, sA, B, sB, D, _raw(stream))
+    if status is not None:
+        _check(status)
+        return D
+    M, K = _matrix(A, "A")
+    N = _matrix(B, "B")[0]
+    if K % 32:
+        raise ValueError(f"K is {K}; four-bit weights have groups of 32")
+    ptrs = _pointers_here((A, "A", _fp8_types(), (M, K)), (sA, "sA", _f32(), (_cdiv(K, 128), _align4(M))), (B, "B", _bytes(), (N, K // 2)),
+                          (sB, "sB", _bytes(), (N, K // 32)), (D, "D", _d_types(f32), (M, N)))
+    _check(getattr(load(), name)(*ptrs, M, N, K, _stream(stream)))
+    return D
+
+
+def dg_fp8_mxfp4_gemm_nt(A, sA, B, sB, D, stream=None):
+    """D [M, N] (bfloat16) = A·Bᵀ for a few rows of A [M, K] (E4M3, scales as dg_fp8_gemm_nt's) and four-bit weights: B uint8 [N, K/2]
+    (E2M1, the even k in a byte's low half), sB uint8 [N, K/32] (E8M0)."""
+    return _mxfp4("dg_fp8_mxfp4_gemm_nt", A, sA, B, sB, D, stream)
+
+
+def dg_fp8_mxfp4_gemm_nt_f32(A, sA, B, sB, D, stream=None):
+    """As dg_fp8_mxfp4_gemm_nt, storing the FP32 sums."""
+    return _mxfp4("dg_fp8_mxfp4_gemm_nt_f32", A, sA, B, sB, D, stream)
 
 
 def dg_fp8_grouped_masked_swiglu(A, sA, B, sB, masked_m, H, stream=None):

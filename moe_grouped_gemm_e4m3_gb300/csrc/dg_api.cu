@@ -912,6 +912,186 @@ dg_status run_swiglu_backward(const uint16_t* dH, const uint16_t* GU, const int3
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "SwiGLU backward launch");
 }
 
+// ---------------------------------------------------------------------------------------------
+// The operators around the experts' products.
+
+// Whether [a, a + na) and [b, b + nb) share bytes (null: nothing).
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+dg_status check_norm_sizes(int M, int N) {
+  if (M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  if (N > dg::kNormMaxN) return fail(DG_ERR_UNSUPPORTED, "N is beyond " + std::to_string(dg::kNormMaxN));
+  return DG_OK;
+}
+
+dg_status run_norm(const void* X, const void* B, const float* w_after, const float* gate, const float* scale, const float* W,
+                   double eps, void* R, void* Y, uint8_t* Yq, void* sY, float* rstd, float* rstd_after, int M, int N,
+                   dg_stream_t stream, bool f32, bool ue8m0) {
+  t_last_error.clear();
+  dg_status s = check_norm_sizes(M, N);
+  if (s != DG_OK) return s;
+  if (!(eps >= 0.0 && eps <= 3e38)) return fail(DG_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (M == 0 || N == 0) return DG_OK;
+  if (!X) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  if (!B && (w_after || gate || scale || R || rstd_after))
+    return fail(DG_ERR_INVALID_ARG, "w_after, gate, scale, R and rstd_after go with a block's output B");
+  if (rstd_after && !w_after) return fail(DG_ERR_INVALID_ARG, "rstd_after goes with w_after");
+  if (!W && (Y || Yq || sY || rstd)) return fail(DG_ERR_INVALID_ARG, "Y, Yq and rstd go with W");
+  if ((s = check_form("rows of Y", Yq, sY)) != DG_OK) return s;
+  if (!R && !Y && !Yq) return fail(DG_ERR_INVALID_ARG, "no output asked for");
+  if (Yq && N % 16 != 0) return fail(DG_ERR_ALIGNMENT, "N must be a multiple of 16 for E4M3 rows (16-byte rows of codes)");
+  const uintptr_t size = f32 ? 4 : 2;
+  for (const void* p : {X, B, (const void*)R, (const void*)Y})
+    if (!aligned(p, size)) return fail(DG_ERR_ALIGNMENT, "X, B, R and Y must be aligned to their element");
+  for (const float* p : {w_after, gate, scale, W, (const float*)rstd, (const float*)rstd_after})
+    if (!aligned(p, 4)) return fail(DG_ERR_ALIGNMENT, "vectors must be 4-byte aligned");
+  const size_t bytes = (size_t)M * N * size;
+  for (const void* in : {X, B})
+    for (const void* out : {(const void*)R, (const void*)Y})
+      if (out != in && overlap(out, bytes, in, bytes))
+        return fail(DG_ERR_INVALID_ARG, "an output overlaps an input without being the same tensor");
+  if (overlap(R, bytes, Y, bytes)) return fail(DG_ERR_INVALID_ARG, "R and Y overlap");
+  for (const void* p : {X, B, (const void*)R, (const void*)Y})
+    if (overlap(Yq, (size_t)M * N, p, bytes)) return fail(DG_ERR_INVALID_ARG, "Yq overlaps another tensor");
+  dg::StreamArgs sa;
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const dg::NormArgs a{X, B, w_after, W, gate, scale, (float)eps, R, Y, Yq, sY, rstd, rstd_after, M, N};
+  const cudaError_t e = dg::launch_norm(a, f32, ue8m0, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "norm launch");
+}
+
+dg_status run_norm_backward(const void* dY, const void* dR, const void* R, const void* B, const float* W, const float* w_after,
+                            const float* gate, const float* scale, const float* rstd, const float* rstd_after, void* dX,
+                            void* dB, float* dW, float* dw_after, float* dgate, float* dscale, void* workspace,
+                            long long workspace_bytes, int M, int N, dg_stream_t stream, bool f32) {
+  t_last_error.clear();
+  dg_status s = check_norm_sizes(M, N);
+  if (s != DG_OK) return s;
+  if (N == 0) return DG_OK;
+  if (!dX && !dB && !dW && !dw_after && !dgate && !dscale) return fail(DG_ERR_INVALID_ARG, "no gradient asked for");
+  const int sums = (dW != nullptr) + (dscale != nullptr) + (dw_after != nullptr);
+  for (const float* p : {W, w_after, gate, scale, rstd, rstd_after, (const float*)dW, (const float*)dw_after, (const float*)dgate,
+                         (const float*)dscale})
+    if (!aligned(p, 4)) return fail(DG_ERR_ALIGNMENT, "vectors must be 4-byte aligned");
+  dg::StreamArgs sa;
+  if (M == 0) {   // sums over no rows
+    if (sums == 0) return DG_OK;
+    if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+    for (float* p : {dW, dw_after, dscale})
+      if (p) {
+        const cudaError_t e = cudaMemsetAsync(p, 0, (size_t)N * sizeof(float), sa.stream);
+        if (e != cudaSuccess) return fail_cuda(e, "cudaMemsetAsync");
+      }
+    return DG_OK;
+  }
+  if (!dY && !dR) return fail(DG_ERR_INVALID_ARG, "neither dY nor dR");
+  if (dY ? !R || !W || !rstd : dW != nullptr) return fail(DG_ERR_INVALID_ARG, "dY goes with R, W and rstd, and dW with dY");
+  if (!B && (w_after || gate || scale || dB || dw_after || dgate || dscale))
+    return fail(DG_ERR_INVALID_ARG, "w_after, gate, scale and their gradients go with a block's output B");
+  if (w_after && !rstd_after) return fail(DG_ERR_INVALID_ARG, "w_after goes with rstd_after");
+  if ((dw_after && !w_after) || (dgate && !gate) || (dscale && !scale))
+    return fail(DG_ERR_INVALID_ARG, "a gradient of an absent vector");
+  const uintptr_t size = f32 ? 4 : 2;
+  for (const void* p : {dY, dR, R, B, (const void*)dX, (const void*)dB})
+    if (!aligned(p, size)) return fail(DG_ERR_ALIGNMENT, "matrices must be aligned to their element");
+  const size_t bytes = (size_t)M * N * size;
+  for (const void* in : {dY, dR, R, B})
+    for (const void* out : {(const void*)dX, (const void*)dB})
+      if (out != in && overlap(out, bytes, in, bytes))
+        return fail(DG_ERR_INVALID_ARG, "an output overlaps an input without being the same tensor");
+  if (overlap(dX, bytes, dB, bytes)) return fail(DG_ERR_INVALID_ARG, "dX and dB overlap");
+  const long long need = dg::norm_backward_floats(M, N, sums) * (long long)sizeof(float);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(DG_ERR_INVALID_ARG, "the workspace holds " + std::to_string(workspace ? workspace_bytes : 0) + " bytes, this call needs " +
+                                        std::to_string(need) + " (dg_residual_norm_backward_workspace)");
+  if (!aligned(workspace, 16)) return fail(DG_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const dg::NormBackwardArgs a{dY, dR,    dY ? R : nullptr, B,        rstd, rstd_after, W, w_after, gate, scale, dX, dB, dgate,
+                               dW, dscale, dw_after,         static_cast<float*>(workspace), sums, M, N, 0, 0};
+  const cudaError_t e = dg::launch_norm_backward(a, f32, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "norm backward launch");
+}
+
+dg_status run_route(const void* logits, const float* bias, int32_t* ids, float* weights, const float* dweights, void* dlogits,
+                    int score, int renormalize, double factor, int T, int E, int k, dg_stream_t stream, bool bf16, bool backward) {
+  t_last_error.clear();
+  if (T < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  if (E < 1 || k < 1 || k > E) return fail(DG_ERR_INVALID_ARG, "k must be in [1, E]");
+  if (E > dg::kRouteMaxE || k > dg::kRouteMaxK)
+    return fail(DG_ERR_UNSUPPORTED, "at most " + std::to_string(dg::kRouteMaxE) + " experts and " + std::to_string(dg::kRouteMaxK) + " of them a token");
+  if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return fail(DG_ERR_INVALID_ARG, "score must be DG_SCORE_SOFTMAX or DG_SCORE_SIGMOID");
+  if (!std::isfinite((float)factor)) return fail(DG_ERR_INVALID_ARG, "factor must be finite");
+  if (T == 0) return DG_OK;
+  if (!logits || !ids || (backward ? !dweights || !dlogits : !weights)) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  const uintptr_t size = bf16 ? 2 : 4;
+  if (!aligned(logits, size) || !aligned(dlogits, size) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return fail(DG_ERR_ALIGNMENT, "tensors must be aligned to their element");
+  const size_t bytes = (size_t)T * E * size;
+  if (backward && dlogits != logits && overlap(dlogits, bytes, logits, bytes))
+    return fail(DG_ERR_INVALID_ARG, "dlogits overlaps logits without being the same tensor");
+  dg::StreamArgs sa;
+  const dg_status s = stream_args(stream, &sa);
+  if (s != DG_OK) return s;
+  const dg::RouteArgs a{logits, bias, ids, weights, dweights, dlogits, score == DG_SCORE_SIGMOID, renormalize != 0, (float)factor, T, E, k};
+  const cudaError_t e = dg::launch_route(a, bf16, backward, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "router launch");
+}
+
+dg_status run_moe(const uint8_t* A, const void* sA, const uint8_t* W1, const void* sW1, const uint8_t* W2, const void* sW2,
+                  const int32_t* topk_ids, const float* topk_weights, void* Y, void* workspace, long long workspace_bytes, int T, int k,
+                  int E, int K, int I, int N, dg_stream_t stream, dg::WeightForm form, bool out_f32) {
+  t_last_error.clear();
+  if (T < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  if (E < 1 || k < 1 || K < 1 || I < 1) return fail(DG_ERR_INVALID_ARG, "E, k, K and I must be positive");
+  if (E > dg::kMoeMaxE || k > dg::kMoeMaxK)
+    return fail(DG_ERR_UNSUPPORTED, "at most " + std::to_string(dg::kMoeMaxE) + " experts and " + std::to_string(dg::kMoeMaxK) + " of them a token");
+  const int k_step = form == dg::kMxfp4 ? 32 : 16;
+  if (K % k_step != 0 || I % 128 != 0 || N % 16 != 0)
+    return fail(DG_ERR_ALIGNMENT, "K must be a multiple of " + std::to_string(k_step) + ", I of 128 and N of 16");
+  if (T == 0 || N == 0) return DG_OK;
+  if (!A || !sA || !W1 || !sW1 || !W2 || !sW2 || !topk_ids || !topk_weights || !Y) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned(A, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(workspace, 16))
+    return fail(DG_ERR_ALIGNMENT, "A, W1, W2 and the workspace must be 16-byte aligned");
+  if (!aligned(sA, 4) || !aligned(sW1, 4) || !aligned(sW2, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(Y, out_f32 ? 4 : 2))
+    return fail(DG_ERR_ALIGNMENT, "scales, ids and weights must be 4-byte aligned, Y to its element");
+  if ((long long)T * k > INT_MAX / 2 || (long long)E * (I / 8) > INT_MAX / 2 || K > INT_MAX - 1024 || I > INT_MAX / 4 || N > INT_MAX - 1024 || T > INT_MAX - 1024)
+    return fail(DG_ERR_UNSUPPORTED, "too many tokens or columns");
+  const long long need = dg::moe_workspace_bytes(T, k, I);
+  if (!workspace || workspace_bytes < need)
+    return fail(DG_ERR_INVALID_ARG, "the workspace holds " + std::to_string(workspace ? workspace_bytes : 0) + " bytes, this call needs " +
+                                        std::to_string(need) + " (dg_fp8_moe_workspace)");
+  DeviceState* st = nullptr;
+  dg_status s = device_state(&st);
+  if (s != DG_OK) return s;
+  dg::StreamArgs sa;
+  if ((s = stream_args(stream, &sa)) != DG_OK) return s;
+  const dg::MoeArgs m{A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, st->status, T, k, E, K, I, N};
+  const cudaError_t e = dg::launch_moe(m, form, out_f32, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "expert layer launch");
+}
+
+dg_status run_mxfp4_gemm(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, void* D, int M, int N, int K,
+                         dg_stream_t stream, bool out_f32) {
+  t_last_error.clear();
+  if (M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
+  if (K < 1) return fail(DG_ERR_INVALID_ARG, "K must be positive");
+  if (K % 32 != 0 || N % 8 != 0) return fail(DG_ERR_ALIGNMENT, "K must be a multiple of 32 and N of 8");
+  if (M == 0 || N == 0) return DG_OK;
+  if (!A || !sA || !B || !sB || !D) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned(A, 16) || !aligned(B, 16)) return fail(DG_ERR_ALIGNMENT, "A and B must be 16-byte aligned");
+  if (!aligned(sA, 4) || !aligned(sB, 4) || !aligned(D, out_f32 ? 4 : 2))
+    return fail(DG_ERR_ALIGNMENT, "sA and sB must be 4-byte aligned, D to its element");
+  if (M > INT_MAX - 1024 || N > INT_MAX - 1024 || K > INT_MAX - 1024) return fail(DG_ERR_UNSUPPORTED, "a size is too large");
+  dg::StreamArgs sa;
+  const dg_status s = stream_args(stream, &sa);
+  if (s != DG_OK) return s;
+  const cudaError_t e = dg::launch_mxfp4_gemm(A, sA, B, sB, D, out_f32, M, N, K, sa);
+  return e == cudaSuccess ? DG_OK : fail_cuda(e, "four-bit product launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -1297,6 +1477,109 @@ dg_status dg_dropout_f32(const float* X, const float* R, float* Y, const uint64_
                          dg_stream_t stream) {
   return run_dropout(X, R, Y, true, rng, p, n, stream);
 }
+
+dg_status dg_residual_norm_bf16(const uint16_t* X, const uint16_t* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, uint16_t* R, uint16_t* Y, uint8_t* Yq, float* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream) {
+  return run_norm(X, B, w_after, gate, scale, W, eps, R, Y, Yq, sY, rstd, rstd_after, M, N, stream, false, false);
+}
+dg_status dg_residual_norm_bf16_ue8m0(const uint16_t* X, const uint16_t* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, uint16_t* R, uint16_t* Y, uint8_t* Yq, int32_t* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream) {
+  return run_norm(X, B, w_after, gate, scale, W, eps, R, Y, Yq, sY, rstd, rstd_after, M, N, stream, false, true);
+}
+dg_status dg_residual_norm_backward_bf16(const uint16_t* dY, const uint16_t* dR, const uint16_t* R, const uint16_t* B, const float* W,
+                                         const float* w_after, const float* gate, const float* scale, const float* rstd,
+                                         const float* rstd_after, uint16_t* dX, uint16_t* dB, float* dW, float* dw_after, float* dgate,
+                                         float* dscale, void* workspace, long long workspace_bytes, int M, int N,
+                                         dg_stream_t stream) {
+  return run_norm_backward(dY, dR, R, B, W, w_after, gate, scale, rstd, rstd_after, dX, dB, dW, dw_after, dgate, dscale, workspace,
+                           workspace_bytes, M, N, stream, false);
+}
+dg_status dg_route_topk_bf16(const uint16_t* logits, const float* bias, int32_t* ids, float* weights, int score, int renormalize,
+                            double factor, int T, int E, int k, dg_stream_t stream) {
+  return run_route(logits, bias, ids, weights, nullptr, nullptr, score, renormalize, factor, T, E, k, stream, true, false);
+}
+dg_status dg_route_topk_backward_bf16(const float* dweights, const uint16_t* logits, const int32_t* ids, uint16_t* dlogits, int score,
+                                     int renormalize, double factor, int T, int E, int k, dg_stream_t stream) {
+  return run_route(logits, nullptr, const_cast<int32_t*>(ids), nullptr, dweights, dlogits, score, renormalize, factor, T, E, k, stream,
+                   true, true);
+}
+dg_status dg_residual_norm_f32(const float* X, const float* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, float* R, float* Y, uint8_t* Yq, float* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream) {
+  return run_norm(X, B, w_after, gate, scale, W, eps, R, Y, Yq, sY, rstd, rstd_after, M, N, stream, true, false);
+}
+dg_status dg_residual_norm_f32_ue8m0(const float* X, const float* B, const float* w_after, const float* gate, const float* scale,
+                                const float* W, double eps, float* R, float* Y, uint8_t* Yq, int32_t* sY, float* rstd,
+                                float* rstd_after, int M, int N, dg_stream_t stream) {
+  return run_norm(X, B, w_after, gate, scale, W, eps, R, Y, Yq, sY, rstd, rstd_after, M, N, stream, true, true);
+}
+dg_status dg_residual_norm_backward_f32(const float* dY, const float* dR, const float* R, const float* B, const float* W,
+                                         const float* w_after, const float* gate, const float* scale, const float* rstd,
+                                         const float* rstd_after, float* dX, float* dB, float* dW, float* dw_after, float* dgate,
+                                         float* dscale, void* workspace, long long workspace_bytes, int M, int N,
+                                         dg_stream_t stream) {
+  return run_norm_backward(dY, dR, R, B, W, w_after, gate, scale, rstd, rstd_after, dX, dB, dW, dw_after, dgate, dscale, workspace,
+                           workspace_bytes, M, N, stream, true);
+}
+dg_status dg_route_topk_f32(const float* logits, const float* bias, int32_t* ids, float* weights, int score, int renormalize,
+                            double factor, int T, int E, int k, dg_stream_t stream) {
+  return run_route(logits, bias, ids, weights, nullptr, nullptr, score, renormalize, factor, T, E, k, stream, false, false);
+}
+dg_status dg_route_topk_backward_f32(const float* dweights, const float* logits, const int32_t* ids, float* dlogits, int score,
+                                     int renormalize, double factor, int T, int E, int k, dg_stream_t stream) {
+  return run_route(logits, nullptr, const_cast<int32_t*>(ids), nullptr, dweights, dlogits, score, renormalize, factor, T, E, k, stream,
+                   false, true);
+}
+dg_status dg_fp8_moe_swiglu(const uint8_t* A, const float* sA, const uint8_t* W1, const float* sW1, const uint8_t* W2,
+                              const float* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kFp8Scaled,
+                 false);
+}
+dg_status dg_fp8_moe_swiglu_f32(const uint8_t* A, const float* sA, const uint8_t* W1, const float* sW1, const uint8_t* W2,
+                              const float* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kFp8Scaled,
+                 true);
+}
+dg_status dg_fp8_moe_swiglu_ue8m0(const uint8_t* A, const int32_t* sA, const uint8_t* W1, const int32_t* sW1, const uint8_t* W2,
+                              const int32_t* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kFp8Packed,
+                 false);
+}
+dg_status dg_fp8_moe_swiglu_ue8m0_f32(const uint8_t* A, const int32_t* sA, const uint8_t* W1, const int32_t* sW1, const uint8_t* W2,
+                              const int32_t* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kFp8Packed,
+                 true);
+}
+dg_status dg_fp8_moe_swiglu_mxfp4(const uint8_t* A, const float* sA, const uint8_t* W1, const uint8_t* sW1, const uint8_t* W2,
+                              const uint8_t* sW2, const int32_t* topk_ids, const float* topk_weights, uint16_t* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kMxfp4,
+                 false);
+}
+dg_status dg_fp8_moe_swiglu_mxfp4_f32(const uint8_t* A, const float* sA, const uint8_t* W1, const uint8_t* sW1, const uint8_t* W2,
+                              const uint8_t* sW2, const int32_t* topk_ids, const float* topk_weights, float* Y, void* workspace,
+                              long long workspace_bytes, int T, int k, int E, int K, int I, int N, dg_stream_t stream) {
+  return run_moe(A, sA, W1, sW1, W2, sW2, topk_ids, topk_weights, Y, workspace, workspace_bytes, T, k, E, K, I, N, stream, dg::kMxfp4,
+                 true);
+}
+dg_status dg_fp8_mxfp4_gemm_nt(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, uint16_t* D, int M, int N,
+                               int K, dg_stream_t stream) {
+  return run_mxfp4_gemm(A, sA, B, sB, D, M, N, K, stream, false);
+}
+dg_status dg_fp8_mxfp4_gemm_nt_f32(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, float* D, int M, int N,
+                               int K, dg_stream_t stream) {
+  return run_mxfp4_gemm(A, sA, B, sB, D, M, N, K, stream, true);
+}
+long long dg_residual_norm_backward_workspace(int M, int N) {
+  return M <= 0 || N <= 0 || N > dg::kNormMaxN ? 0 : dg::norm_backward_floats(M, N, 3) * (long long)sizeof(float);
+}
+long long dg_fp8_moe_workspace(int T, int k, int I) { return T <= 0 || k <= 0 || I <= 0 ? 0 : dg::moe_workspace_bytes(T, k, I); }
 
 int dg_get_tma_aligned_size(int x, int elem_bytes) {
   if (x < 0 || (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4 && elem_bytes != 8 && elem_bytes != 16)) return -1;

@@ -96,6 +96,67 @@ cudaError_t launch_cast(const uint16_t* x, const int32_t* m_indices, const CastF
 cudaError_t launch_swiglu_backward(const uint16_t* dh, const uint16_t* gu, const int32_t* m_indices,
                                    const Dropout& d, const CastForms& dgu, const CastForms& h, int M, int I,
                                    bool ue8m0, const StreamArgs& s);
+// The norms at a block's boundary (dg_norm.cu): pointers to BF16 or FP32 rows of N, vectors of N or M in FP32; those of
+// absent parts are null.
+struct NormArgs {
+  const void *x, *b;
+  const float *w_after, *w, *gate, *scale;
+  float eps;
+  void *r, *y;
+  uint8_t* q;   // E4M3 rows of Y, and their scales
+  void* sq;
+  float *rstd, *rstd_after;
+  int M, N;
+};
+cudaError_t launch_norm(const NormArgs& a, bool f32, bool ue8m0, const StreamArgs& s);
+struct NormBackwardArgs {
+  const void *dy, *dr, *r, *b;
+  const float *rstd, *rstd_after, *w, *w_after, *gate, *scale;
+  void *dx, *db;
+  float *dgate, *dw, *dscale, *dw_after;
+  float* partial;   // the workspace: norm_backward_floats
+  int sums;         // how many of dw, dscale and dw_after
+  int M, N;
+  int parts, stages;   // set by launch_norm_backward
+};
+long long norm_backward_floats(int M, int N, int sums);
+cudaError_t launch_norm_backward(NormBackwardArgs a, bool f32, const StreamArgs& s);
+constexpr int kNormMaxN = 16384;
+// The router (dg_route.cu): logits [T, E] in FP32 or BF16.
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;            // [T, k]: written by the forward pass, read by the backward one
+  float* weights;          // [T, k]
+  const float* dweights;   // [T, k]
+  void* dlogits;
+  bool sigmoid, renorm;
+  float factor;
+  int T, E, k;
+};
+constexpr int kRouteMaxE = 1024, kRouteMaxK = 32;
+cudaError_t launch_route(const RouteArgs& a, bool bf16, bool backward, const StreamArgs& s);
+// Products of few tokens with streamed weights (dg_few.cu).
+enum WeightForm { kFp8Scaled, kFp8Packed, kMxfp4 };
+struct MoeArgs {
+  const uint8_t* A;
+  const void* sA;
+  const uint8_t* w1;
+  const void* s1;
+  const uint8_t* w2;
+  const void* s2;
+  const int32_t* ids;     // [T, k]
+  const float* weights;   // [T, k]
+  void* y;                // [T, N]
+  void* workspace;        // moe_workspace_bytes
+  int* status;
+  int T, k, E, K, I, N;
+};
+constexpr int kMoeMaxE = 1024, kMoeMaxK = 32;
+long long moe_workspace_bytes(int T, int k, int I);
+cudaError_t launch_moe(const MoeArgs& a, WeightForm form, bool out_f32, const StreamArgs& s);
+cudaError_t launch_mxfp4_gemm(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, void* D, bool out_f32, int M,
+                              int N, int K, const StreamArgs& s);
 // How many clusters of `cluster` CTAs of the dense / contiguous instantiation for (block_n,
 // out_f32) can be resident at once (0 if the query fails).
 int cluster_capacity_dense(int block_n, bool out_f32, int cluster);

@@ -1,0 +1,389 @@
+"""The norms at a block's boundary and their backward pass against the plain 64-bit definition (tests/_block_ref.py, where the
+bounds are derived), over sizes, alignments, types and which parts are present; differences; launch modes, streams and graphs."""
+import itertools
+
+import pytest
+import torch
+
+import _block_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def dg():
+    import moe_grouped_gemm_e4m3_gb300 as m
+    m.load()
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    yield m
+    assert m.dg_get_device_status() == 0
+
+
+def _cdiv(a, b):
+    return -(-a // b)
+
+
+def _align4(x):
+    return 4 * _cdiv(x, 4)
+
+
+def _data(M, N, dt, seed=0, after=True, gate=True, scale=True, block=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    d = dict(X=(2 * r(M, N)).to(dt), W=1 + 0.3 * r(N), B=(0.5 * r(M, N)).to(dt), w_after=1 + 0.3 * r(N), gate=torch.sigmoid(r(M)),
+             scale=0.2 * r(N), dY=r(M, N).to(dt), dR=r(M, N).to(dt))
+    d["X"][:, ::7] *= 8                                  # loud channels
+    if not block:
+        d.update(B=None, w_after=None, gate=None, scale=None)
+    for name, there in (("w_after", after), ("gate", gate), ("scale", scale)):
+        if not there:
+            d[name] = None
+    return d
+
+
+def _forward(dg, d, q=None, **extra):
+    """All outputs of the call, behind which no byte may change."""
+    M, N = d["X"].shape
+    dt = d["X"].dtype
+    f = lambda n: torch.full((n + 8,), 7.0, device="cuda")  # noqa: E731
+    m = lambda t: torch.full((M * N + 16,), 7.0, device="cuda").to(t)  # noqa: E731
+    bufs = dict(Y=m(dt), rstd=f(M))
+    if d["B"] is not None:
+        bufs["R"] = m(dt)
+    if d["w_after"] is not None:
+        bufs["rstd_after"] = f(M)
+    out = {n: b[:M * N].view(M, N) if n in "YR" else b[:M] for n, b in bufs.items()}
+    if q:
+        words = _cdiv(N, 512) if q == "ue8m0" else _cdiv(N, 128)
+        bufs["Yq"] = torch.full((M * N + 16,), 0x5A, dtype=torch.uint8, device="cuda")
+        out["Yq"] = bufs["Yq"][:M * N].view(M, N)
+        out["sY"] = torch.full((words, _align4(M)), -3, device="cuda", dtype=torch.int32 if q == "ue8m0" else F32)
+    call = dg.dg_residual_norm_ue8m0 if q == "ue8m0" else dg.dg_residual_norm
+    call(d["X"], d["W"], B=d["B"], w_after=d["w_after"], gate=d["gate"], scale=d["scale"], eps=EPS, **out, **extra)
+    torch.cuda.synchronize()
+    for n, b in bufs.items():
+        tail = b[out[n].numel():]
+        assert bool((tail == (0x5A if n == "Yq" else 7)).all()), f"{n} written past its end"
+    return out
+
+
+def _check_forward(out, d, q=None):
+    want = R.norm(d["X"], d["W"], d["B"], d["w_after"], d["gate"], d["scale"], EPS, d["X"].dtype)
+    for n in ("R", "Y", "rstd", "rstd_after"):
+        if n in out:
+            R.close(out[n], want[n], n)
+    if q:
+        M, N = d["X"].shape
+        codes, scales = R.cast_rows(*want["y"], q == "ue8m0")
+        n = _cdiv(N, 128)
+        if q == "ue8m0":
+            s = R.e8m0_words(out["sY"].t().contiguous(), n)
+            assert bool(((s[:M] == scales[0]) | (s[:M] == scales[1])).all())
+            assert bool((out["sY"][:, M:] == 0x7F7F7F7F).all())
+            rest = R.e8m0_words(out["sY"].t().contiguous(), 4 * out["sY"].shape[0])[:, n:]
+            assert bool((rest == 1).all())
+        else:
+            s = out["sY"].t().double()
+            R.close(s[:M], scales, "sY")
+            assert bool((out["sY"][:, M:] == 0).all())
+        got = out["Yq"].view(torch.float8_e4m3fn).double() * s[:M].repeat_interleave(128, 1)[:, :N]
+        R.close(got, codes, "Yq")
+
+
+SIZES = [(1, 1), (1, 8), (3, 7), (2, 64), (5, 130), (4, 272), (7, 1024), (3, 1032), (9, 2112), (2, 4096), (3, 4104), (5, 7168), (2, 8200),
+         (2, 16384), (1, 16383), (301, 96)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M,N", SIZES)
+def test_forward_sizes(dg, M, N, dt):
+    d = _data(M, N, dt)
+    q = "fp32" if N % 16 == 0 else None
+    _check_forward(_forward(dg, d, q), d, q)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("after,gate,scale", list(itertools.product([False, True], repeat=3)))
+@pytest.mark.parametrize("N", [400, 2112])
+def test_forward_parts(dg, N, after, gate, scale, dt):
+    d = _data(6, N, dt, after=after, gate=gate, scale=scale)
+    _check_forward(_forward(dg, d, "ue8m0"), d, "ue8m0")
+    d = _data(6, N, dt, block=False)
+    _check_forward(_forward(dg, d, "fp32"), d, "fp32")
+
+
+def test_the_last_norm_is_optional(dg):
+    d = _data(5, 200, BF)
+    want = _forward(dg, d)["R"]
+    out = torch.empty_like(want)
+    dg.dg_residual_norm(d["X"], None, B=d["B"], w_after=d["w_after"], gate=d["gate"], scale=d["scale"], R=out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("shift", [1, 3, 4])
+def test_any_alignment(dg, dt, shift):
+    M, N = 4, 264
+
+    def off(t):
+        b = torch.empty(t.numel() + shift, dtype=t.dtype, device="cuda")
+        b[shift:].copy_(t.reshape(-1))
+        return b[shift:].view(t.shape)
+
+    d = _data(M, N, dt)
+    moved = {n: off(t) for n, t in d.items()}
+    a, b = _forward(dg, d), _forward(dg, moved)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n          # the same order of operations
+    for at in ("X", "W"):                          # one tensor alone
+        c = _forward(dg, {**d, at: moved[at]})
+        assert all(torch.equal(a[n], c[n]) for n in a)
+    _check_backward(_backward(dg, moved), moved)
+
+
+def test_outputs_may_be_inputs(dg):
+    d = _data(9, 2112, BF)
+    want = _forward(dg, d)
+    x = d["X"].clone()
+    y = torch.empty_like(x)
+    dg.dg_residual_norm(x, d["W"], B=d["B"], w_after=d["w_after"], gate=d["gate"], scale=d["scale"], R=x, Y=y, eps=EPS)
+    assert torch.equal(x, want["R"]) and torch.equal(y, want["Y"])
+    x, b = d["X"].clone(), d["B"].clone()
+    dg.dg_residual_norm(x, d["W"], B=b, w_after=d["w_after"], gate=d["gate"], scale=d["scale"], R=x, Y=b, eps=EPS)
+    assert torch.equal(x, want["R"]) and torch.equal(b, want["Y"])
+
+
+def test_forward_special_rows(dg):
+    """Zeros, a NaN, an infinity: each row by itself."""
+    d = _data(8, 256, F32)
+    for n in ("X", "B"):
+        d[n][1] = 0
+    d["X"][3, 5] = float("nan")
+    d["X"][4, 200] = float("inf")
+    d["B"][5, 7] = float("nan")
+    out = _forward(dg, d, "fp32")
+    fine = [0, 1, 2, 6, 7]
+    part = {n: (t[fine] if t is not None and t.dim() == 2 else t) for n, t in d.items()}
+    part["gate"] = d["gate"][fine]
+    got = {n: (t[fine] if n != "sY" else t[:, fine + [0] * 3]) for n, t in out.items()}
+    want = R.norm(part["X"], part["W"], part["B"], part["w_after"], part["gate"], part["scale"], EPS, F32)
+    for n in ("R", "Y", "rstd", "rstd_after"):
+        R.close(got[n], want[n], n)
+    assert bool((out["Y"][1] == 0).all()) and bool((out["Yq"][1] == 0).all()) and bool((out["sY"][:, 1] == 1).all())
+    assert bool(torch.isnan(out["Y"][3]).all()) and bool(torch.isnan(out["Y"][5]).all()) and bool(torch.isnan(out["Y"][4, 200]))
+
+
+# ---------------------------------------------------------------------------------------- backward
+
+def _stats(d):
+    rs = (d["X"].double().square().mean(1) + EPS).rsqrt().float()
+    ra = None if d["w_after"] is None else (d["B"].double().square().mean(1) + EPS).rsqrt().float()
+    return rs, ra
+
+
+def _backward(dg, d, dy=True, dr=True, **extra):
+    M, N = d["X"].shape
+    rs, ra = _stats(d)
+    e = lambda *s: torch.full(s, 7.0, device="cuda")  # noqa: E731
+    out = dict(dX=torch.empty_like(d["X"]))
+    if dy:
+        out["dW"] = e(N)
+    if d["B"] is not None:
+        out["dB"] = torch.empty_like(d["X"])
+    for n, src, size in (("dw_after", "w_after", N), ("dgate", "gate", M), ("dscale", "scale", N)):
+        if d[src] is not None:
+            out[n] = e(size)
+    dg.dg_residual_norm_backward(d["dY"] if dy else None, d["X"] if dy else None, rs if dy else None, d["W"] if dy else None,
+                                 dR=d["dR"] if dr else None, B=d["B"], rstd_after=ra, w_after=d["w_after"], gate=d["gate"],
+                                 scale=d["scale"], **out, **extra)
+    return out
+
+
+def _check_backward(out, d, dy=True, dr=True):
+    rs, ra = _stats(d)
+    want = R.norm_backward(d["dY"] if dy else None, d["dR"] if dr else None, d["X"], rs, d["W"], d["B"], ra, d["w_after"], d["gate"],
+                           d["scale"], d["X"].dtype)
+    for n in out:
+        R.close(out[n], want[n], n)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M,N", SIZES + [(200, 1024), (700, 264), (1300, 40)])
+def test_backward_sizes(dg, M, N, dt):
+    d = _data(M, N, dt)
+    _check_backward(_backward(dg, d), d)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("dy,dr", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("after,gate,scale", list(itertools.product([False, True], repeat=3)))
+def test_backward_parts(dg, after, gate, scale, dy, dr, dt):
+    for N in (130, 400):
+        d = _data(160, N, dt, after=after, gate=gate, scale=scale)
+        _check_backward(_backward(dg, d, dy, dr), d, dy, dr)
+    d = _data(160, 400, dt, block=False)
+    _check_backward(_backward(dg, d, dy, dr), d, dy, dr)
+
+
+def test_backward_of_no_rows_is_zero(dg):
+    d = _data(0, 264, F32)
+    out = _backward(dg, d)
+    for n in ("dW", "dw_after", "dscale"):
+        assert bool((out[n] == 0).all())
+
+
+def test_backward_outputs_may_be_inputs(dg):
+    d = _data(300, 520, BF)
+    want = _backward(dg, d)
+    rs, ra = _stats(d)
+    for over in ("dY", "dR"):
+        c = {n: t.clone() for n, t in d.items()}
+        dg.dg_residual_norm_backward(c["dY"], c["X"], rs, c["W"], dR=c["dR"], B=c["B"], rstd_after=ra, w_after=c["w_after"], gate=c["gate"],
+                                     scale=c["scale"], dX=c[over], dB=c["B"])
+        assert torch.equal(c[over], want["dX"]) and torch.equal(c["B"], want["dB"])
+
+
+def test_backward_against_differences(dg):
+    """The forward call's own outputs, moved along random directions (FP32; differences of 2^-10 steps)."""
+    M, N = 6, 136
+    d = _data(M, N, F32, seed=3)
+    out = _forward(dg, d)
+    e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+    got = dict(dX=e(M, N), dB=e(M, N), dW=e(N), dw_after=e(N), dgate=e(M), dscale=e(N))
+    dg.dg_residual_norm_backward(d["dY"], out["R"], out["rstd"], d["W"], dR=d["dR"], B=d["B"], rstd_after=out["rstd_after"],
+                                 w_after=d["w_after"], gate=d["gate"], scale=d["scale"], **got)
+
+    def loss(v):
+        o = R.norm(v["X"], v["W"], v["B"], v["w_after"], v["gate"], v["scale"], EPS, F32)
+        return (o["Y"][0] * d["dY"].double()).sum() + (o["R"][0] * d["dR"].double()).sum()
+
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for name, grad in (("X", "dX"), ("B", "dB"), ("W", "dW"), ("w_after", "dw_after"), ("gate", "dgate"), ("scale", "dscale")):
+        v = torch.randn(d[name].shape, generator=g, device="cuda", dtype=torch.float64)
+        step = 2.0 ** -12
+        hi = loss({**d, name: d[name].double() + step * v})
+        lo = loss({**d, name: d[name].double() - step * v})
+        slope = float((hi - lo) / (2 * step))
+        along = float((got[grad].double() * v).sum())
+        # third-order term of a step of 2^-12 (values of order 10): below 2^-24·10^3; FP32 gradients: 2^-15 of the terms
+        size = float((got[grad].double() * v).abs().sum())
+        assert abs(slope - along) <= 2.0 ** -14 * size + 2.0 ** -13, (name, slope, along)
+
+
+def test_backward_workspaces(dg):
+    d = _data(200, 272, BF)
+    want = _backward(dg, d)
+    need = dg.dg_residual_norm_backward_workspace(200, 272)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = _backward(dg, d, workspace=ws[:need])
+    assert all(torch.equal(want[n], got[n]) for n in want) and bool((ws[need:] == 0xFF).all())
+    with pytest.raises(dg.DGError, match="workspace"):
+        _backward(dg, d, workspace=ws[:1024])
+
+
+# --------------------------------------------------------------------------- launches, streams, graphs
+
+def test_same_bits_under_every_launch_setting(dg):
+    """Sums do not depend on the SMs used, on early starts or on which path of the binding makes the call."""
+    d = _data(333, 1056, BF)
+    first = {**_forward(dg, d, "fp32"), **_backward(dg, d)}
+    before = dg.dg_get_pdl()
+    try:
+        for pdl, sms in ((True, 0), (False, 0), (None, 3), (None, 1)):
+            dg.dg_set_pdl(pdl)
+            dg.dg_set_num_sms(sms)
+            again = {**_forward(dg, d, "fp32"), **_backward(dg, d)}
+            assert all(torch.equal(first[n], again[n]) for n in first), (pdl, sms)
+    finally:
+        dg.dg_set_num_sms(0)
+        dg.dg_set_pdl(before)
+
+
+def test_both_paths_of_the_binding_make_the_same_call(dg, monkeypatch):
+    d = _data(21, 272, BF)
+    a = {**_forward(dg, d, "ue8m0"), **_backward(dg, d)}
+    assert dg._bind() is not dg._NoBind, "the short path is not built"
+    s = d["X"]
+    taken = dg._bind().norm(0, s, None, None, None, None, d["W"], EPS, None, torch.empty_like(s), None, None, None, None, None)
+    assert taken == 0
+    monkeypatch.setattr(dg, "_bind", lambda: dg._NoBind)
+    b = {**_forward(dg, d, "ue8m0"), **_backward(dg, d)}
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_streams_and_two_calls_at_once(dg):
+    ds = [_data(400, 2112, BF, seed=i) for i in range(2)]
+    want = [_backward(dg, d) for d in ds]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    for _ in range(5):
+        got = [_backward(dg, d, stream=s) for d, s in zip(ds, streams)]       # the call's own stream, not the current one
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            assert all(torch.equal(w[n], g[n]) for n in w)
+        with torch.cuda.stream(streams[0]):
+            g = _backward(dg, ds[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[0][n], g[n]) for n in g)
+
+
+def test_captured_and_replayed_on_new_values(dg):
+    d, other = _data(130, 1024, BF), _data(130, 1024, BF, seed=9)
+    rs, ra = _stats(d)
+    out = {n: torch.empty_like(d["X"]) for n in ("dX", "dB")}
+    out.update({n: torch.empty(1024, device="cuda") for n in ("dW", "dw_after", "dscale")}, dgate=torch.empty(130, device="cuda"))
+    st = {**{n: d[n].clone() for n in d}, "rs": rs, "ra": ra}
+
+    def call(o):
+        dg.dg_residual_norm_backward(st["dY"], st["X"], st["rs"], st["W"], dR=st["dR"], B=st["B"], rstd_after=st["ra"],
+                                     w_after=st["w_after"], gate=st["gate"], scale=st["scale"], **o)
+
+    call(out)
+    graphs, outs = [], []
+    for _ in range(2):                                       # two graphs, each with a workspace of its own
+        g, o = torch.cuda.CUDAGraph(), {n: torch.empty_like(t) for n, t in out.items()}
+        with torch.cuda.graph(g):
+            call(o)
+        graphs.append(g)
+        outs.append(o)
+    for n in d:
+        st[n].copy_(other[n])
+    r2, a2 = _stats(other)
+    st["rs"].copy_(r2)
+    st["ra"].copy_(a2)
+    call(out)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(out[n], o[n]) for n in out)
+
+
+def test_offsets_past_32_bits(dg):
+    """Rows behind the 2^31st element."""
+    M, N = 131080, 16384
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = torch.zeros(M, N, dtype=BF, device="cuda")
+    x[-3:] = torch.randn(3, N, device="cuda").to(BF)
+    w, y, rstd = torch.ones(N, device="cuda"), torch.empty_like(x), torch.empty(M, device="cuda")
+    dg.dg_residual_norm(x, w, Y=y, rstd=rstd, eps=EPS)
+    want = R.norm(x[-3:], w, None, None, None, None, EPS, BF)
+    R.close(y[-3:], want["Y"], "Y")
+    R.close(rstd[-3:], want["rstd"], "rstd")
+    assert not bool(y[:-3].any())
+    dw, dx = torch.empty(N, device="cuda"), y
+    dy = torch.zeros_like(x)
+    dy[-3:] = 1.0
+    dg.dg_residual_norm_backward(dy, x, rstd, w, dX=dx, dW=dw)
+    back = R.norm_backward(dy[-3:], None, x[-3:], rstd[-3:], w, None, None, None, None, None, BF)
+    R.close(dx[-3:], back["dX"], "dX")
+    terms = dy[-3:].double() * x[-3:].double() * rstd[-3:].double()[:, None]
+    R.close(dw, R.columns(terms, 2.0 ** -22 * terms.abs(), M), "dW")
