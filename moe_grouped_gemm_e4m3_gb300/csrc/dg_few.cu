@@ -34,8 +34,9 @@ namespace {
 
 enum Kind { kStreamUp, kStreamDown, kStreamDense };
 
-constexpr int kRows = 16, kUnitBytes = 128;                 // of a unit: weight rows, bytes of each
-constexpr int kStage = kRows * kUnitBytes + kRows * 12;     // codes, then scales (E2M1: 12 bytes a row; E4M3: two words)
+constexpr int kUnitBytes = 128;   // of a unit's rows
+// A stage of the ring holds a unit of R tiles of 16 rows: codes, then scales (E2M1: 12 bytes a row; E4M3: one or two words).
+constexpr int stage_bytes(int R) { return 16 * R * (kUnitBytes + 12); }
 
 struct FewArgs {
   const uint8_t* x;        // E4M3 rows: tokens (kStreamUp, kStreamDense) or the cast h of each (token, choice) (kStreamDown)
@@ -50,12 +51,6 @@ struct FewArgs {
   int K;                   // contraction
   int rows;                // weight rows an expert (kStreamUp: 2I)
 };
-
-__device__ __forceinline__ void mma_16x8x16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 // Two E4M3 codes (the low or high half of a word) as FP16.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t w) {
@@ -75,18 +70,12 @@ __device__ __forceinline__ void e2m1_x8(uint32_t w, uint32_t (&r)[4]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
 }
 
-__device__ __forceinline__ void copy_16(uint32_t to, const uint8_t* from, bool live) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+// (With no bytes the address is not read, and zeros are written.)
+__device__ __forceinline__ void copy_16(uint32_t to, const uint8_t* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_4(uint32_t to, const void* from, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ uint4 load_x(const uint8_t* p, bool live) {
-  return live ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-}
-__device__ __forceinline__ uint2 load_x8(const uint8_t* p, bool live) {
-  return live ? __ldg(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
 }
 
 // The tokens of one pass (at most 32 of them): which experts they use, and where each (expert, token) pair's h row is.
@@ -166,278 +155,401 @@ __device__ void build_routing(const Routing& r, const FewArgs& a, int t0, int to
   __syncthreads();
 }
 
-template <Kind KIND, WeightForm FORM, int NT, bool OUT_F32>
+// A place in a warp's sequence of units: an item of the CTA (kStreamUp: block `block` of the expert number `at`), for kStreamDown one of
+// the active experts (`at`, a walk over them inside the item), and a unit along K. A warp takes each W-th unit of every item of
+// its CTA. What depends on the item and the expert alone is computed where those change, so a step along K is a few additions.
+template <Kind KIND>
+struct Cursor {
+  int at, block, u;
+  __device__ __forceinline__ void start_item(int warp, int units_k, int active) {
+    u = warp;
+    if constexpr (KIND == kStreamDown) {
+      at = 0;
+      while (u >= units_k && at < active) u -= units_k, ++at;
+    }
+  }
+  __device__ __forceinline__ void start(int warp, int units_k, int active, int blocks) {
+    at = 0, block = blockIdx.x;
+    if constexpr (KIND == kStreamUp)
+      while (block >= blocks) block -= blocks, ++at;
+    start_item(warp, units_k, active);
+  }
+  __device__ __forceinline__ bool in_item(int units_k, int active) const { return KIND == kStreamDown ? at < active : u < units_k; }
+  __device__ __forceinline__ bool item_left(int active, int blocks) const { return KIND == kStreamUp ? at < active : block < blocks; }
+  __device__ __forceinline__ void next_item(int warp, int units_k, int active, int blocks) {
+    block += gridDim.x;
+    if constexpr (KIND == kStreamUp)
+      while (block >= blocks) block -= blocks, ++at;
+    start_item(warp, units_k, active);
+  }
+  // One unit on, within the item; whether the expert has changed.
+  __device__ __forceinline__ bool step(int W, int units_k, int active) {
+    u += W;
+    bool changed = false;
+    if constexpr (KIND == kStreamDown)
+      while (u >= units_k && at < active) u -= units_k, ++at, changed = true;
+    return changed;
+  }
+};
+
+// The tokens' side of a unit: this lane's bytes of its column's token, and the scales of the two tokens of its accumulators.
+template <int NT, bool FOUR>
+struct Operands {
+  uint32_t x[NT][FOUR ? 16 : 8];
+  float2 s[NT][FOUR ? 2 : 1];
+};
+
+__device__ __forceinline__ void mma_16x8x16(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0].x), "+f"(c[0].y), "+f"(c[1].x), "+f"(c[1].y)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four E8M0 codes of a word as FP32, two a conversion (code 0 is a subnormal, 255 NaN).
+__device__ __forceinline__ void e8m0_x4(uint32_t w, float (&v)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __nv_bfloat162_raw b = __nv_cvt_e8m0x2_to_bf162raw((__nv_fp8x2_storage_t)(w >> (16 * h)));
+    v[2 * h] = __uint_as_float((uint32_t)b.x << 16);
+    v[2 * h + 1] = __uint_as_float((uint32_t)b.y << 16);
+  }
+}
+
+template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
 __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const int stages) {
   extern __shared__ __align__(16) uint8_t ring_of_all[];
   constexpr bool kRouted = KIND != kStreamDense, kFour = FORM == kMxfp4;
-  constexpr int kUnitK = kFour ? 256 : 128;
+  constexpr int kUnitK = kFour ? 256 : 128, kRows = 16 * R, kStage = stage_bytes(R);
+  constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, W = blockDim.x / 32, g = lane / 4, t4 = lane % 4;
-  float* const sums = reinterpret_cast<float*>(ring_of_all + (size_t)W * stages * kStage);   // [2][W][NT][4][32]
-  const Routing route(reinterpret_cast<uint8_t*>(sums + 2 * W * NT * 128), a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
+  float* const sums = reinterpret_cast<float*>(ring_of_all + (size_t)W * stages * kStage);   // [2][W][R][NT][4][32]
+  const Routing route(reinterpret_cast<uint8_t*>(sums + 2 * W * R * NT * 128), a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
   const uint32_t ring = smem_u32(ring_of_all) + warp * stages * kStage;
   const uint8_t* const ring_at = ring_of_all + (size_t)warp * stages * kStage;
-  if constexpr (KIND != kStreamDown) griddep_wait();   // (kStreamDown reads weights and ids first: see launch_moe)
+  if constexpr (KIND != kStreamDown) griddep_wait();   // (kStreamDown reads weights and ids first: see launch_moe_form)
   griddep_launch_dependents();
 
   const int units_k = (a.K + kUnitK - 1) / kUnitK, groups_k = (a.K + 127) / 128;
-  const int row_bytes = kFour ? a.K / 2 : a.K, row_scales = a.K / 32;
-  const int blocks = KIND == kStreamUp ? a.rows / 16 : (a.rows + 15) / 16;   // items an expert (kStreamDown: in all)
+  const int row_bytes = kFour ? a.K / 2 : a.K, row_scales = a.K / 32, half = a.rows / 2;
+  const int blocks = (a.rows + kRows - 1) / kRows;   // of an expert's rows
   const int ldx = (a.T + 3) / 4 * 4;
+  // Row l of a block: gate and up rows by turns of eight (kStreamUp), or one after another.
+  auto row_of = [&](int block, int l) {
+    return KIND == kStreamUp ? block * 8 * R + (l >> 4) * 8 + (l & 7) + ((l & 8) ? half : 0) : block * kRows + l;
+  };
+  const int word_steps = FORM == kFp8Packed ? (groups_k + 3) / 4 : groups_k;   // E4M3 weights' scales along K
+  const uint8_t* const scales_end = static_cast<const uint8_t*>(a.sw) + (size_t)(kRouted ? a.E : 1) * a.rows * row_scales;
+  // where this lane copies to in a stage: chunk lane % 8 of rows lane / 8 + 4j
+  const int copy_row = lane / 8, copy_byte = (lane % 8) * 16;
+  const uint32_t to_even = copy_row * kUnitBytes + ((lane % 8) ^ copy_row) * 16, to_odd = (copy_row + 4) * kUnitBytes + ((lane % 8) ^ (copy_row + 4)) * 16;
+  const size_t four_rows = (size_t)4 * row_bytes, eight_rows = 2 * four_rows, half_rows = (size_t)half * row_bytes;
   bool waited = KIND != kStreamDown;
 
   for (int t0 = 0; t0 < a.T; t0 += 8 * NT) {
     const int tokens = a.T - t0 < 8 * NT ? a.T - t0 : 8 * NT;
     if constexpr (kRouted) build_routing(route, a, t0, tokens, KIND == kStreamDown);
     const int active = kRouted ? *route.count : 1;
-    const int items = KIND == kStreamUp ? active * blocks : blocks, per = KIND == kStreamDown ? active * units_k : units_k;
 
-    // The copies' place: an item and one of its units (the expert, and the unit along K).
-    int p_item = blockIdx.x, p_at = 0, p_u = warp, p_stage = 0;
-    auto settle = [&](int& item, int& at, int& u) {   // to the next unit that there is, when u has run past the row
-      if constexpr (KIND == kStreamDown) {
-        while (u >= units_k) {
-          u -= units_k;
-          if (++at >= active) {
-            at = 0, u = warp, item += gridDim.x;
-            while (u >= units_k && at < active) u -= units_k, ++at;
-            if (at >= active) item = items, at = 0, u = 0;   // this warp has no unit of any item
-            break;
-          }
-        }
-      } else if (u >= units_k) {
-        u = warp, item += gridDim.x;
-        if (u >= units_k) item = items;
-      }
-    };
-    auto first = [&](int& item, int& at, int& u) {
-      item = blockIdx.x, at = 0, u = warp;
-      if constexpr (KIND == kStreamDown) {
-        while (u >= units_k && at < active) u -= units_k, ++at;
-        if (at >= active) item = items;
-      } else if (u >= units_k) {
-        item = items;
-      }
-    };
-    first(p_item, p_at, p_u);
-    auto issue = [&]() {
-      if (p_item < items) {
-        const int expert = KIND == kStreamUp ? route.active[p_item / blocks] : KIND == kStreamDown ? route.active[p_at] : 0;
-        const int block = KIND == kStreamUp ? p_item % blocks : p_item;
-        const uint32_t to = ring + p_stage * kStage;
-        // rows 0..7 and 8..15 of the unit start here in the expert's matrix
-        const int lo = KIND == kStreamUp ? block * 8 : block * 16, hi = KIND == kStreamUp ? a.rows / 2 + lo : lo + 8;
-        const int r = lane / 8, c = lane % 8;
-        const int byte = p_u * kUnitBytes + c * 16;
-        const bool live = byte < row_bytes;
-        const size_t first_row = (size_t)expert * a.rows;
+    // ---- copies
+    Cursor<KIND> p{};
+    const uint8_t* p_from = a.w;                 // this lane's bytes of the unit's row `copy_row`
+    const uint8_t* p_scales[kFour ? kScaleCopies : 1];
+    int p_stage = 0;
+    auto copy_enter = [&]() {   // at another item or expert
+      const int expert = !kRouted ? 0 : route.active[p.at];
+      const size_t first_row = (size_t)expert * a.rows;
+      p_from = a.w + (first_row + row_of(p.block, copy_row)) * row_bytes + p.u * kUnitBytes + copy_byte;
+      if constexpr (kFour) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int local = r + 4 * j, row = j < 2 ? lo + local : hi + local - 8;
-          const bool there = live && (KIND != kStreamDense || row < a.rows);
-          copy_16(to + local * kUnitBytes + ((c ^ (local & 7)) * 16), there ? a.w + (first_row + row) * row_bytes + byte : a.w, there);
+        for (int i = 0; i < kScaleCopies; ++i) {
+          const int q = lane + 32 * i, l = q / 3, row = row_of(p.block, l);
+          const bool there = q < kRows * 3 && (KIND == kStreamUp || row < a.rows);
+          const size_t at = ((first_row + row) * row_scales & ~(size_t)3) + p.u * 8 + (q % 3) * 4;
+          p_scales[i] = there ? static_cast<const uint8_t*>(a.sw) + at : scales_end;
+        }
+      } else {
+        const int nb = row_of(p.block, (lane & 1) * 8) / 128;
+        p_scales[0] = static_cast<const uint8_t*>(a.sw) + (((size_t)expert * ((a.rows + 127) / 128) + nb) * word_steps) * 4;
+      }
+    };
+    auto issue = [&]() {
+      if (p.item_left(active, blocks)) {
+        const uint32_t to = ring + p_stage * kStage;
+        // rows copy_row + 4j, which kStreamUp takes from the gate half, the up half, and so on; zeros behind the end of K
+        const int bytes = p.u * kUnitBytes + copy_byte < row_bytes ? 16 : 0;
+        auto copy = [&](int j, int bytes) {
+          const size_t more = KIND == kStreamUp ? (j >> 2) * eight_rows + (j & 1) * four_rows + (j & 2 ? half_rows : 0) : j * four_rows;
+          copy_16(to + (j >> 1) * 8 * kUnitBytes + (j & 1 ? to_odd : to_even), p_from + more, bytes);
+        };
+        if (KIND == kStreamUp || (p.block + 1) * kRows <= a.rows) {
+#pragma unroll
+          for (int j = 0; j < 4 * R; ++j) copy(j, bytes);
+        } else {   // the last block of a number of rows that is no multiple
+#pragma unroll
+          for (int j = 0; j < 4 * R; ++j)
+            if (p.block * kRows + copy_row + 4 * j < a.rows) copy(j, bytes);
         }
         if constexpr (kFour) {
-          // eight scale bytes of each row from any place: the three aligned words that hold them
-          for (int q = lane; q < kRows * 3; q += 32) {
-            const int local = q / 3, row = local < 8 ? lo + local : hi + local - 8;
-            if (KIND != kStreamDense || row < a.rows) {
-              const size_t at = (first_row + row) * row_scales + p_u * 8, word = (at & ~(size_t)3) + (q % 3) * 4;
-              const size_t end = (size_t)(kRouted ? a.E : 1) * a.rows * row_scales;
-              const int bytes = word >= end ? 0 : end - word < 4 ? (int)(end - word) : 4;
-              copy_4(to + kRows * kUnitBytes + local * 12 + (q % 3) * 4, static_cast<const uint8_t*>(a.sw) + (bytes ? word : 0), bytes);
-            }
+          // eight scale bytes of each row from any place: the three aligned words that hold them, as far as there are any
+#pragma unroll
+          for (int i = 0; i < kScaleCopies; ++i) {
+            const ptrdiff_t left = scales_end - p_scales[i];
+            const int bytes = left >= 4 ? 4 : left > 0 ? (int)left : 0;
+            if (i * 32 + lane < kRows * 3) copy_4(to + kRows * kUnitBytes + (lane + 32 * i) * 4, bytes ? p_scales[i] : static_cast<const uint8_t*>(a.sw), bytes);
+            p_scales[i] += 8 * W;
           }
-        } else {
-          // the scales of both halves' 128-row blocks: an FP32 value each, or the packed word with this K-block's byte
-          if (lane < 2) {
-            const int ns = FORM == kFp8Packed ? (groups_k + 3) / 4 : groups_k, kq = FORM == kFp8Packed ? p_u / 4 : p_u;
-            const int nb = (lane == 0 ? lo : hi) / 128;
-            copy_4(to + kRows * kUnitBytes + lane * 4,
-                   static_cast<const uint32_t*>(a.sw) + ((size_t)expert * ((a.rows + 127) / 128) + nb) * ns + kq, 4);
-          }
+        } else if (lane < (KIND == kStreamUp ? 2 : 1)) {
+          // the scale of the rows' 128-row block (gate and up: two): an FP32 value, or the packed word with this K-block's byte
+          copy_4(to + kRows * kUnitBytes + lane * 4, p_scales[0] + (FORM == kFp8Packed ? p.u / 4 : p.u) * 4, 4);
         }
-        p_u += W;
-        settle(p_item, p_at, p_u);
+        p_from += W * kUnitBytes;
         if (++p_stage == stages) p_stage = 0;
+        const bool changed = p.step(W, units_k, active);
+        if (!p.in_item(units_k, active)) {
+          p.next_item(warp, units_k, active, blocks);
+          if (!p.in_item(units_k, active)) p.at = active, p.block = blocks;   // this warp has no unit of any item
+          if (p.item_left(active, blocks)) copy_enter();
+        } else if (changed) {
+          copy_enter();
+        }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    p.start(warp, units_k, active, blocks);
+    if (!p.in_item(units_k, active)) p.at = active, p.block = blocks;
+    if (p.item_left(active, blocks)) copy_enter();
+
+    // ---- the tokens' operands. Columns without a token, or whose token does not use the expert, read some row there is: their
+    // sums are dropped (`on`). Chunks behind the end of K, whose weights are zeros, read the row's last one.
+    const uint8_t* x_of[NT];     // this lane's bytes of its tokens' rows
+    uint32_t on = 0;             // bit 2i + c: token i·8 + 2·t4 + c has the expert
+    const float* s_of[NT][2];    // those tokens' scales, and (kStreamDown) weights
+    float weight_of[NT][2];
+    auto enter = [&](const Cursor<KIND>& c) {   // at another item or expert
+      const uint32_t mask = kRouted ? route.mask[route.active[c.at]] : 0xffffffffu;
+      const int first = KIND == kStreamDown ? route.first[c.at] : 0;
+      on = 0;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int t = i * 8 + g;
+        const bool live = t < tokens && (mask >> t & 1);
+        size_t row = (size_t)(t0 + (live ? t : 0));
+        if constexpr (KIND == kStreamDown) row = (size_t)t0 * a.k + route.row[live ? first + __popc(mask & ((1u << t) - 1)) : first];
+        x_of[i] = a.x + row * a.K;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tc = i * 8 + 2 * t4 + h;
+          const bool there = tc < tokens && (mask >> tc & 1);
+          if (there) on |= 1u << (2 * i + h);
+          if constexpr (KIND == kStreamDown) {
+            const int pair = there ? first + __popc(mask & ((1u << tc) - 1)) : first;
+            s_of[i][h] = static_cast<const float*>(a.sx) + ((size_t)t0 * a.k + route.row[pair]) * groups_k;
+            weight_of[i][h] = route.weight[pair];
+          } else {
+            s_of[i][h] = static_cast<const float*>(a.sx) + t0 + (there ? tc : 0);
+          }
+        }
+      }
+    };
+    auto load = [&](const Cursor<KIND>& c, Operands<NT, kFour>& o) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        if constexpr (kFour) {   // word t4 of each chunk of 32: eight consecutive values
+          const uint8_t* x = x_of[i] + c.u * 256 + t4 * 8;
+          if (c.u * 256 + 256 <= a.K) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + j * 32));
+              o.x[i][2 * j] = v.x, o.x[i][2 * j + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint2 v = __ldg(reinterpret_cast<const uint2*>(x_of[i] + min(c.u * 256 + j * 32, a.K - 32) + t4 * 8));
+              o.x[i][2 * j] = v.x, o.x[i][2 * j + 1] = v.y;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x_of[i] + min(c.u * 128 + t4 * 32 + h * 16, a.K - 16)));
+            o.x[i][4 * h] = v.x, o.x[i][4 * h + 1] = v.y, o.x[i][4 * h + 2] = v.z, o.x[i][4 * h + 3] = v.w;
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < (kFour ? 2 : 1); ++b) {
+          const int kb = kFour ? min(2 * c.u + b, groups_k - 1) : c.u;
+          float s[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (KIND == kStreamDown)
+              s[h] = s_of[i][h][kb] * weight_of[i][h];   // (written by the launch before: not through the read-only path)
+            else if constexpr (FORM == kFp8Packed)
+              s[h] = ue8m0_value(__ldg(reinterpret_cast<const uint32_t*>(s_of[i][h]) + (size_t)(kb >> 2) * ldx) >> (8 * (kb & 3)));
+            else
+              s[h] = __ldg(s_of[i][h] + (size_t)kb * ldx);
+          }
+          o.s[i][b] = make_float2(s[0], s[1]);
+        }
+      }
+    };
+
     for (int s = 0; s < stages - 1; ++s) issue();
     if constexpr (KIND == kStreamDown) {
       if (!waited) griddep_wait(), waited = true;
     }
-
+    Cursor<KIND> c;
+    c.start(warp, units_k, active, blocks);
     int stage = 0, buffer = 0;
-    for (int item = blockIdx.x; item < items; item += gridDim.x, buffer ^= 1) {
-      float acc[NT][4] = {};
-      int at = KIND == kStreamUp ? item / blocks : 0, u = warp;
-      if constexpr (KIND == kStreamDown)
-        while (u >= units_k && at < active) u -= units_k, ++at;
-      for (int n = warp; n < per; n += W) {
-        const uint32_t mask = kRouted ? route.mask[route.active[at]] : 0xffffffffu;
-        // the tokens' operands: column n·8 + g of this lane
-        const uint8_t* xs[NT];
-        bool live[NT];
-        float sx[NT][kFour ? 2 : 1][2];
-        bool on[NT][2];
+    for (; c.item_left(active, blocks); buffer ^= 1) {
+      const int item_at = c.at, item_block = c.block;
+      float2 acc[R][NT][2] = {};
+      uint32_t shift[kFour ? R : 1][2];   // E2M1: where the scale bytes of this lane's rows start in their words
+      auto shifts = [&]() {
+        if constexpr (kFour) {
+          const size_t first_row = (size_t)(kRouted ? route.active[c.at] : 0) * a.rows;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const int t = i * 8 + g;
-          live[i] = t < tokens && (mask >> t & 1);
-          size_t row = (size_t)(t0 + t);
-          if (KIND == kStreamDown && live[i]) row = (size_t)t0 * a.k + route.row[route.first[at] + __popc(mask & ((1u << t) - 1))];
-          xs[i] = a.x + (live[i] ? row : 0) * a.K;
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {   // the scales of the tokens of this lane's accumulators
-            const int tc = i * 8 + 2 * t4 + c;
-            const bool there = tc < tokens && (mask >> tc & 1);
-            on[i][c] = there;
-#pragma unroll
-            for (int b = 0; b < (kFour ? 2 : 1); ++b) {
-              const int kb = kFour ? 2 * u + b : u;
-              float s = 0.0f;
-              if (there && kb < groups_k) {
-                if constexpr (KIND == kStreamDown) {
-                  const int pair = route.first[at] + __popc(mask & ((1u << tc) - 1));
-                  s = static_cast<const float*>(a.sx)[((size_t)t0 * a.k + route.row[pair]) * groups_k + kb] * route.weight[pair];
-                } else if constexpr (FORM == kFp8Packed) {
-                  s = ue8m0_value(__ldg(static_cast<const uint32_t*>(a.sx) + (size_t)(kb / 4) * ldx + t0 + tc) >> (8 * (kb & 3)));
-                } else {
-                  s = __ldg(static_cast<const float*>(a.sx) + (size_t)kb * ldx + t0 + tc);
-                }
-              }
-              sx[i][b][c] = s;
-            }
-          }
+            for (int h = 0; h < 2; ++h) shift[r][h] = 8 * ((uint32_t)((first_row + row_of(c.block, r * 16 + h * 8 + g)) * row_scales) & 3);
         }
-        if (stages == 4) asm volatile("cp.async.wait_group 2;" ::: "memory");
-        else if (stages == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 0;" ::: "memory");   // (two stages)
-        __syncwarp();
+      };
+      if (c.in_item(units_k, active)) shifts(), enter(c);
+      while (c.in_item(units_k, active)) {
+        Operands<NT, kFour> o;
+        load(c, o);    // (from L1 or L2: behind the copies' addresses and the wait)
         issue();
+        if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");   // (two stages)
+        __syncwarp();
         const uint8_t* unit = ring_at + stage * kStage;
+        const int u = c.u;
         if constexpr (kFour) {
           // 8 groups of 32: a lane has word t4 of chunk j of its rows
-          const uint8_t* sc = unit + kRows * kUnitBytes;
-          uint32_t scales[2][2];   // of rows g and g + 8: eight bytes
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int local = g + 8 * h;
-            const int row = KIND == kStreamUp ? (item % blocks) * 8 + g + h * (a.rows / 2) : item * 16 + local;
-            const int expert = kRouted ? route.active[at] : 0;
-            const uint32_t shift = (uint32_t)(((size_t)expert * a.rows + row) * row_scales + u * 8) & 3;
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(sc + local * 12);
-            const uint32_t w0 = w[0], w1 = w[1], w2 = w[2];
-            scales[h][0] = __funnelshift_r(w0, w1, 8 * shift);
-            scales[h][1] = __funnelshift_r(w1, w2, 8 * shift);
-          }
+          for (int r = 0; r < R; ++r) {
+            const uint8_t* rows = unit + (r * 16 + g) * kUnitBytes + t4 * 4;
+            const uint32_t* sc = reinterpret_cast<const uint32_t*>(unit + kRows * kUnitBytes + (r * 16 + g) * 12);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float part[NT][4] = {};
+            for (int b = 0; b < 2; ++b) {
+              float s0[4], s1[4];
+              // (groups behind the end of K have bytes of another row: none, so that no NaN meets the zeros there)
+              const int left = a.K / 32 - u * 8 - b * 4;
+              const uint32_t there = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+              e8m0_x4(__funnelshift_r(sc[b], sc[b + 1], shift[r][0]) & there, s0);
+              e8m0_x4(__funnelshift_r(sc[24 + b], sc[25 + b], shift[r][1]) & there, s1);
+              float2 part[NT][2] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int chunk = b * 4 + j, k = u * 256 + chunk * 32 + t4 * 8;
-              const bool in = u * 256 + chunk * 32 < a.K;
-              uint32_t lo[4], hi[4];
-              e2m1_x8(*reinterpret_cast<const uint32_t*>(unit + g * kUnitBytes + ((chunk ^ g) * 16) + t4 * 4), lo);
-              e2m1_x8(*reinterpret_cast<const uint32_t*>(unit + (g + 8) * kUnitBytes + ((chunk ^ g) * 16) + t4 * 4), hi);
-              const float s0 = in ? ue8m0_value(scales[0][b] >> (8 * j)) : 0.0f, s1 = in ? ue8m0_value(scales[1][b] >> (8 * j)) : 0.0f;
-              const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+              for (int j = 0; j < 4; ++j) {
+                const int chunk = b * 4 + j;
+                uint32_t lo[4], hi[4];
+                e2m1_x8(*reinterpret_cast<const uint32_t*>(rows + ((chunk ^ g) * 16)), lo);
+                e2m1_x8(*reinterpret_cast<const uint32_t*>(rows + 8 * kUnitBytes + ((chunk ^ g) * 16)), hi);
+                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-              for (int i = 0; i < NT; ++i) {
-                const uint2 x = load_x8(xs[i] + k, live[i] && in);
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma_16x8x16(c, a0, e4m3_lo(x.x), e4m3_hi(x.x));
-                mma_16x8x16(c, a1, e4m3_lo(x.y), e4m3_hi(x.y));
-                part[i][0] = fmaf(c[0], s0, part[i][0]);
-                part[i][1] = fmaf(c[1], s0, part[i][1]);
-                part[i][2] = fmaf(c[2], s1, part[i][2]);
-                part[i][3] = fmaf(c[3], s1, part[i][3]);
+                for (int i = 0; i < NT; ++i) {
+                  const uint32_t x0 = o.x[i][2 * chunk], x1 = o.x[i][2 * chunk + 1];
+                  float2 m[2] = {};
+                  mma_16x8x16(m, a0, e4m3_lo(x0), e4m3_hi(x0));
+                  mma_16x8x16(m, a1, e4m3_lo(x1), e4m3_hi(x1));
+                  part[i][0].x = fmaf(m[0].x, s0[j], part[i][0].x);
+                  part[i][0].y = fmaf(m[0].y, s0[j], part[i][0].y);
+                  part[i][1].x = fmaf(m[1].x, s1[j], part[i][1].x);
+                  part[i][1].y = fmaf(m[1].y, s1[j], part[i][1].y);
+                }
               }
+#pragma unroll
+              for (int i = 0; i < NT; ++i)   // (the bits: 0·NaN of another token's expert)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  if (on >> (2 * i) & 1) acc[r][i][h].x = fmaf(part[i][h].x, o.s[i][b].x, acc[r][i][h].x);
+                  if (on >> (2 * i + 1) & 1) acc[r][i][h].y = fmaf(part[i][h].y, o.s[i][b].y, acc[r][i][h].y);
+                }
             }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (on[i][q & 1]) acc[i][q] = fmaf(part[i][q], sx[i][b][q & 1], acc[i][q]);   // (0·NaN of another token's expert)
           }
         } else {
           // one group of 128: a lane has 32 consecutive bytes of its rows
-          const int k = u * 128 + t4 * 32;
-          uint4 x[NT][2];
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) x[i][h] = load_x(xs[i] + k + 16 * h, live[i] && k + 16 * h < a.K);
-          float part[NT][4] = {};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 w0 = *reinterpret_cast<const uint4*>(unit + g * kUnitBytes + (((2 * t4 + h) ^ g) * 16));
-            const uint4 w1 = *reinterpret_cast<const uint4*>(unit + (g + 8) * kUnitBytes + (((2 * t4 + h) ^ g) * 16));
-            auto word = [&](uint32_t lo, uint32_t hi, auto of) {
-              const uint32_t f[4] = {e4m3_lo(lo), e4m3_lo(hi), e4m3_hi(lo), e4m3_hi(hi)};
-#pragma unroll
-              for (int i = 0; i < NT; ++i) mma_16x8x16(part[i], f, e4m3_lo(of(x[i][h])), e4m3_hi(of(x[i][h])));
-            };
-            word(w0.x, w1.x, [](const uint4& v) { return v.x; });
-            word(w0.y, w1.y, [](const uint4& v) { return v.y; });
-            word(w0.z, w1.z, [](const uint4& v) { return v.z; });
-            word(w0.w, w1.w, [](const uint4& v) { return v.w; });
-          }
           const uint32_t* sc = reinterpret_cast<const uint32_t*>(unit + kRows * kUnitBytes);
-          float s0, s1;
-          if constexpr (FORM == kFp8Packed)
-            s0 = ue8m0_value(sc[0] >> (8 * (u & 3))), s1 = ue8m0_value(sc[1] >> (8 * (u & 3)));
-          else
-            s0 = __uint_as_float(sc[0]), s1 = __uint_as_float(sc[1]);
+          const uint32_t c0 = sc[0], c1 = KIND == kStreamUp ? sc[1] : c0;
+          const float s0 = FORM == kFp8Packed ? ue8m0_value(c0 >> (8 * (u & 3))) : __uint_as_float(c0);
+          const float s1 = FORM == kFp8Packed ? ue8m0_value(c1 >> (8 * (u & 3))) : __uint_as_float(c1);
+          float2 part[R][NT][2] = {};
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              if (on[i][q & 1]) acc[i][q] = fmaf(part[i][q], (q < 2 ? s0 : s1) * sx[i][0][q & 1], acc[i][q]);   // (0·NaN, see above)
+            for (int r = 0; r < R; ++r) {
+              const uint8_t* rows = unit + (r * 16 + g) * kUnitBytes + (((2 * t4 + h) ^ g) * 16);
+              const uint4 w0 = *reinterpret_cast<const uint4*>(rows), w1 = *reinterpret_cast<const uint4*>(rows + 8 * kUnitBytes);
+              const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t f[4] = {e4m3_lo(lo[j]), e4m3_lo(hi[j]), e4m3_hi(lo[j]), e4m3_hi(hi[j])};
+#pragma unroll
+                for (int i = 0; i < NT; ++i) mma_16x8x16(part[r][i], f, e4m3_lo(o.x[i][4 * h + j]), e4m3_hi(o.x[i][4 * h + j]));
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const float2 f0 = __fmul2_rn(o.s[i][0], make_float2(s0, s0)), f1 = __fmul2_rn(o.s[i][0], make_float2(s1, s1));
+#pragma unroll
+            for (int r = 0; r < R; ++r) {   // (the bits: see above)
+              if (on >> (2 * i) & 1) {
+                acc[r][i][0].x = fmaf(part[r][i][0].x, f0.x, acc[r][i][0].x);
+                acc[r][i][1].x = fmaf(part[r][i][1].x, f1.x, acc[r][i][1].x);
+              }
+              if (on >> (2 * i + 1) & 1) {
+                acc[r][i][0].y = fmaf(part[r][i][0].y, f0.y, acc[r][i][0].y);
+                acc[r][i][1].y = fmaf(part[r][i][1].y, f1.y, acc[r][i][1].y);
+              }
+            }
+          }
         }
         __syncwarp();   // the stage is free for the copies of the next turn
         if (++stage == stages) stage = 0;
-        u += W;
-        if constexpr (KIND == kStreamDown)
-          while (u >= units_k && at < active) u -= units_k, ++at;
+        if (c.step(W, units_k, active) && c.in_item(units_k, active)) shifts(), enter(c);
       }
 
       // the warps' sums, in warp order (two buffers by turns: one barrier an item)
-      float* const mine = sums + (size_t)buffer * W * NT * 128;
+      float* const mine = sums + (size_t)buffer * W * R * NT * 128;
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mine[((warp * NT + i) * 4 + q) * 32 + lane] = acc[i][q];
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mine[(((warp * R + r) * NT + i) * 4 + q) * 32 + lane] = q & 1 ? acc[r][i][q >> 1].y : acc[r][i][q >> 1].x;
       __syncthreads();
-      auto sum = [&](int m, int row) {   // token m, row of the 16
-        const int q = (row / 8) * 2 + m % 2, from = ((m / 8) * 4 + q) * 32 + (row % 8) * 4 + (m % 8) / 2;
+      auto sum = [&](int m, int l) {   // token m, row l
+        const int q = ((l >> 3) & 1) * 2 + m % 2, from = (((l >> 4) * NT + m / 8) * 4 + q) * 32 + (l % 8) * 4 + (m % 8) / 2;
         float s = 0.0f;
-        for (int w = 0; w < W; ++w) s += mine[w * NT * 128 + from];
+        for (int w = 0; w < W; ++w) s += mine[w * R * NT * 128 + from];
         return s;
       };
       if constexpr (KIND == kStreamUp) {
-        const int act = item / blocks, j0 = (item % blocks) * 8;
-        const uint32_t mask = route.mask[route.active[act]];
-        for (int o = threadIdx.x; o < 8 * tokens; o += blockDim.x) {
-          const int m = o / 8, j = o % 8;
+        const uint32_t mask = route.mask[route.active[item_at]];
+        for (int o = threadIdx.x; o < 8 * R * tokens; o += blockDim.x) {
+          const int m = o / (8 * R), j = o % (8 * R);
           if (!(mask >> m & 1)) continue;
-          const size_t row = (size_t)t0 * a.k + route.row[route.first[act] + __popc(mask & ((1u << m) - 1))];
-          const float gate = sum(m, j), up = sum(m, 8 + j);
-          static_cast<float*>(a.out)[row * (a.rows / 2) + j0 + j] = silu_f32(gate) * up;
+          const size_t row = (size_t)t0 * a.k + route.row[route.first[item_at] + __popc(mask & ((1u << m) - 1))];
+          const int l = (j >> 3) * 16 + (j & 7);
+          const float gate = sum(m, l), up = sum(m, l + 8);
+          static_cast<float*>(a.out)[row * half + item_block * 8 * R + j] = silu_f32(gate) * up;
         }
       } else {
-        for (int o = threadIdx.x; o < 16 * tokens; o += blockDim.x) {
-          const int m = o / 16, j = o % 16, n = item * 16 + j;
-          if (n >= a.rows) continue;
+        for (int o = threadIdx.x; o < kRows * tokens; o += blockDim.x) {
+          const int m = o / kRows, j = o % kRows, col = item_block * kRows + j;
+          if (col >= a.rows) continue;
           const float v = sum(m, j);
-          const size_t to = (size_t)(t0 + m) * a.rows + n;
+          const size_t to = (size_t)(t0 + m) * a.rows + col;
           if constexpr (OUT_F32)
             static_cast<float*>(a.out)[to] = v;
           else
             static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(v);
         }
       }
+      c.at = item_at;
+      c.next_item(warp, units_k, active, blocks);
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
@@ -468,30 +580,39 @@ __global__ void __launch_bounds__(256) h_cast_kernel(const float* __restrict__ h
   }
 }
 
-// Warps a CTA: the number among which an item's units divide best. Sixteen warps an SM in all, with as many stages as fit.
+constexpr int kFewSms = 152;
+
+// How a launch is laid out: warps a CTA, CTAs an SM, stages of a warp's ring.
 struct FewPlan {
   int warps, ctas, stages;
   size_t smem;
+  double cost;
 };
-FewPlan few_plan(int units, int NT, size_t routing, const SmLimit& limit) {
-  FewPlan p{8, 0, 0, 0};
-  double least = 1e9;
-  for (int w : {8, 4, 16}) {
-    const double turns = (double)((units + w - 1) / w) * w / units;
-    if (turns < least - 0.02) least = turns, p.warps = w;
-  }
-  for (p.ctas = limit.capped ? 1 : 16 / p.warps;; --p.ctas)
+// Sixteen warps fill an SM, twelve on units of two tiles (whose stages are twice as large; 16 x 2 stages, 14 x 3 and 8 x 4 take 5% longer
+// than 12 x 3 for one token through 8 of 32 experts of 7168x2048, E4M3). The fewer warps run, the longer a step of each stays the same; so
+// the least of rounds of items x turns of a warp x warps. `items` are those of a whole GPU, whatever dg_set_num_sms says.
+FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, const SmLimit& limit) {
+  const int most = R == 2 ? 12 : 16;
+  FewPlan p{};
+  p.cost = 1e300;
+  for (int w = most; w >= 4; --w)
+    for (int c = 1; c * w <= most; ++c) {
+      const double rounds = (double)((items + (long long)kFewSms * c - 1) / ((long long)kFewSms * c));
+      const double cost = rounds * ((units + w - 1) / w) * most;
+      if (cost < p.cost * (1.0 - 1e-9)) p.cost = cost, p.warps = w, p.ctas = c;
+    }
+  if (limit.capped) p.ctas = 1;
+  for (;; --p.ctas)
     for (p.stages = 4; p.stages >= (p.ctas == 1 ? 2 : 3); --p.stages) {
-      p.smem = (size_t)p.warps * (p.stages * kStage + 2 * NT * 128 * sizeof(float)) + routing;
+      p.smem = (size_t)p.warps * (p.stages * stage_bytes(R) + 2 * R * NT * 128 * sizeof(float)) + routing;
       if (p.ctas * (p.smem + 1024) <= (size_t)227 << 10) return p;
     }
 }
 
-template <Kind KIND, WeightForm FORM, int NT, bool OUT_F32>
-cudaError_t launch_stream_nt(const FewArgs& a, int items, int units, const StreamArgs& s) {
-  auto kernel = stream_kernel<KIND, FORM, NT, OUT_F32>;
-  const int pairs = (a.T < 8 * NT ? a.T : 8 * NT) * a.k;
-  const FewPlan plan = few_plan(units, NT, Routing::bytes(a.E, pairs), s.limit);
+template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
+cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
+  auto kernel = stream_kernel<KIND, FORM, NT, R, OUT_F32>;
+  const int items = (rows + 16 * R - 1) / (16 * R);
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -505,11 +626,26 @@ cudaError_t launch_stream_nt(const FewArgs& a, int items, int units, const Strea
   return launch_plain(kernel, (int)(items < most ? items : most), plan.warps * 32, plan.smem, s, a, plan.stages);
 }
 
+// rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
+// Units of two tiles (32 rows) share the tokens' operands and the steps between them and cost about 1.5 of one tile (us, two and one:
+// 16 tokens through 64 experts 328 and 400, one token through 8 63.4 and 66.1). E2M1 weights, where conversions are most of the work, gain
+// nothing (1x7168x16384 20.5 and 18.3), and four column tiles leave no registers for them.
+template <Kind KIND, WeightForm FORM, int NT, bool OUT_F32>
+cudaError_t launch_stream_tokens(const FewArgs& a, int rows, int units, const StreamArgs& s) {
+  const size_t routing = Routing::bytes(a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
+  const FewPlan one = few_plan((rows + 15) / 16, units, NT, 1, routing, s.limit);
+  if constexpr (NT <= 2 && FORM != kMxfp4) {
+    const FewPlan two = few_plan((rows + 31) / 32, units, NT, 2, routing, s.limit);
+    if (1.5 * two.cost <= 1.1 * one.cost) return launch_stream_nt<KIND, FORM, NT, 2, OUT_F32>(a, rows, two, s);
+  }
+  return launch_stream_nt<KIND, FORM, NT, 1, OUT_F32>(a, rows, one, s);
+}
+
 template <Kind KIND, WeightForm FORM, bool OUT_F32>
-cudaError_t launch_stream(const FewArgs& a, int items, int units, const StreamArgs& s) {
-  if (a.T <= 8) return launch_stream_nt<KIND, FORM, 1, OUT_F32>(a, items, units, s);
-  if (a.T <= 16) return launch_stream_nt<KIND, FORM, 2, OUT_F32>(a, items, units, s);
-  return launch_stream_nt<KIND, FORM, 4, OUT_F32>(a, items, units, s);
+cudaError_t launch_stream(const FewArgs& a, int rows, int units, const StreamArgs& s) {
+  if (a.T <= 8) return launch_stream_tokens<KIND, FORM, 1, OUT_F32>(a, rows, units, s);
+  if (a.T <= 16) return launch_stream_tokens<KIND, FORM, 2, OUT_F32>(a, rows, units, s);
+  return launch_stream_tokens<KIND, FORM, 4, OUT_F32>(a, rows, units, s);
 }
 
 size_t align16(size_t n) { return (n + 15) / 16 * 16; }
@@ -523,15 +659,15 @@ cudaError_t launch_moe_form(const MoeArgs& m, bool out_f32, const StreamArgs& s)
   constexpr int unit_k = FORM == kMxfp4 ? 256 : 128;
   const int most = (int)((long long)m.T * m.k < m.E ? (long long)m.T * m.k : m.E);   // experts that can be active
   FewArgs up{m.A, m.sA, m.w1, m.s1, m.ids, m.weights, h, m.status, m.T, m.k, m.E, m.K, 2 * m.I};
-  cudaError_t e = launch_stream<kStreamUp, FORM, true>(up, most * (m.I / 8), (m.K + unit_k - 1) / unit_k, s);
+  cudaError_t e = launch_stream<kStreamUp, FORM, true>(up, most * 2 * m.I, (m.K + unit_k - 1) / unit_k, s);
   if (e != cudaSuccess) return e;
   const long long groups = (long long)rows * (m.I / 128);
   e = launch_plain(FORM == kFp8Packed ? h_cast_kernel<true> : h_cast_kernel<false>, (int)s.limit.all((groups + 7) / 8), 256, 0, s,
                    (const float*)h, m.ids, q, sq, groups, m.I / 128);
   if (e != cudaSuccess) return e;
   FewArgs down{q, sq, m.w2, m.s2, m.ids, m.weights, m.y, m.status, m.T, m.k, m.E, m.I, m.N};
-  const int units = (m.I + unit_k - 1) / unit_k * most, items = (m.N + 15) / 16;
-  return out_f32 ? launch_stream<kStreamDown, FORM, true>(down, items, units, s) : launch_stream<kStreamDown, FORM, false>(down, items, units, s);
+  const int units = (m.I + unit_k - 1) / unit_k * most;
+  return out_f32 ? launch_stream<kStreamDown, FORM, true>(down, m.N, units, s) : launch_stream<kStreamDown, FORM, false>(down, m.N, units, s);
 }
 
 }  // namespace
@@ -549,8 +685,8 @@ cudaError_t launch_moe(const MoeArgs& m, WeightForm form, bool out_f32, const St
 cudaError_t launch_mxfp4_gemm(const uint8_t* A, const float* sA, const uint8_t* B, const uint8_t* sB, void* D, bool out_f32, int M,
                               int N, int K, const StreamArgs& s) {
   FewArgs a{A, sA, B, sB, nullptr, nullptr, D, nullptr, M, 0, 1, K, N};
-  const int items = (N + 15) / 16, units = (K + 255) / 256;
-  return out_f32 ? launch_stream<kStreamDense, kMxfp4, true>(a, items, units, s) : launch_stream<kStreamDense, kMxfp4, false>(a, items, units, s);
+  const int units = (K + 255) / 256;
+  return out_f32 ? launch_stream<kStreamDense, kMxfp4, true>(a, N, units, s) : launch_stream<kStreamDense, kMxfp4, false>(a, N, units, s);
 }
 
 }  // namespace dg
