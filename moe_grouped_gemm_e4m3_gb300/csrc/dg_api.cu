@@ -958,7 +958,7 @@ dg_status run_norm(const void* X, const void* B, const float* w_after, const flo
     if (overlap(Yq, (size_t)M * N, p, bytes)) return fail(DG_ERR_INVALID_ARG, "Yq overlaps another tensor");
   dg::StreamArgs sa;
   if ((s = stream_args(stream, &sa)) != DG_OK) return s;
-  const dg::NormArgs a{X, B, w_after, W, gate, scale, (float)eps, R, Y, Yq, sY, rstd, rstd_after, M, N};
+  const dg::NormArgs a{X, B, w_after, W, gate, scale, (float)eps, R, Y, Yq, sY, rstd, rstd_after, M, N, 0};
   const cudaError_t e = dg::launch_norm(a, f32, ue8m0, sa);
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "norm launch");
 }
@@ -972,7 +972,7 @@ dg_status run_norm_backward(const void* dY, const void* dR, const void* R, const
   if (s != DG_OK) return s;
   if (N == 0) return DG_OK;
   if (!dX && !dB && !dW && !dw_after && !dgate && !dscale) return fail(DG_ERR_INVALID_ARG, "no gradient asked for");
-  const int sums = (dW != nullptr) + (dscale != nullptr) + (dw_after != nullptr);
+  const int sums = (dW ? 1 : 0) + (dscale || dw_after ? 1 : 0);
   for (const float* p : {W, w_after, gate, scale, rstd, rstd_after, (const float*)dW, (const float*)dw_after, (const float*)dgate,
                          (const float*)dscale})
     if (!aligned(p, 4)) return fail(DG_ERR_ALIGNMENT, "vectors must be 4-byte aligned");
@@ -1010,7 +1010,7 @@ dg_status run_norm_backward(const void* dY, const void* dR, const void* R, const
   if (!aligned(workspace, 16)) return fail(DG_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
   if ((s = stream_args(stream, &sa)) != DG_OK) return s;
   const dg::NormBackwardArgs a{dY, dR,    dY ? R : nullptr, B,        rstd, rstd_after, W, w_after, gate, scale, dX, dB, dgate,
-                               dW, dscale, dw_after,         static_cast<float*>(workspace), sums, M, N, 0, 0};
+                               dW, dscale, dw_after,         static_cast<float*>(workspace), M, N, 0, 0, 0};
   const cudaError_t e = dg::launch_norm_backward(a, f32, sa);
   return e == cudaSuccess ? DG_OK : fail_cuda(e, "norm backward launch");
 }
@@ -1577,7 +1577,7 @@ dg_status dg_fp8_mxfp4_gemm_nt_f32(const uint8_t* A, const float* sA, const uint
   return run_mxfp4_gemm(A, sA, B, sB, D, M, N, K, stream, true);
 }
 long long dg_residual_norm_backward_workspace(int M, int N) {
-  return M <= 0 || N <= 0 || N > dg::kNormMaxN ? 0 : dg::norm_backward_floats(M, N, 3) * (long long)sizeof(float);
+  return M <= 0 || N <= 0 || N > dg::kNormMaxN ? 0 : dg::norm_backward_floats(M, N, 2) * (long long)sizeof(float);
 }
 long long dg_fp8_moe_workspace(int T, int k, int I) { return T <= 0 || k <= 0 || I <= 0 ? 0 : dg::moe_workspace_bytes(T, k, I); }
 

@@ -107,19 +107,19 @@ struct NormArgs {
   void* sq;
   float *rstd, *rstd_after;
   int M, N;
+  int stages;   // set by launch_norm
 };
-cudaError_t launch_norm(const NormArgs& a, bool f32, bool ue8m0, const StreamArgs& s);
+cudaError_t launch_norm(NormArgs a, bool f32, bool ue8m0, const StreamArgs& s);
 struct NormBackwardArgs {
   const void *dy, *dr, *r, *b;
   const float *rstd, *rstd_after, *w, *w_after, *gate, *scale;
   void *dx, *db;
   float *dgate, *dw, *dscale, *dw_after;
   float* partial;   // the workspace: norm_backward_floats
-  int sums;         // how many of dw, dscale and dw_after
   int M, N;
-  int parts, stages;   // set by launch_norm_backward
+  int sums, parts, stages;   // set by launch_norm_backward
 };
-long long norm_backward_floats(int M, int N, int sums);
+long long norm_backward_floats(int M, int N, int sums);   // sums: one with dw, one with dscale or dw_after
 cudaError_t launch_norm_backward(NormBackwardArgs a, bool f32, const StreamArgs& s);
 constexpr int kNormMaxN = 16384;
 // The router (dg_route.cu): logits [T, E] in FP32 or BF16.

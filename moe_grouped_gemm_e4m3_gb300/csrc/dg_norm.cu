@@ -29,18 +29,21 @@ namespace dg {
 namespace {
 
 // Sums of K values over the CTA, in a fixed order; every thread gets them. `red` holds 32 floats a value and is used by
-// turns of two, so that one barrier a call is enough.
+// turns of two, so that one barrier a call is enough. In two parts: each warp's sums go to `red`, then behind the barrier to everyone.
 template <int K>
-__device__ __forceinline__ void block_sum(float (&v)[K], float (*red)[32], int warps) {
+__device__ __forceinline__ void warp_part(float (&v)[K], float (*red)[32]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (warps == 1) return;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  if (lane == 0)
+  if (threadIdx.x % 32 == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) red[k][warp] = v[k];
+    for (int k = 0; k < K; ++k) red[k][threadIdx.x / 32] = v[k];
+}
+template <int K>
+__device__ __forceinline__ void block_part(float (&v)[K], float (*red)[32], int warps) {
+  if (warps == 1) return;
+  const int lane = threadIdx.x % 32;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = lane < warps ? red[k][lane] : 0.0f;
@@ -49,128 +52,221 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float (*red)[32], int w
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
-
-// Eight elements from column c of a row of n; zeros past its end.
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int c, int n, float (&v)[8]) {
-  if (VEC)
-    unpack8(*reinterpret_cast<const uint4*>(row + c), v);
-  else
-    load8_part(row + c, n - c < 8 ? n - c : 8, v);
+template <int K>
+__device__ __forceinline__ void block_sum(float (&v)[K], float (*red)[32], int warps) {
+  warp_part(v, red);
+  block_part(v, red, warps);
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(const float* row, int c, int n, float (&v)[8]) {
-  if (VEC) {
-    const float4 a = reinterpret_cast<const float4*>(row + c)[0], b = reinterpret_cast<const float4*>(row + c)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+
+// Eight elements from column c of a row of n, two a register pair (the arithmetic is on pairs); zeros past the row's end.
+using Eight = float2[4];
+__device__ __forceinline__ void unpack(const uint4& w, Eight& v) {
+  v[0] = make_float2(bf16_lo(w.x), bf16_hi(w.x));
+  v[1] = make_float2(bf16_lo(w.y), bf16_hi(w.y));
+  v[2] = make_float2(bf16_lo(w.z), bf16_hi(w.z));
+  v[3] = make_float2(bf16_lo(w.w), bf16_hi(w.w));
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int n, Eight& v) {
+  if constexpr (!VEC) {
+    float e[8];
+    load8_part(row + c, n - c < 8 ? n - c : 8, e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(e[2 * j], e[2 * j + 1]);
+  } else if constexpr (sizeof(T) == 2) {
+    unpack(*reinterpret_cast<const uint4*>(row + c), v);
   } else {
-    load8_part(row + c, n - c < 8 ? n - c : 8, v);
+    const float4 a = reinterpret_cast<const float4*>(row + c)[0], b = reinterpret_cast<const float4*>(row + c)[1];
+    v[0] = make_float2(a.x, a.y), v[1] = make_float2(a.z, a.w), v[2] = make_float2(b.x, b.y), v[3] = make_float2(b.z, b.w);
   }
 }
 template <bool VEC, typename T>
-__device__ __forceinline__ void put8(T* row, int c, int n, const float (&v)[8]) {
-  if (VEC)
-    store8(row + c, v);
+__device__ __forceinline__ void put8(T* row, int c, int n, const Eight& v) {
+  const float e[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+  if constexpr (VEC)
+    store8(row + c, e);
   else
-    store8_part(row + c, n - c < 8 ? n - c : 8, v);
+    store8_part(row + c, n - c < 8 ? n - c : 8, e);
 }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // ---------------------------------------------------------------------------------------------
-// Forward. A CTA takes one row, a thread V vectors of eight columns, in registers from the loads to the stores.
+// The rows of a CTA. Its inputs are copied ahead into a ring of `stages` rows in shared memory, each thread's columns to its own
+// places (so no barrier guards them); with no stages (rows too long for it, or any alignment) they are read from the rows
+// themselves. A thread's V vectors of eight columns are the same in every row, so what belongs to the columns stays in registers.
+template <typename T>
+__device__ __forceinline__ void copy_async(uint8_t* to, const T* from) {   // eight elements
+#pragma unroll
+  for (size_t o = 0; o < 8 * sizeof(T); o += 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + o)), "l"(reinterpret_cast<const uint8_t*>(from) + o)
+                 : "memory");
+}
+
+template <typename T, bool VEC, int V, int INPUTS>
+struct RowRing {
+  uint8_t* mine;                 // this thread's first place
+  const T* in[INPUTS];           // the matrices at this thread's first column, null where absent (no places of the ring then)
+  int off[INPUTS];               // of each input's places in a stage, in bytes
+  int stage_bytes = 0, stages, M, N, column0, column_step;
+  int head = 0;                  // the current row's stage, in bytes
+
+  __device__ __forceinline__ RowRing(uint8_t* ring, int stages, int M, int N)
+      : mine(ring + threadIdx.x * (int)(8 * sizeof(T))), stages(stages), M(M), N(N), column0(threadIdx.x * 8), column_step(blockDim.x * 8) {}
+  __device__ __forceinline__ void add(int k, const void* p) {
+    in[k] = static_cast<const T*>(p);
+    off[k] = stage_bytes;
+    if (p) stage_bytes += V * column_step * (int)sizeof(T);
+  }
+  __device__ __forceinline__ int column(int i) const { return column0 + i * column_step; }
+  __device__ __forceinline__ void fetch(long long m, int at) {
+    if constexpr (VEC) {
+      if (stages > 0 && m < M) {
+        const size_t row = (size_t)m * N + column0;
+#pragma unroll
+        for (int k = 0; k < INPUTS; ++k) {
+          if (!in[k]) continue;
+          const T* from = in[k] + row;
+          uint8_t* to = mine + at + off[k];
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (column(i) < N) copy_async(to + i * column_step * (int)sizeof(T), from + i * column_step);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ void begin(long long m, long long step) {
+    head = 0;
+    for (int s = 0; s < stages - 1; ++s) fetch(m + s * step, s * stage_bytes);
+  }
+  // The current row m's inputs are there; the row stages - 1 further on is asked for, into the stage that the row before has left.
+  __device__ __forceinline__ void arrive(long long m, long long step) {
+    if constexpr (VEC) {
+      if (stages == 0) return;
+      fetch(m + (stages - 1) * step, (head == 0 ? stages * stage_bytes : head) - stage_bytes);
+      if (stages == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+      else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      else asm volatile("cp.async.wait_group 2;" ::: "memory");
+    }
+  }
+  // The same while the row before m keeps its stage (three stages): the row after m is asked for instead.
+  __device__ __forceinline__ void arrive_keeping(long long m, long long step) {
+    if constexpr (VEC) {
+      const int past = head + stage_bytes >= stages * stage_bytes ? 0 : head + stage_bytes;
+      fetch(m + step, past);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ void leave() {
+    head += stage_bytes;
+    if (head >= stages * stage_bytes) head = 0;
+  }
+  __device__ __forceinline__ void end() {
+    if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
+  // (`at`: the row's stage)
+  __device__ __forceinline__ void get(int k, int i, long long m, int at, Eight& v) const {
+    if (VEC && stages > 0)
+      load8<true>(reinterpret_cast<const T*>(mine + at + off[k] + i * column_step * (int)sizeof(T)), 0, 8, v);
+    else
+      load8<VEC>(in[k] + (size_t)m * N, column(i), N, v);
+  }
+};
+
+// Eight columns of a vector that may be absent: ones then, and zeros past the row's end.
+template <bool VEC>
+__device__ __forceinline__ void columns_of(const float* p, int c, int n, Eight& v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = make_float2(c + 2 * j < n ? 1.0f : 0.0f, c + 2 * j + 1 < n ? 1.0f : 0.0f);
+  if (p && c < n) load8<VEC>(p, c, n, v);
+}
+__device__ __forceinline__ float sum_of(const float2& v) { return v.x + v.y; }
+
+// Forward. A CTA takes one row at a time, a thread V vectors of eight columns.
 template <typename T, bool VEC, int V, bool UE>
-__global__ void __launch_bounds__(128 * V) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1) norm_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][1][32];
-  griddep_wait();
-  griddep_launch_dependents();
   const int N = a.N, warps = blockDim.x / 32, tid = threadIdx.x;
   const float inv_n = 1.0f / (float)N;
-  int turn = 0;
-  for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
-    const size_t at = (size_t)m * N;
-    const T* x = static_cast<const T*>(a.x) + at;
-    float r[V][8];
+  griddep_wait();
+  griddep_launch_dependents();
+  RowRing<T, VEC, V, 2> rows(ring, a.stages, a.M, N);
+  rows.add(0, a.x);
+  rows.add(1, a.b);
+  rows.begin(blockIdx.x, gridDim.x);
+  Eight after[V], before[V];   // w_after·scale, W
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (i * blockDim.x + tid) * 8;
-      if (c < N)
-        load8<VEC>(x, c, N, r[i]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
-    }
+  for (int i = 0; i < V; ++i) {
+    const int c = rows.column(i);
     if (a.b) {
-      const T* b = static_cast<const T*>(a.b) + at;
-      float p[V][8];
+      Eight sc;
+      columns_of<VEC>(a.w_after, c, N, after[i]);
+      columns_of<VEC>(a.scale, c, N, sc);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = (i * blockDim.x + tid) * 8;
-        if (c < N)
-          load8<VEC>(b, c, N, p[i]);
-        else
+      for (int j = 0; j < 4; ++j) after[i][j] = __fmul2_rn(after[i][j], sc[j]);
+    }
+    columns_of<VEC>(a.w, c, N, before[i]);
+  }
+  int turn = 0;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const size_t at = (size_t)m * N;
+    float f = a.b && a.gate ? a.gate[m] : 1.0f;   // of the whole row
+    rows.arrive(m, gridDim.x);
+    Eight r[V] = {};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[i][j] = 0.0f;
-      }
-      float f = a.gate ? a.gate[m] : 1.0f;   // of the whole row
+    for (int i = 0; i < V; ++i)
+      if (rows.column(i) < N) rows.get(0, i, m, rows.head, r[i]);
+    if (a.b) {
+      Eight p[V] = {};
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (rows.column(i) < N) rows.get(1, i, m, rows.head, p[i]);
       if (a.w_after) {
-        float s[1] = {0.0f};
+        float2 sq = both(0.0f);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[0] = fmaf(p[i][j], p[i][j], s[0]);
+          for (int j = 0; j < 4; ++j) sq = __ffma2_rn(p[i][j], p[i][j], sq);
+        float s[1] = {sum_of(sq)};
         block_sum(s, red[turn], warps);
         turn ^= 1;
         const float ra = rsqrtf(fmaf(s[0], inv_n, a.eps));
         if (a.rstd_after && tid == 0) a.rstd_after[m] = ra;
         f *= ra;
       }
-      T* out = a.r ? static_cast<T*>(a.r) + at : nullptr;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (i * blockDim.x + tid) * 8;
+        const int c = rows.column(i);
         if (c >= N) continue;
-        if (a.w_after) {
-          float w[8];
-          load8<VEC>(a.w_after, c, N, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[i][j] *= w[j];
-        }
-        if (a.scale) {
-          float w[8];
-          load8<VEC>(a.scale, c, N, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) p[i][j] *= w[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(p[i][j], f, r[i][j]);
-        if (out) put8<VEC>(out, c, N, r[i]);
+        for (int j = 0; j < 4; ++j) r[i][j] = __ffma2_rn(__fmul2_rn(p[i][j], after[i][j]), both(f), r[i][j]);
+        if (a.r) put8<VEC>(static_cast<T*>(a.r) + at, c, N, r[i]);
       }
     }
+    rows.leave();
     if (!a.w) continue;
-    float s[1] = {0.0f};
+    float2 sq = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(r[i][j], r[i][j], s[0]);
+      for (int j = 0; j < 4; ++j) sq = __ffma2_rn(r[i][j], r[i][j], sq);
+    float s[1] = {sum_of(sq)};
     block_sum(s, red[turn], warps);
     turn ^= 1;
     const float rs = rsqrtf(fmaf(s[0], inv_n, a.eps));
     if (a.rstd && tid == 0) a.rstd[m] = rs;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (i * blockDim.x + tid) * 8;
+      const int c = rows.column(i);
       const bool live = c < N;
-      if (live) {
-        float w[8];
-        load8<VEC>(a.w, c, N, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] *= rs * w[j];
-        if (a.y) put8<VEC>(static_cast<T*>(a.y) + at, c, N, r[i]);
-      }
+      for (int j = 0; j < 4; ++j) r[i][j] = __fmul2_rn(r[i][j], __fmul2_rn(both(rs), before[i][j]));
+      if (live && a.y) put8<VEC>(static_cast<T*>(a.y) + at, c, N, r[i]);
       if (a.q) {   // sixteen lanes hold a group of 128; columns past N are zeros
         float top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(r[i][j]));
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, fmaxf(fabsf(r[i][j].x), fabsf(r[i][j].y)));
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (live) {
@@ -179,7 +275,10 @@ __global__ void __launch_bounds__(128 * V) norm_kernel(const NormArgs a) {
           group_scale<UE>(top, factor, scale);
           uint32_t q[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) q[j] = e4m3x2_satfinite(__fmul_rn(r[i][2 * j], factor), __fmul_rn(r[i][2 * j + 1], factor));
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = __fmul2_rn(r[i][j], both(factor));
+            q[j] = e4m3x2_satfinite(v.x, v.y);
+          }
           *reinterpret_cast<uint2*>(a.q + at + c) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
           if (tid % 16 == 0) {
             const int groups = (N + 127) / 128, ld = (a.M + 3) / 4 * 4;
@@ -191,202 +290,213 @@ __global__ void __launch_bounds__(128 * V) norm_kernel(const NormArgs a) {
       }
     }
   }
+  rows.end();
 }
 
 // ---------------------------------------------------------------------------------------------
-// Backward.
-template <typename T>
-__device__ __forceinline__ void copy_async(uint8_t* to, const T* from) {   // eight elements, to this thread's own place
-#pragma unroll
-  for (size_t o = 0; o < 8 * sizeof(T); o += 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + o)), "l"(reinterpret_cast<const uint8_t*>(from) + o)
-                 : "memory");
-}
-
-// The inputs of `stages` rows are copied ahead into a ring in shared memory, each thread's columns to its own places (so no
-// barrier guards them); with no stages (rows too long for it, or any alignment) they are read from the rows themselves.
+// Backward. Both dscale = w_after·t and dw_after = scale·t come from t = Σ_m gate·G·b̂, so two columns' sums are kept.
 template <typename T, bool VEC, int V>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const NormBackwardArgs a) {
+__global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 4 : 1) norm_backward_kernel(const NormBackwardArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][3][32];
+  enum { kDY, kR, kDR, kB };
+  const int N = a.N, tid = threadIdx.x, warps = blockDim.x / 32;
+  const float inv_n = 1.0f / (float)N;
+  const bool dy = a.dy, dr = a.dr, b = a.b, along_b = b && (a.w_after || a.dgate);
   griddep_wait();
   griddep_launch_dependents();
-  const int N = a.N, TH = blockDim.x, tid = threadIdx.x, warps = TH / 32, stages = a.stages;
-  const float inv_n = 1.0f / (float)N;
-  const T *const dy = static_cast<const T*>(a.dy), *const dr = static_cast<const T*>(a.dr), *const r = static_cast<const T*>(a.r),
-          *const b = static_cast<const T*>(a.b);
-  // inputs of a stage one after another, each thread's vectors in its own places
-  const size_t plane = (size_t)TH * V * 8 * sizeof(T);
-  const int n_in = (dy ? 2 : 0) + (dr ? 1 : 0) + (b ? 1 : 0);   // (R only with dY)
-  auto place = [&](int stage, int input, int i) { return ring + (size_t)(stage * n_in + input) * plane + ((size_t)i * TH + tid) * 8 * sizeof(T); };
-  auto fetch = [&](int m, int stage) {
-    if constexpr (VEC) {
-      if (stages > 0 && m < a.M) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = (i * TH + tid) * 8;
-          if (c >= N) continue;
-          const size_t at = (size_t)m * N + c;
-          int k = 0;
-          if (dy) copy_async(place(stage, k++, i), dy + at), copy_async(place(stage, k++, i), r + at);
-          if (dr) copy_async(place(stage, k++, i), dr + at);
-          if (b) copy_async(place(stage, k, i), b + at);
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-  };
-  auto get = [&](int stage, int input, int i, const T* from, int m, float (&v)[8]) {
-    if (VEC && stages > 0)
-      load8<true>(reinterpret_cast<const T*>(place(stage, input, i)), 0, 8, v);
-    else
-      load8<VEC>(from + (size_t)m * N, (i * TH + tid) * 8, N, v);
-  };
-  const int in_dr = dy ? 2 : 0, in_b = in_dr + (dr ? 1 : 0);
-
+  RowRing<T, VEC, V, 4> rows(ring, a.stages, a.M, N);
+  rows.add(kDY, a.dy);
+  rows.add(kR, a.r);
+  rows.add(kDR, a.dr);
+  rows.add(kB, a.b);
+  Eight w[V], ws[V];   // W, w_after·scale
   for (int part = blockIdx.x; part < a.parts; part += gridDim.x) {   // (more than one only under dg_set_num_sms)
-    float sw[V][8] = {}, ss[V][8] = {}, sa[V][8] = {};
-    for (int s = 0; s < stages - 1; ++s) fetch(part + s * a.parts, s);
-    int stage = 0, turn = 0;
-    for (int m = part; m < a.M; m += a.parts, turn ^= 1) {
-      {
-        const int ahead = stage == 0 ? stages - 1 : stage - 1;   // the stage that the row before this one has left
-        if (stages > 0) fetch(m + (stages - 1) * a.parts, stages == 1 ? 0 : ahead);
-      }
-      if constexpr (VEC) {
-        if (stages <= 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-        else asm volatile("cp.async.wait_group 2;" ::: "memory");
-      }
-      const float rs = dy ? a.rstd[m] : 0.0f, ra = a.w_after ? a.rstd_after[m] : 1.0f, gate = a.gate ? a.gate[m] : 1.0f;
-      float sums[3] = {0.0f, 0.0f, 0.0f};
+    rows.begin(part, a.parts);
+    if (part == (int)blockIdx.x) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (i * TH + tid) * 8;
-        if (c >= N) continue;
-        float p[8], g[8] = {}, xh[8];
-        if (b && (a.w_after || a.dgate)) {
-          get(stage, in_b, i, b, m, p);
+        Eight sc;
+        columns_of<VEC>(a.w, rows.column(i), N, w[i]);
+        columns_of<VEC>(a.w_after, rows.column(i), N, ws[i]);
+        columns_of<VEC>(a.scale, rows.column(i), N, sc);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) p[j] *= ra;
-          float w[8];
-          if (a.w_after) {
-            load8<VEC>(a.w_after, c, N, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] *= w[j];
-          }
-          if (a.scale) {
-            load8<VEC>(a.scale, c, N, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) p[j] *= w[j];
-          }
-          if (dr) get(stage, in_dr, i, dr, m, g);
-        }
-        if (dy) {
-          float w[8], d[8];
-          get(stage, 0, i, dy, m, d);
-          get(stage, 1, i, r, m, xh);
-          load8<VEC>(a.w, c, N, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float gw = d[j] * w[j];
-            xh[j] *= rs;
-            sums[0] = fmaf(gw, xh[j], sums[0]);
-            g[j] = fmaf(rs, gw, g[j]);
-          }
-        }
-        if (b && (a.w_after || a.dgate)) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sums[1] = fmaf(p[j], g[j], sums[1]);
-            if (dy) sums[2] = fmaf(p[j], xh[j], sums[2]);
-          }
-        }
+        for (int j = 0; j < 4; ++j) ws[i][j] = __fmul2_rn(ws[i][j], sc[j]);
       }
-      if (dy || a.w_after || a.dgate) block_sum(sums, red[turn], warps);
-      const float c1 = sums[0] * inv_n, along = fmaf(-c1 * rs, sums[2], sums[1]);   // Σ scale·P·G
-      if (a.dgate && tid == 0) a.dgate[m] = along;
-      const float c2 = gate * along * inv_n;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = (i * TH + tid) * 8;
-        if (c >= N) continue;
-        const size_t at = (size_t)m * N;
-        float g[8] = {};
-        if (dr) get(stage, in_dr, i, dr, m, g);
-        if (dy) {
-          float w[8], d[8], xh[8];
-          get(stage, 0, i, dy, m, d);
-          get(stage, 1, i, r, m, xh);
-          load8<VEC>(a.w, c, N, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            xh[j] *= rs;
-            sw[i][j] = fmaf(d[j], xh[j], sw[i][j]);
-            g[j] = fmaf(rs, fmaf(-xh[j], c1, d[j] * w[j]), g[j]);
-          }
-        }
-        float q[8];
-        if (b) {
-          float bh[8], w[8], sc[8];
-          get(stage, in_b, i, b, m, bh);
-          if (a.w_after) load8<VEC>(a.w_after, c, N, w);
-          if (a.scale) load8<VEC>(a.scale, c, N, sc);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            bh[j] *= ra;
-            const float t = gate * g[j];
-            ss[i][j] = fmaf(t, a.w_after ? bh[j] * w[j] : bh[j], ss[i][j]);
-            q[j] = a.scale ? t * sc[j] : t;
-            if (a.w_after) {
-              sa[i][j] = fmaf(q[j], bh[j], sa[i][j]);
-              q[j] = ra * fmaf(-bh[j], c2, q[j] * w[j]);
-            }
-          }
-        }
-        if (a.dx) put8<VEC>(static_cast<T*>(a.dx) + at, c, N, g);
-        if (a.db) put8<VEC>(static_cast<T*>(a.db) + at, c, N, q);
-      }
-      if (++stage >= stages) stage = 0;
     }
-    if constexpr (VEC) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    Eight sw[V] = {}, st[V] = {};   // Σ dY·x̂, Σ gate·G·b̂
+    // Σ dY·W·R, Σ scale·P·(dR + r·dY·W), Σ scale·P·R of row m (r, ra where a whole sum has them: in `scalars`), this thread's part
+    auto row_sums = [&](long long m, int at, float rs, float (&sums)[3]) {
+      float2 two[3] = {};
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (rows.column(i) >= N) continue;
+        Eight g = {}, x = {};
+        if (dr) rows.get(kDR, i, m, at, g);
+        if (dy) {
+          Eight d;
+          rows.get(kDY, i, m, at, d);
+          rows.get(kR, i, m, at, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 gw = __fmul2_rn(d[j], w[i][j]);
+            two[0] = __ffma2_rn(gw, x[j], two[0]);
+            g[j] = __ffma2_rn(both(rs), gw, g[j]);
+          }
+        }
+        if (along_b) {
+          Eight p;
+          rows.get(kB, i, m, at, p);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p[j] = __fmul2_rn(p[j], ws[i][j]);
+            two[1] = __ffma2_rn(p[j], g[j], two[1]);
+            two[2] = __ffma2_rn(p[j], x[j], two[2]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sums[k] = sum_of(two[k]);
+    };
+    struct Row {   // the scalars of a row
+      float rs, ra, gate;
+    };
+    auto row_of = [&](long long m) { return Row{dy ? a.rstd[m] : 0.0f, a.w_after ? a.rstd_after[m] : 1.0f, a.gate ? a.gate[m] : 1.0f}; };
+    auto gradients = [&](long long m, int at, const Row& row, const float (&sums)[3]) {
+      const float rs = row.rs, ra = row.ra;
+      const float c1 = sums[0] * rs * inv_n;                                                // mean(dY·W·x̂)
+      const float along = ra * fmaf(-c1 * rs * rs, sums[2], sums[1]);                       // Σ scale·P·G
+      if (a.dgate && tid == 0) a.dgate[m] = along;
+      const float c2 = a.w_after ? row.gate * along * inv_n * ra * ra : 0.0f, k1 = c1 * rs; // (of B, of R)
+      const float gra = row.gate * ra;
+      const size_t to = (size_t)m * N;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = rows.column(i);
+        if (c >= N) continue;
+        Eight g = {}, p;
+        if (dr) rows.get(kDR, i, m, at, g);
+        if (dy) {
+          Eight d, x;
+          rows.get(kDY, i, m, at, d);
+          rows.get(kR, i, m, at, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sw[i][j] = __ffma2_rn(__fmul2_rn(d[j], both(rs)), x[j], sw[i][j]);
+            g[j] = __ffma2_rn(both(rs), __ffma2_rn(x[j], both(-k1), __fmul2_rn(d[j], w[i][j])), g[j]);
+          }
+        }
+        if (b) rows.get(kB, i, m, at, p);   // (dX may be B)
+        if (a.dx) put8<VEC>(static_cast<T*>(a.dx) + to, c, N, g);
+        if (b) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 t = __fmul2_rn(both(gra), g[j]);
+            st[i][j] = __ffma2_rn(t, p[j], st[i][j]);
+            g[j] = __ffma2_rn(t, ws[i][j], __fmul2_rn(p[j], both(-c2)));
+          }
+          if (a.db) put8<VEC>(static_cast<T*>(a.db) + to, c, N, g);
+        }
+      }
+    };
+    const bool reduce = dy || along_b;
+    float sums[3] = {0.0f, 0.0f, 0.0f};
+    int turn = 0;
+    if (rows.stages >= 3) {
+      // One row's sums are formed beside the gradients of the row before, so the reduction's latency is behind those.
+      Row row = row_of(part);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");   // (of the two rows asked for)
+      if (reduce) {
+        row_sums(part, rows.head, row.rs, sums);
+        block_sum(sums, red[turn], warps);
+      }
+      for (long long m = part; m < a.M; m += a.parts) {
+        const long long next = m + a.parts;
+        const int at = rows.head;
+        const bool more = next < a.M;
+        Row then = row;
+        float more_sums[3] = {0.0f, 0.0f, 0.0f};
+        rows.leave();
+        if (more) {
+          then = row_of(next);
+          rows.arrive_keeping(next, a.parts);
+          if (reduce) {
+            turn ^= 1;
+            row_sums(next, rows.head, then.rs, more_sums);
+            warp_part(more_sums, red[turn]);
+          }
+        }
+        gradients(m, at, row, sums);
+        if (more && reduce) block_part(more_sums, red[turn], warps);
+        row = then;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sums[k] = more_sums[k];
+      }
+    } else {
+      for (long long m = part; m < a.M; m += a.parts, turn ^= 1) {
+        const Row row = row_of(m);
+        rows.arrive(m, a.parts);
+        if (reduce) {
+          row_sums(m, rows.head, row.rs, sums);
+          block_sum(sums, red[turn], warps);
+        }
+        gradients(m, rows.head, row, sums);
+        rows.leave();
+      }
+    }
+    rows.end();
     // the workspace: [parts][sums kept][N]
     float* out = a.partial + (size_t)part * a.sums * N;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (i * TH + tid) * 8;
+      const int c = rows.column(i);
       if (c >= N) continue;
-      int k = 0;
-      if (a.dw) put8<VEC>(out + (size_t)k++ * N, c, N, sw[i]);
-      if (a.dscale) put8<VEC>(out + (size_t)k++ * N, c, N, ss[i]);
-      if (a.dw_after) put8<VEC>(out + (size_t)k * N, c, N, sa[i]);
+      if (a.dw) put8<VEC>(out, c, N, sw[i]);
+      if (a.dscale || a.dw_after) put8<VEC>(out + (size_t)(a.dw ? N : 0), c, N, st[i]);
     }
     __syncthreads();   // red is free for the next part
   }
 }
 
-// Adds the partial rows: eight threads a column, each its share of the rows in order, then the eight in order.
-constexpr int kSumCols = 32, kSumShares = 8;
-__global__ void __launch_bounds__(kSumCols* kSumShares) norm_sum_kernel(const float* __restrict__ partial, int parts, int sums, int N,
-                                                                         float* out0, float* out1, float* out2) {
-  __shared__ float share[kSumShares][kSumCols];
+// Adds the partial rows: a thread takes four columns of each kSumShares-th row, then the shares are added in order.
+constexpr int kSumCols = 32, kSumShares = 64;
+__global__ void __launch_bounds__(kSumCols / 4 * kSumShares) norm_sum_kernel(const NormBackwardArgs a) {
+  __shared__ float share[kSumShares][kSumCols + 1];
   griddep_wait();
   griddep_launch_dependents();
-  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols, blocks = (N + kSumCols - 1) / kSumCols;
-  for (int block = blockIdx.x; block < blocks * sums; block += gridDim.x) {
-    const int k = block / blocks, n = (block % blocks) * kSumCols + col;
-    float s = 0.0f;
+  const int N = a.N, quad = threadIdx.x % (kSumCols / 4) * 4, row = threadIdx.x / (kSumCols / 4), blocks = (N + kSumCols - 1) / kSumCols;
+  for (int block = blockIdx.x; block < blocks * a.sums; block += gridDim.x) {
+    const int k = block / blocks, n = (block % blocks) * kSumCols + quad;
+    float s[4] = {};
     if (n < N) {
-      const float* p = partial + (size_t)k * N + n;
-#pragma unroll 8
-      for (int i = row; i < parts; i += kSumShares) s += p[(size_t)i * sums * N];
-    }
-    share[row][col] = s;
-    __syncthreads();
-    if (row == 0 && n < N) {
+      const float* p = a.partial + (size_t)k * N + n;
+      if (N % 4 == 0) {
+#pragma unroll 4
+        for (int i = row; i < a.parts; i += kSumShares) {
+          const float4 v = *reinterpret_cast<const float4*>(p + (size_t)i * a.sums * N);
+          s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+        }
+      } else {
+        for (int i = row; i < a.parts; i += kSumShares)
 #pragma unroll
-      for (int i = 1; i < kSumShares; ++i) s += share[i][col];
-      (k == 0 ? out0 : k == 1 ? out1 : out2)[n] = s;
+          for (int j = 0; j < 4; ++j)
+            if (n + j < N) s[j] += p[(size_t)i * a.sums * N + j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) share[row][quad + j] = s[j];
+    __syncthreads();
+    const int col = threadIdx.x, at = (block % blocks) * kSumCols + col;
+    if (col < kSumCols && at < N) {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kSumShares; ++i) v += share[i][col];
+      if (k == 0 && a.dw) {
+        a.dw[at] = v;
+      } else {
+        if (a.dscale) a.dscale[at] = a.w_after ? v * a.w_after[at] : v;
+        if (a.dw_after) a.dw_after[at] = a.scale ? v * a.scale[at] : v;
+      }
     }
     __syncthreads();
   }
@@ -394,87 +504,88 @@ __global__ void __launch_bounds__(kSumCols* kSumShares) norm_sum_kernel(const fl
 
 int threads_for(int N, int V) { return ((N + 8 * V - 1) / (8 * V) + 31) / 32 * 32; }
 
-template <typename T, bool VEC, bool UE>
-cudaError_t launch_forward(const NormArgs& a, const StreamArgs& s) {
-  const int grid = (int)s.limit.all(a.M);
-  if (a.N <= 1024) return launch_plain(norm_kernel<T, VEC, 1, UE>, grid, threads_for(a.N, 1), 0, s, a);
-  if (a.N <= 4096) return launch_plain(norm_kernel<T, VEC, 2, UE>, grid, threads_for(a.N, 2), 0, s, a);
-  return launch_plain(norm_kernel<T, VEC, 4, UE>, grid, threads_for(a.N, 4), 0, s, a);
-}
-
 bool all_aligned(std::initializer_list<const void*> ps) {
   uintptr_t bits = 0;
   for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
   return bits % 16 == 0;
 }
 
-constexpr int kRingBytes = 216 << 10;   // of an SM, over its CTAs
-
-struct BackwardPlan {
+// How rows of N are laid out: vectors and threads of a CTA, CTAs an SM, and how many of them take the rows by turns.
+constexpr int kNormSms = 152, kRingBytes = 216 << 10;   // (the ring: of an SM, over its CTAs)
+struct RowPlan {
   int V, threads, per_sm, parts;
 };
-constexpr int kNormSms = 152;
-BackwardPlan backward_plan(int M, int N) {
-  const int V = N <= 4096 ? 1 : N <= 8192 ? 2 : 4, threads = threads_for(N, V);
-  const int per_sm = threads <= 64 ? 8 : threads <= 128 ? 4 : threads <= 256 ? 2 : 1, parts = kNormSms * per_sm;
+RowPlan row_plan(int M, int N) {
+  const int V = N <= 1024 ? 1 : N <= 8192 ? 2 : 4, threads = threads_for(N, V);
+  const int fit = 512 / threads, per_sm = fit > 8 ? 8 : fit, parts = kNormSms * per_sm;
   return {V, threads, per_sm, M < parts ? M : parts};
+}
+int ring_stages(const RowPlan& p, bool vec, int inputs, size_t size, size_t* bytes) {
+  const size_t stage = (size_t)p.threads * p.V * 8 * size * inputs, most = (size_t)kRingBytes / p.per_sm;
+  const int stages = !vec ? 0 : 3 * stage <= most ? 3 : 2 * stage <= most ? 2 : stage <= most ? 1 : 0;
+  *bytes = stages * stage;
+  return stages;
+}
+
+// Launches a kernel of the plan's V, its shared-memory limit set on first use per device.
+template <typename Kernel, typename Args>
+cudaError_t launch_rows(Kernel kernel, bool (&configured)[64], const RowPlan& p, size_t smem, const StreamArgs& s, const Args& a) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)) != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  return launch_plain(kernel, (int)s.limit.all(p.parts), p.threads, smem, s, a);
+}
+
+template <typename F>
+cudaError_t with_vectors(int V, F f) {
+  return V == 1 ? f(std::integral_constant<int, 1>{}) : V == 2 ? f(std::integral_constant<int, 2>{}) : f(std::integral_constant<int, 4>{});
 }
 
 }  // namespace
 
-long long norm_backward_floats(int M, int N, int sums) {
-  return (long long)backward_plan(M, N).parts * sums * N;
-}
+long long norm_backward_floats(int M, int N, int sums) { return (long long)row_plan(M, N).parts * sums * N; }
 
-cudaError_t launch_norm(const NormArgs& a, bool f32, bool ue8m0, const StreamArgs& s) {
+cudaError_t launch_norm(NormArgs a, bool f32, bool ue8m0, const StreamArgs& s) {
   const bool vec = a.N % 8 == 0 && all_aligned({a.x, a.b, a.r, a.y, a.w, a.w_after, a.scale});
-  auto go = [&](auto one) {
-    using T = decltype(one);
-    if (a.q && ue8m0) return vec ? launch_forward<T, true, true>(a, s) : launch_forward<T, false, true>(a, s);
-    return vec ? launch_forward<T, true, false>(a, s) : launch_forward<T, false, false>(a, s);
-  };
-  return f32 ? go(0.0f) : go(__nv_bfloat16{});
+  const RowPlan plan = row_plan(a.M, a.N);
+  size_t smem;
+  a.stages = ring_stages(plan, vec, a.b ? 2 : 1, f32 ? 4 : 2, &smem);
+  return with_vectors(plan.V, [&](auto v) {
+    auto go = [&](auto one, auto vector, auto ue) {
+      constexpr int V = decltype(v)::value;
+      static bool configured[64] = {};
+      return launch_rows(norm_kernel<decltype(one), decltype(vector)::value, V, decltype(ue)::value>, configured, plan, smem, s, a);
+    };
+    auto scales = [&](auto one, auto vector) { return a.q && ue8m0 ? go(one, vector, std::true_type{}) : go(one, vector, std::false_type{}); };
+    auto type = [&](auto vector) { return f32 ? scales(0.0f, vector) : scales(__nv_bfloat16{}, vector); };
+    return vec ? type(std::true_type{}) : type(std::false_type{});
+  });
 }
 
 cudaError_t launch_norm_backward(NormBackwardArgs a, bool f32, const StreamArgs& s) {
   const bool vec = a.N % 8 == 0 && all_aligned({a.dy, a.dr, a.r, a.b, a.dx, a.db, a.w, a.w_after, a.scale, a.partial});
-  const BackwardPlan plan = backward_plan(a.M, a.N);
+  const RowPlan plan = row_plan(a.M, a.N);
+  size_t smem;
+  a.stages = ring_stages(plan, vec, (a.dy ? 2 : 0) + (a.dr ? 1 : 0) + (a.b ? 1 : 0), f32 ? 4 : 2, &smem);
   a.parts = plan.parts;
-  auto go = [&](auto one, auto vector, auto v) -> cudaError_t {
-    using T = decltype(one);
-    constexpr bool VEC = decltype(vector)::value;
-    constexpr int V = decltype(v)::value;
-    auto kernel = norm_backward_kernel<T, VEC, V>;
-    const size_t stage = (size_t)plan.threads * V * 8 * sizeof(T) * ((a.dy ? 2 : 0) + (a.dr ? 1 : 0) + (a.b ? 1 : 0));
-    const size_t most = (size_t)kRingBytes / plan.per_sm;
-    a.stages = !VEC ? 0 : 3 * stage <= most ? 3 : 2 * stage <= most ? 2 : stage <= most ? 1 : 0;
-    const size_t smem = a.stages * stage;
-    static bool configured[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
-      if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes)) != cudaSuccess) return e;
-      configured[dev] = true;
-    }
-    return launch_plain(kernel, (int)s.limit.all(plan.parts), plan.threads, smem, s, a);
-  };
-  auto pick = [&](auto one, auto vector) {
-    return plan.V == 1 ? go(one, vector, std::integral_constant<int, 1>{})
-                       : plan.V == 2 ? go(one, vector, std::integral_constant<int, 2>{}) : go(one, vector, std::integral_constant<int, 4>{});
-  };
-  auto type = [&](auto vector) { return f32 ? pick(0.0f, vector) : pick(__nv_bfloat16{}, vector); };
-  cudaError_t e = vec ? type(std::true_type{}) : type(std::false_type{});
+  a.sums = (a.dw ? 1 : 0) + (a.dscale || a.dw_after ? 1 : 0);
+  cudaError_t e = with_vectors(plan.V, [&](auto v) {
+    auto go = [&](auto one, auto vector) {
+      constexpr int V = decltype(v)::value;
+      static bool configured[64] = {};
+      return launch_rows(norm_backward_kernel<decltype(one), decltype(vector)::value, V>, configured, plan, smem, s, a);
+    };
+    auto type = [&](auto vector) { return f32 ? go(0.0f, vector) : go(__nv_bfloat16{}, vector); };
+    return vec ? type(std::true_type{}) : type(std::false_type{});
+  });
   if (e != cudaSuccess || a.sums == 0) return e;
-  float* outs[3];
-  int k = 0;
-  for (float* o : {a.dw, a.dscale, a.dw_after})
-    if (o) outs[k++] = o;
-  for (; k < 3; ++k) outs[k] = nullptr;
   const int blocks = (a.N + kSumCols - 1) / kSumCols * a.sums;
-  return launch_plain(norm_sum_kernel, (int)s.limit.all(blocks), kSumCols * kSumShares, 0, s, (const float*)a.partial, a.parts, a.sums,
-                      a.N, outs[0], outs[1], outs[2]);
+  return launch_plain(norm_sum_kernel, (int)s.limit.all(blocks), kSumCols / 4 * kSumShares, 0, s, a);
 }
 
 }  // namespace dg

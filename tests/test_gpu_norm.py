@@ -236,14 +236,15 @@ def test_backward_of_no_rows_is_zero(dg):
 
 
 def test_backward_outputs_may_be_inputs(dg):
-    d = _data(300, 520, BF)
-    want = _backward(dg, d)
-    rs, ra = _stats(d)
-    for over in ("dY", "dR"):
-        c = {n: t.clone() for n, t in d.items()}
-        dg.dg_residual_norm_backward(c["dY"], c["X"], rs, c["W"], dR=c["dR"], B=c["B"], rstd_after=ra, w_after=c["w_after"], gate=c["gate"],
-                                     scale=c["scale"], dX=c[over], dB=c["B"])
-        assert torch.equal(c[over], want["dX"]) and torch.equal(c["B"], want["dB"])
+    for N in (520, 517):                       # (517: rows read elementwise)
+        d = _data(300, N, BF)
+        want = _backward(dg, d)
+        rs, ra = _stats(d)
+        for over, other in (("dY", "B"), ("dR", "B"), ("X", "dY"), ("B", "dR")):
+            c = {n: t.clone() for n, t in d.items()}
+            dg.dg_residual_norm_backward(c["dY"], c["X"], rs, c["W"], dR=c["dR"], B=c["B"], rstd_after=ra, w_after=c["w_after"], gate=c["gate"],
+                                         scale=c["scale"], dX=c[over], dB=c[other])
+            assert torch.equal(c[over], want["dX"]) and torch.equal(c[other], want["dB"])
 
 
 def test_backward_against_differences(dg):
