@@ -6,13 +6,18 @@
 // Backward, with dw' = f·dw:  ds_i = dw'_i   or   (dw'_i − Σ_j dw'_j s_j / S) / S,  zero elsewhere;
 //     dl_e = s_e (ds_e − Σ s ds)  (softmax)   or   ds_e s_e (1 − s_e)  (sigmoid).
 //
-// A score next to the border of the k-th is settled in FP64: FP32 scores within 4e-6 of a round's best are within their
-// rounding of it, so those candidates (rarely any) are computed again, and the selection is that of the exact scores
+// A score next to the border of the k-th is settled in FP64: FP32 scores within 1.5e-6 (sigmoid) of a round's best are
+// within their rounding of it, so those candidates (rarely any) are computed again, and the selection is that of the exact scores
 // whatever exp's last bits are. Logits that are NaN or -inf, and biases of -inf, are never selected; a token
 // with fewer than k others gets the index -1 and the weight 0 in the places left.
 //
-// One warp a token, E/32 logits a lane in registers. A round of the selection is two warp reductions (the largest key as an
-// ordered integer, the lowest index that has it).
+// One warp a token, E/32 logits a lane in registers. The selection runs on keys as ordered integers whose last bits are cut off
+// for the index, so that one number tells both: a lane sorts its own, and a round is one warp-wide maximum of the lanes' first
+// and a step of the lane that had it (four times fewer instructions than keys and indexes by themselves). It goes one round
+// further than k, so that wherever the cut bits (or a bias's rounding) could matter two neighbours of the sorted k + 1 are near each
+// other; only then (1 to 3% of the tokens) the rounds are made again with whole keys. The weights are computed from the selected
+// logits by one lane each. In the backward pass every logit's gradient but the selected ones' is −s·Σ s ds (or zero), so these
+// are stored as if none were selected, and the k lanes of the selected store theirs behind them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,63 +29,125 @@ namespace dg {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr float kNear = 4e-6f;
+// How near keys may be in FP32 and be told apart, relative to max(1, key). Sigmoid: its fast exponential and division are within 4e-7
+// of it, the sum's rounding 6e-8, two keys twice that; softmax: its sum of up to 37 terms one behind the other adds 2.2e-6.
+constexpr float kNearSigmoid = 1.5e-6f, kNearSoftmax = 8e-6f;
 
-// Larger floats have larger integers; what is never selected has 0.
+// Larger floats have larger integers; what is never selected (NaN, -inf) has 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
-  if (!(x > -INFINITY)) return 0;
   const uint32_t b = __float_as_uint(x);
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return x > -INFINITY ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ double warp_sum(double v) {
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// The scores of a lane's logits (index j·32 + lane), NaN and -inf scoring 0. Softmax: also the row's largest logit and sum.
-template <int VPL>
-__device__ __forceinline__ void scores(const float (&l)[VPL], bool sigmoid, float (&s)[VPL], float& top) {
-  if (sigmoid) {
-    top = 0.0f;
+__device__ __forceinline__ float sigmoid(float x) { return x > -INFINITY ? 1.0f / (1.0f + expf(-x)) : 0.0f; }   // (NaN: 0 too)
+
+// A lane's logits: of every 128 four neighbours (QUADS: E a multiple of four, rows that start on 16 bytes, BF16 on 8), or every 32nd.
+template <bool QUADS>
+__device__ __forceinline__ int expert_of(int j, int lane) {
+  return QUADS ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane;
+}
+template <bool QUADS, int VPL, typename T>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&l)[VPL]) {
+  if constexpr (QUADS) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) s[j] = l[j] > -INFINITY ? 1.0f / (1.0f + expf(-l[j])) : 0.0f;
-    return;
+    for (int j = 0; j < VPL; j += 4) {
+      const int e = expert_of<true>(j, lane);
+      if (e < E) {
+        if constexpr (sizeof(T) == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(row + e);
+          l[j] = v.x, l[j + 1] = v.y, l[j + 2] = v.z, l[j + 3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(row + e);
+          l[j] = bf16_lo(v.x), l[j + 1] = bf16_hi(v.x), l[j + 2] = bf16_lo(v.y), l[j + 3] = bf16_hi(v.y);
+        }
+      } else {
+        l[j] = l[j + 1] = l[j + 2] = l[j + 3] = -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) l[j] = j * 32 + lane < E ? to_f32(row[j * 32 + lane]) : -INFINITY;
   }
-  uint32_t best = 0;
+}
+
+// The softmax of a row: its largest logit and 1 / Σ exp(l - largest) (0 where there is none); NaN and -inf count as nothing.
+struct Softmax {
+  float top, inverse;
+  __device__ __forceinline__ float operator()(float l) const { return l > -INFINITY ? expf(l - top) * inverse : 0.0f; }
+};
+// (exps: those of the lane's logits, for whoever wants them all)
+template <int VPL>
+__device__ __forceinline__ Softmax softmax_of(const float (&l)[VPL], float (&exps)[VPL]) {
+  float best = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) best = max(best, ordered(l[j]));
-  top = unordered(__reduce_max_sync(0xffffffffu, best));
+  for (int j = 0; j < VPL; ++j) best = fmaxf(best, l[j]);   // (a NaN is passed over)
+  Softmax s;
+  s.top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    s[j] = l[j] > -INFINITY ? expf(l[j] - top) : 0.0f;
-    sum += s[j];
+    exps[j] = l[j] > -INFINITY ? expf(l[j] - s.top) : 0.0f;
+    sum += exps[j];
   }
   sum = warp_sum(sum);
-  const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) s[j] *= f;
+  s.inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
+  return s;
 }
 
-template <int VPL, typename T>
-__device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&l)[VPL]) {
+// The keys of a lane's logits, as ordered integers; 0 for what is never selected. (Their errors are far below the near ones'
+// distance: the fast exponential's counts by s(1 - s), the reciprocal's by s.)
+template <bool QUADS, int VPL>
+__device__ __forceinline__ void keys_of(const RouteArgs& a, const Softmax& soft, const float (&l)[VPL], const float (&exps)[VPL], int lane,
+                                        uint32_t (&key)[VPL]) {
+  if (!a.bias) {
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) l[j] = j * 32 + lane < E ? to_f32(row[j * 32 + lane]) : -INFINITY;
+    for (int j = 0; j < VPL; ++j) key[j] = ordered(l[j]);
+    return;
+  }
+  float b[VPL];
+  load_logits<QUADS>(a.bias, a.E, lane, b);   // (-inf past the end)
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    float s;
+    if (a.sigmoid)
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-l[j])));
+    else
+      s = exps[j] * soft.inverse;
+    const uint32_t k = ordered(s + b[j]);
+    key[j] = l[j] > -INFINITY ? k : 0u;
+  }
 }
 
-// The best of the candidates (bit j of a lane: index j·32 + lane) by their exact scores. `total` is the softmax's exact sum,
-// or 0 while no round of this token has asked for it. Rare, so out of line and with the logits read again.
-template <typename T>
-__device__ __noinline__ int settle(const T* row, const float* bias, int E, uint32_t near, int lane, bool sigmoid, float top, double& total) {
-  if (!sigmoid && total == 0.0) {
+// Sorts a lane's numbers, the largest first (odd-even merge: Batcher, "Sorting networks and their applications", 1968).
+template <int N>
+__device__ __forceinline__ void sort_descending(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+            v[i + j] = hi, v[i + j + k] = lo;
+          }
+}
+
+// The best of the candidates (bit j of a lane) by their exact scores. `total` is the softmax's exact sum, or 0 while no round of
+// this token has asked for it. Rare, so out of line and with the logits read again.
+template <bool QUADS, typename T>
+__device__ __noinline__ int settle(const T* row, const float* bias, int E, uint32_t near, int lane, bool is_sigmoid, float top, double& total) {
+  if (!is_sigmoid && total == 0.0) {
     double part = 0.0;
     for (int e = lane; e < E; e += 32)
       if (to_f32(row[e]) > -INFINITY) part += exp((double)to_f32(row[e]) - (double)top);
@@ -89,8 +156,8 @@ __device__ __noinline__ int settle(const T* row, const float* bias, int E, uint3
   double most = -INFINITY;
   int winner = INT32_MAX;
   for (; near; near &= near - 1) {
-    const int e = (__ffs(near) - 1) * 32 + lane;
-    const double l = (double)to_f32(row[e]), v = (sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / total) + (double)bias[e];
+    const int e = expert_of<QUADS>(__ffs(near) - 1, lane);
+    const double l = (double)to_f32(row[e]), v = (is_sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / total) + (double)bias[e];
     if (v > most || winner == INT32_MAX) most = v, winner = e;
   }
 #pragma unroll
@@ -102,123 +169,172 @@ __device__ __noinline__ int settle(const T* row, const float* bias, int E, uint3
   return winner;
 }
 
-template <typename T, int VPL>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
+// The selection with whole keys, for tokens with near ones: lane i's choice. Out of line; the logits are read again.
+template <int VPL, bool QUADS, typename T>
+__device__ __noinline__ int select_carefully(const RouteArgs& a, const T* row, const Softmax& soft, int lane) {
+  const float near = a.sigmoid ? kNearSigmoid : kNearSoftmax;
+  float l[VPL], exps[VPL] = {};
+  load_logits<QUADS>(row, a.E, lane, l);
+  if (!a.sigmoid)
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) exps[j] = l[j] > -INFINITY ? expf(l[j] - soft.top) : 0.0f;
+  uint32_t key[VPL];
+  keys_of<QUADS>(a, soft, l, exps, lane, key);
+  double total = 0.0;
+  int mine = -1;
+  for (int i = 0; i < a.k; ++i) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) best = max(best, key[j]);
+    best = __reduce_max_sync(0xffffffffu, best);
+    if (best == 0) break;
+    const float c = unordered(best);
+    const uint32_t border = a.bias ? max(1u, ordered(c - near * fmaxf(1.0f, fabsf(c)))) : best;
+    uint32_t candidates = 0;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) candidates |= (key[j] >= border ? 1u : 0u) << j;
+    // (a lane's experts ascend with j, so its first candidate is its lowest)
+    int winner = (int)__reduce_min_sync(0xffffffffu, candidates ? (unsigned)expert_of<QUADS>(__ffs(candidates) - 1, lane) : (unsigned)INT32_MAX);
+    const uint32_t lanes = __ballot_sync(0xffffffffu, candidates != 0);
+    if (a.bias && ((lanes & (lanes - 1)) || __any_sync(0xffffffffu, candidates & (candidates - 1))))
+      winner = settle<QUADS>(row, a.bias, a.E, candidates, lane, a.sigmoid, soft.top, total);
+#pragma unroll
+    for (int j = 0; j < VPL; ++j)
+      if (expert_of<QUADS>(j, lane) == winner) key[j] = 0;
+    if (lane == i) mine = winner;
+  }
+  return mine;
+}
+
+template <typename T, int VPL, bool QUADS>
+__global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(const RouteArgs a) {
+  constexpr uint32_t kIndex = VPL * 32 - 1;   // the bits of a key that its index takes
+  const int rounds = a.k < a.E ? a.k + 1 : a.k;
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
   for (long long t = (long long)blockIdx.x * kWarps + threadIdx.x / 32; t < a.T; t += (long long)gridDim.x * kWarps) {
-    float l[VPL], s[VPL], top;
     const T* row = static_cast<const T*>(a.logits) + t * a.E;
-    load_logits(row, a.E, lane, l);
-    scores(l, a.sigmoid, s, top);
+    float l[VPL];
+    load_logits<QUADS>(row, a.E, lane, l);
+    Softmax soft{};
+    float exps[VPL] = {};
+    if (!a.sigmoid) soft = softmax_of(l, exps);
     uint32_t key[VPL];
+    keys_of<QUADS>(a, soft, l, exps, lane, key);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = j * 32 + lane;
-      key[j] = ordered(!a.bias ? l[j] : e < a.E && l[j] > -INFINITY ? s[j] + a.bias[e] : -INFINITY);
-    }
-    double total = 0.0;   // softmax: the exact sum, once a near tie asks for it
-    int mine = -1;        // lane i keeps the i-th choice
-    float weight = 0.0f;
-    for (int i = 0; i < a.k; ++i) {
-      uint32_t best = 0;
+    for (int j = 0; j < VPL; ++j) key[j] = key[j] ? (key[j] & ~kIndex) | (kIndex - expert_of<QUADS>(j, lane)) : 0u;   // (the lower index is the larger number)
+    sort_descending(key);
+    uint32_t mine = 0, top = 0;   // lane i keeps the i-th
+    for (int i = 0; i < rounds; ++i) {
+      top = __reduce_max_sync(0xffffffffu, key[0]);
+      if (key[0] == top) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) best = max(best, key[j]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      if (best == 0) break;
-      int winner = INT32_MAX;
-#pragma unroll
-      for (int j = VPL - 1; j >= 0; --j)
-        if (key[j] == best) winner = j * 32 + lane;
-      winner = (int)__reduce_min_sync(0xffffffffu, (unsigned)winner);
-      if (a.bias) {
-        const float b = unordered(best);
-        const uint32_t border = max(1u, ordered(b - kNear * fmaxf(1.0f, fabsf(b))));
-        uint32_t near = 0;   // bit j
-#pragma unroll
-        for (int j = 0; j < VPL; ++j) near |= (key[j] >= border ? 1u : 0u) << j;
-        const int others = __popc(near) - (winner % 32 == lane ? 1 : 0);
-        if (__any_sync(0xffffffffu, others > 0)) winner = settle(row, a.bias, a.E, near, lane, a.sigmoid, top, total);
+        for (int j = 0; j + 1 < VPL; ++j) key[j] = key[j + 1];
+        key[VPL - 1] = 0;
       }
-      float w = 0.0f;
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (j * 32 + lane == winner) {
-          w = s[j];
-          key[j] = 0;
-        }
-      w = __shfl_sync(0xffffffffu, w, winner % 32);
-      if (lane == i) mine = winner, weight = w;
+      if (lane == i) mine = top;
+    }
+    // Whether a choice and the one behind it could change places: the same but for the cut bits, or (bias) within the rounding.
+    uint32_t behind = __shfl_down_sync(0xffffffffu, mine, 1);
+    if (lane == 31) behind = rounds == 33 ? top : 0u;   // (the 33rd has no lane)
+    bool near = behind != 0 && (mine ^ behind) <= kIndex;
+    if (a.bias && behind != 0) {
+      const float x = unordered(mine & ~kIndex), y = unordered(behind | kIndex);
+      near |= x - y <= (a.sigmoid ? kNearSigmoid : kNearSoftmax) * fmaxf(1.0f, fmaxf(fabsf(unordered(mine | kIndex)), fabsf(unordered(behind & ~kIndex))));
+    }
+    int choice = lane < a.k && mine ? (int)(kIndex - (mine & kIndex)) : -1;
+    if (__any_sync(0xffffffffu, near)) choice = select_carefully<VPL, QUADS>(a, row, soft, lane);
+    if (lane >= a.k) choice = -1;
+    float weight = 0.0f;
+    if (choice >= 0) {
+      const float x = to_f32(row[choice]);
+      weight = a.sigmoid ? sigmoid(x) : soft(x);
     }
     if (a.renorm) weight = weight / (warp_sum(weight) + 1e-20f);
     if (lane < a.k) {
-      a.ids[t * a.k + lane] = mine;
+      a.ids[t * a.k + lane] = choice;
       a.weights[t * a.k + lane] = weight * a.factor;
     }
   }
 }
 
-template <typename T, int VPL>
+template <typename T, int VPL, bool QUADS>
 __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const RouteArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
   for (long long t = (long long)blockIdx.x * kWarps + threadIdx.x / 32; t < a.T; t += (long long)gridDim.x * kWarps) {
-    float l[VPL], s[VPL], top;
-    load_logits(static_cast<const T*>(a.logits) + t * a.E, a.E, lane, l);
+    const T* row = static_cast<const T*>(a.logits) + t * a.E;
+    T* out = static_cast<T*>(a.dlogits) + t * a.E;
     int e = lane < a.k ? a.ids[t * a.k + lane] : -1;
-    if (e >= a.E) e = -1;
-    float d = e >= 0 ? a.factor * a.dweights[t * a.k + lane] : 0.0f;
-    scores(l, a.sigmoid, s, top);
-    float ds[VPL] = {};
+    float d = lane < a.k ? a.dweights[t * a.k + lane] : 0.0f;
+    float l[VPL];
+    if (!a.sigmoid) load_logits<QUADS>(row, a.E, lane, l);
+    if (e < 0 || e >= a.E) e = -1, d = 0.0f;
+    d *= a.factor;
+    const float x = e >= 0 ? to_f32(row[e]) : 0.0f;   // (behind the row's own loads: in L1 then)
+    Softmax soft{};
+    if (!a.sigmoid) soft = softmax_of(l, l);
+    const float s = e < 0 ? 0.0f : a.sigmoid ? sigmoid(x) : soft(x);
     if (a.renorm) {
-      float sel = 0.0f;   // the score of this lane's choice
-      for (int i = 0; i < a.k; ++i) {
-        const int at = __shfl_sync(0xffffffffu, e, i);
-        float v = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPL; ++j)
-          if (at == j * 32 + lane) v = s[j];
-        v = __shfl_sync(0xffffffffu, v, at & 31);
-        if (lane == i && at >= 0) sel = v;
-      }
-      const float total = warp_sum(sel) + 1e-20f, mean = warp_sum(d * sel) / total;
+      const float total = warp_sum(s) + 1e-20f, mean = warp_sum(d * s) / total;
       d = e >= 0 ? (d - mean) / total : 0.0f;
     }
-    for (int i = 0; i < a.k; ++i) {
-      const int at = __shfl_sync(0xffffffffu, e, i);
-      const float v = __shfl_sync(0xffffffffu, d, i);
+    const float along = a.sigmoid ? 0.0f : warp_sum(s * d);
+    // an expert chosen twice: each of its lanes has the sum
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    float all = d;
+    if (__any_sync(0xffffffffu, e >= 0 && (same & (same - 1)))) {
+      all = 0.0f;
+      for (int i = 0; i < 32; ++i) {
+        const float v = __shfl_sync(0xffffffffu, d, i);
+        if (same >> i & 1) all += v;
+      }
+    }
+    __syncwarp();   // dlogits may be logits: every lane has read what it needs
+    if constexpr (QUADS) {
+#pragma unroll
+      for (int j = 0; j < VPL; j += 4) {
+        const int c = expert_of<true>(j, lane);
+        if (c >= a.E) continue;
+        float v[4] = {};
+        if (!a.sigmoid)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = -along * (l[j + i] * soft.inverse);   // (exponentials by now)
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(out + c) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<uint2*>(out + c) = make_uint2(round_bf16x2(v[0], v[1]), round_bf16x2(v[2], v[3]));
+      }
+    } else {
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
-        if (at == j * 32 + lane) ds[j] += v;
+        if (j * 32 + lane < a.E) store_f32(out + j * 32 + lane, a.sigmoid ? 0.0f : -along * (l[j] * soft.inverse));
     }
-    float along = 0.0f;
-    if (!a.sigmoid) {
-#pragma unroll
-      for (int j = 0; j < VPL; ++j) along = fmaf(s[j], ds[j], along);
-      along = warp_sum(along);
-    }
-    T* out = static_cast<T*>(a.dlogits) + t * a.E;
-#pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (j * 32 + lane < a.E) store_f32(out + j * 32 + lane, a.sigmoid ? ds[j] * s[j] * (1.0f - s[j]) : s[j] * (ds[j] - along));
+    __syncwarp();   // (the selected ones' stores come behind)
+    if (e >= 0) store_f32(out + e, a.sigmoid ? all * s * (1.0f - s) : s * (all - along));
   }
 }
 
-template <typename T, int VPL>
+template <typename T, int VPL, bool QUADS>
 cudaError_t launch_one(const RouteArgs& a, bool backward, const StreamArgs& s) {
   const int grid = (int)s.limit.all((a.T + kWarps - 1) / kWarps);
-  return launch_plain(backward ? route_backward_kernel<T, VPL> : route_kernel<T, VPL>, grid, 32 * kWarps, 0, s, a);
+  return launch_plain(backward ? route_backward_kernel<T, VPL, QUADS> : route_kernel<T, VPL, QUADS>, grid, 32 * kWarps, 0, s, a);
 }
 
 template <typename T>
 cudaError_t launch_typed(const RouteArgs& a, bool backward, const StreamArgs& s) {
-  if (a.E <= 64) return launch_one<T, 2>(a, backward, s);
-  if (a.E <= 128) return launch_one<T, 4>(a, backward, s);
-  if (a.E <= 256) return launch_one<T, 8>(a, backward, s);
-  if (a.E <= 512) return launch_one<T, 16>(a, backward, s);
-  return launch_one<T, 32>(a, backward, s);
+  const uintptr_t places = reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.dlogits), bias = reinterpret_cast<uintptr_t>(a.bias);
+  auto pick = [&](auto vpl) {
+    constexpr int VPL = decltype(vpl)::value;
+    return a.E % 4 == 0 && places % (4 * sizeof(T)) == 0 && bias % 16 == 0 ? launch_one<T, VPL, true>(a, backward, s) : launch_one<T, VPL, false>(a, backward, s);
+  };
+  if (a.E <= 64) return launch_one<T, 2, false>(a, backward, s);
+  if (a.E <= 128) return pick(std::integral_constant<int, 4>{});
+  if (a.E <= 256) return pick(std::integral_constant<int, 8>{});
+  if (a.E <= 512) return pick(std::integral_constant<int, 16>{});
+  return pick(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
