@@ -35,8 +35,8 @@ namespace {
 enum Kind { kStreamUp, kStreamDown, kStreamDense };
 
 constexpr int kUnitBytes = 128;   // of a unit's rows
-// A stage of the ring holds a unit of R tiles of 16 rows: codes, then scales (E2M1: 12 bytes a row; E4M3: one or two words).
-constexpr int stage_bytes(int R) { return 16 * R * (kUnitBytes + 12); }
+// A stage of the ring holds a unit of R tiles of 16 rows: codes, then scales (E2M1: 16 bytes a row; E4M3: one or two words).
+constexpr int stage_bytes(int R) { return 16 * R * (kUnitBytes + 16); }
 
 struct FewArgs {
   const uint8_t* x;        // E4M3 rows: tokens (kStreamUp, kStreamDense) or the cast h of each (token, choice) (kStreamDown)
@@ -76,6 +76,10 @@ __device__ __forceinline__ void copy_16(uint32_t to, const uint8_t* from, int by
 }
 __device__ __forceinline__ void copy_4(uint32_t to, const void* from, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void copy_8(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
 }
 
 // The tokens of one pass (at most 32 of them): which experts they use, and where each (expert, token) pair's h row is.
@@ -205,6 +209,13 @@ __device__ __forceinline__ void mma_16x8x16(float2 (&c)[2], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same from zero.
+__device__ __forceinline__ void mma_16x8x16_zero(float2 (&c)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0].x), "=f"(c[0].y), "=f"(c[1].x), "=f"(c[1].y)
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Four E8M0 codes of a word as FP32, two a conversion (code 0 is a subnormal, 255 NaN).
 __device__ __forceinline__ void e8m0_x4(uint32_t w, float (&v)[4]) {
 #pragma unroll
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
   extern __shared__ __align__(16) uint8_t ring_of_all[];
   constexpr bool kRouted = KIND != kStreamDense, kFour = FORM == kMxfp4;
   constexpr int kUnitK = kFour ? 256 : 128, kRows = 16 * R, kStage = stage_bytes(R);
-  constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row
+  constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row, unless they start on eight bytes
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, W = blockDim.x / 32, g = lane / 4, t4 = lane % 4;
   float* const sums = reinterpret_cast<float*>(ring_of_all + (size_t)W * stages * kStage);   // [2][W][R][NT][4][32]
   const Routing route(reinterpret_cast<uint8_t*>(sums + 2 * W * R * NT * 128), a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
@@ -239,6 +250,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
   };
   const int word_steps = FORM == kFp8Packed ? (groups_k + 3) / 4 : groups_k;   // E4M3 weights' scales along K
   const uint8_t* const scales_end = static_cast<const uint8_t*>(a.sw) + (size_t)(kRouted ? a.E : 1) * a.rows * row_scales;
+  const bool eights = kFour && row_scales % 8 == 0 && reinterpret_cast<uintptr_t>(a.sw) % 8 == 0;   // E2M1: a unit's scales of a row in one piece
   // where this lane copies to in a stage: chunk lane % 8 of rows lane / 8 + 4j
   const int copy_row = lane / 8, copy_byte = (lane % 8) * 16;
   const uint32_t to_even = copy_row * kUnitBytes + ((lane % 8) ^ copy_row) * 16, to_odd = (copy_row + 4) * kUnitBytes + ((lane % 8) ^ (copy_row + 4)) * 16;
@@ -262,9 +274,9 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
       if constexpr (kFour) {
 #pragma unroll
         for (int i = 0; i < kScaleCopies; ++i) {
-          const int q = lane + 32 * i, l = q / 3, row = row_of(p.block, l);
-          const bool there = q < kRows * 3 && (KIND == kStreamUp || row < a.rows);
-          const size_t at = ((first_row + row) * row_scales & ~(size_t)3) + p.u * 8 + (q % 3) * 4;
+          const int q = lane + 32 * i, l = eights ? q : q / 3, row = row_of(p.block, l);
+          const bool there = l < kRows && (KIND == kStreamUp || row < a.rows);
+          const size_t at = ((first_row + row) * row_scales & ~(size_t)3) + p.u * 8 + (eights ? 0 : (q % 3) * 4);
           p_scales[i] = there ? static_cast<const uint8_t*>(a.sw) + at : scales_end;
         }
       } else {
@@ -290,13 +302,20 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
             if (p.block * kRows + copy_row + 4 * j < a.rows) copy(j, bytes);
         }
         if constexpr (kFour) {
-          // eight scale bytes of each row from any place: the three aligned words that hold them, as far as there are any
+          // eight scale bytes of each row: in one piece, or from any place the three aligned words that hold them, as far as there are any
+          if (eights) {
+            if (lane < kRows && p_scales[0] != scales_end) {   // (kRows is at most 32)
+              copy_8(to + kRows * kUnitBytes + lane * 16, p_scales[0]);
+              p_scales[0] += 8 * W;
+            }
+          } else {
 #pragma unroll
-          for (int i = 0; i < kScaleCopies; ++i) {
-            const ptrdiff_t left = scales_end - p_scales[i];
-            const int bytes = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-            if (i * 32 + lane < kRows * 3) copy_4(to + kRows * kUnitBytes + (lane + 32 * i) * 4, bytes ? p_scales[i] : static_cast<const uint8_t*>(a.sw), bytes);
-            p_scales[i] += 8 * W;
+            for (int i = 0; i < kScaleCopies; ++i) {
+              const ptrdiff_t left = scales_end - p_scales[i];
+              const int bytes = left >= 4 ? 4 : left > 0 ? (int)left : 0, q = lane + 32 * i;
+              if (q < kRows * 3) copy_4(to + kRows * kUnitBytes + (q / 3) * 16 + (q % 3) * 4, bytes ? p_scales[i] : static_cast<const uint8_t*>(a.sw), bytes);
+              p_scales[i] += 8 * W;
+            }
           }
         } else if (lane < (KIND == kStreamUp ? 2 : 1)) {
           // the scale of the rows' 128-row block (gate and up: two): an FP32 value, or the packed word with this K-block's byte
@@ -430,16 +449,25 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const uint8_t* rows = unit + (r * 16 + g) * kUnitBytes + t4 * 4;
-            const uint32_t* sc = reinterpret_cast<const uint32_t*>(unit + kRows * kUnitBytes + (r * 16 + g) * 12);
+            const uint8_t* sc = unit + kRows * kUnitBytes + (r * 16 + g) * 16;
+            uint2 c0 = *reinterpret_cast<const uint2*>(sc), c1 = *reinterpret_cast<const uint2*>(sc + 128);   // of rows g and g + 8
+            if (!eights) {
+              const uint32_t b0 = reinterpret_cast<const uint32_t*>(sc)[2], b1 = reinterpret_cast<const uint32_t*>(sc + 128)[2];
+              c0 = make_uint2(__funnelshift_r(c0.x, c0.y, shift[r][0]), __funnelshift_r(c0.y, b0, shift[r][0]));
+              c1 = make_uint2(__funnelshift_r(c1.x, c1.y, shift[r][1]), __funnelshift_r(c1.y, b1, shift[r][1]));
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               float s0[4], s1[4];
-              // (groups behind the end of K have bytes of another row: none, so that no NaN meets the zeros there)
-              const int left = a.K / 32 - u * 8 - b * 4;
-              const uint32_t there = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-              e8m0_x4(__funnelshift_r(sc[b], sc[b + 1], shift[r][0]) & there, s0);
-              e8m0_x4(__funnelshift_r(sc[24 + b], sc[25 + b], shift[r][1]) & there, s1);
-              float2 part[NT][2] = {};
+              uint32_t e0 = b ? c0.y : c0.x, e1 = b ? c1.y : c1.x;
+              if (!eights) {   // groups behind the end of K have bytes of another row: none, so that no NaN meets the zeros there
+                const int left = a.K / 32 - u * 8 - b * 4;
+                const uint32_t there = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+                e0 &= there, e1 &= there;
+              }
+              e8m0_x4(e0, s0);
+              e8m0_x4(e1, s1);
+              float2 part[NT][2];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int chunk = b * 4 + j;
@@ -450,13 +478,13 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                   const uint32_t x0 = o.x[i][2 * chunk], x1 = o.x[i][2 * chunk + 1];
-                  float2 m[2] = {};
-                  mma_16x8x16(m, a0, e4m3_lo(x0), e4m3_hi(x0));
+                  float2 m[2];
+                  mma_16x8x16_zero(m, a0, e4m3_lo(x0), e4m3_hi(x0));
                   mma_16x8x16(m, a1, e4m3_lo(x1), e4m3_hi(x1));
-                  part[i][0].x = fmaf(m[0].x, s0[j], part[i][0].x);
-                  part[i][0].y = fmaf(m[0].y, s0[j], part[i][0].y);
-                  part[i][1].x = fmaf(m[1].x, s1[j], part[i][1].x);
-                  part[i][1].y = fmaf(m[1].y, s1[j], part[i][1].y);
+                  part[i][0].x = j ? fmaf(m[0].x, s0[j], part[i][0].x) : m[0].x * s0[j];
+                  part[i][0].y = j ? fmaf(m[0].y, s0[j], part[i][0].y) : m[0].y * s0[j];
+                  part[i][1].x = j ? fmaf(m[1].x, s1[j], part[i][1].x) : m[1].x * s1[j];
+                  part[i][1].y = j ? fmaf(m[1].y, s1[j], part[i][1].y) : m[1].y * s1[j];
                 }
               }
 #pragma unroll
@@ -590,7 +618,7 @@ struct FewPlan {
 };
 // Sixteen warps fill an SM, twelve on units of two tiles (whose stages are twice as large; 16 x 2 stages, 14 x 3 and 8 x 4 take 5% longer
 // than 12 x 3 for one token through 8 of 32 experts of 7168x2048, E4M3). The fewer warps run, the longer a step of each stays the same; so
-// the least of rounds of items x turns of a warp x warps. `items` are those of a whole GPU, whatever dg_set_num_sms says.
+// the least of rounds of items x turns of a warp (and 0.3 for the item's own steps) x warps. `items` are those of a whole GPU, whatever dg_set_num_sms says.
 FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, const SmLimit& limit) {
   const int most = R == 2 ? 12 : 16;
   FewPlan p{};
@@ -598,7 +626,7 @@ FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, cons
   for (int w = most; w >= 4; --w)
     for (int c = 1; c * w <= most; ++c) {
       const double rounds = (double)((items + (long long)kFewSms * c - 1) / ((long long)kFewSms * c));
-      const double cost = rounds * ((units + w - 1) / w) * most;
+      const double cost = rounds * ((units + w - 1) / w + 0.3) * most;
       if (cost < p.cost * (1.0 - 1e-9)) p.cost = cost, p.warps = w, p.ctas = c;
     }
   if (limit.capped) p.ctas = 1;
