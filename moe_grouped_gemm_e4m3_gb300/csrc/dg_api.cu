@@ -924,6 +924,7 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 dg_status check_norm_sizes(int M, int N) {
   if (M < 0 || N < 0) return fail(DG_ERR_INVALID_ARG, "negative size");
   if (N > dg::kNormMaxN) return fail(DG_ERR_UNSUPPORTED, "N is beyond " + std::to_string(dg::kNormMaxN));
+  if (M > INT_MAX - 1024) return fail(DG_ERR_UNSUPPORTED, "too many rows");
   return DG_OK;
 }
 
@@ -1023,6 +1024,7 @@ dg_status run_route(const void* logits, const float* bias, int32_t* ids, float* 
   if (E > dg::kRouteMaxE || k > dg::kRouteMaxK)
     return fail(DG_ERR_UNSUPPORTED, "at most " + std::to_string(dg::kRouteMaxE) + " experts and " + std::to_string(dg::kRouteMaxK) + " of them a token");
   if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID) return fail(DG_ERR_INVALID_ARG, "score must be DG_SCORE_SOFTMAX or DG_SCORE_SIGMOID");
+  if (T > INT_MAX - 1024) return fail(DG_ERR_UNSUPPORTED, "too many tokens");
   if (!std::isfinite((float)factor)) return fail(DG_ERR_INVALID_ARG, "factor must be finite");
   if (T == 0) return DG_OK;
   if (!logits || !ids || (backward ? !dweights || !dlogits : !weights)) return fail(DG_ERR_INVALID_ARG, "null tensor pointer");
@@ -1057,7 +1059,7 @@ dg_status run_moe(const uint8_t* A, const void* sA, const uint8_t* W1, const voi
     return fail(DG_ERR_ALIGNMENT, "A, W1, W2 and the workspace must be 16-byte aligned");
   if (!aligned(sA, 4) || !aligned(sW1, 4) || !aligned(sW2, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(Y, out_f32 ? 4 : 2))
     return fail(DG_ERR_ALIGNMENT, "scales, ids and weights must be 4-byte aligned, Y to its element");
-  if ((long long)T * k > INT_MAX / 2 || (long long)E * (I / 8) > INT_MAX / 2 || K > INT_MAX - 1024 || I > INT_MAX / 4 || N > INT_MAX - 1024 || T > INT_MAX - 1024)
+  if ((long long)T * k * (I / 128) > INT_MAX / 2 || (long long)E * (I / 8) > INT_MAX / 2 || K > INT_MAX - 1024 || I > INT_MAX / 4 || N > INT_MAX - 1024 || T > INT_MAX - 1024)
     return fail(DG_ERR_UNSUPPORTED, "too many tokens or columns");
   const long long need = dg::moe_workspace_bytes(T, k, I);
   if (!workspace || workspace_bytes < need)

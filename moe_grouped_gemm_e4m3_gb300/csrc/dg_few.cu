@@ -85,31 +85,39 @@ __device__ __forceinline__ void copy_8(uint32_t to, const void* from) {
 // The tokens of one pass (at most 32 of them): which experts they use, and where each (expert, token) pair's h row is.
 struct Routing {
   uint32_t* mask;      // [E] tokens of each expert
+  float* chosen;       // [pairs] the choices' weights as given
   float* weight;       // of a pair: its weight (an expert chosen twice: their sum)
+  uint16_t* choice;    // [pairs] the choices as given, kNone for no expert
   uint16_t* active;    // [E] the active experts, ascending
   uint16_t* first;     // [E] of each active expert: its first pair
   uint16_t* row;       // of a pair: the choice t·k + j (within the pass) whose h row it uses
   int* count;          // of active experts
-  __host__ __device__ static size_t bytes(int E, int pairs) { return (size_t)E * 8 + (size_t)pairs * 8 + 16; }
+  static constexpr uint16_t kNone = 0xFFFF;
+  __host__ __device__ static size_t bytes(int E, int pairs) { return (size_t)E * 8 + (size_t)pairs * 12 + 16; }
   __device__ Routing(uint8_t* at, int E, int pairs) {
     mask = reinterpret_cast<uint32_t*>(at);
-    weight = reinterpret_cast<float*>(mask + E);
-    active = reinterpret_cast<uint16_t*>(weight + pairs);
+    chosen = reinterpret_cast<float*>(mask + E);
+    weight = chosen + pairs;
+    choice = reinterpret_cast<uint16_t*>(weight + pairs);
+    active = choice + pairs;
     first = active + E;
     row = first + E;
     count = reinterpret_cast<int*>(at + (bytes(E, pairs) - 16));
   }
 };
 
-__device__ void build_routing(const Routing& r, const FewArgs& a, int t0, int tokens, bool with_weights) {
+// The active experts of a pass: all that the copies of weights need to begin.
+__device__ void find_active(const Routing& r, const FewArgs& a, int t0, int tokens, bool with_weights) {
   const int tid = threadIdx.x, n = tokens * a.k;
   __syncthreads();   // the last pass is done with it
   for (int e = tid; e < a.E; e += blockDim.x) r.mask[e] = 0;
   __syncthreads();
-  const int32_t* ids = a.ids + (size_t)t0 * a.k;
   for (int i = tid; i < n; i += blockDim.x) {
-    const int e = ids[i];
-    if (e >= 0 && e < a.E)
+    const int e = a.ids[(size_t)t0 * a.k + i];
+    const bool some = e >= 0 && e < a.E;
+    if (with_weights) r.chosen[i] = a.weights[(size_t)t0 * a.k + i];
+    r.choice[i] = some ? (uint16_t)e : Routing::kNone;
+    if (some)
       atomicOr(&r.mask[e], 1u << (i / a.k));
     else if (e != -1 && blockIdx.x == 0)
       atomicOr(a.status, kStatusBadGroup);
@@ -121,6 +129,7 @@ __device__ void build_routing(const Routing& r, const FewArgs& a, int t0, int to
       const int e = e0 + tid;
       const uint32_t mask = e < a.E ? r.mask[e] : 0;
       const uint32_t some = __ballot_sync(0xffffffffu, mask != 0);
+      if (some == 0) continue;
       int before = __popc(mask);
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, before, o);
@@ -139,18 +148,21 @@ __device__ void build_routing(const Routing& r, const FewArgs& a, int t0, int to
     if (tid == 0) *r.count = count;
   }
   __syncthreads();
-  // each expert's pairs
-  for (int at = tid / 32; at < *r.count; at += blockDim.x / 32) {
-    const int e = r.active[at], t = tid % 32;
+}
+
+// Each active expert's pairs (beside the first copies).
+__device__ void find_pairs(const Routing& r, const FewArgs& a, bool with_weights) {
+  for (int at = threadIdx.x / 32; at < *r.count; at += blockDim.x / 32) {
+    const int e = r.active[at], t = threadIdx.x % 32;
     const uint32_t mask = r.mask[e];
     if (mask >> t & 1) {
       const int pair = r.first[at] + __popc(mask & ((1u << t) - 1));
       int first = -1;
       float w = 0.0f;
       for (int j = 0; j < a.k; ++j)
-        if (ids[t * a.k + j] == e) {
+        if (r.choice[t * a.k + j] == e) {
           if (first < 0) first = j;
-          if (with_weights) w += a.weights[(size_t)(t0 + t) * a.k + j];
+          if (with_weights) w += r.chosen[t * a.k + j];
         }
       r.row[pair] = (uint16_t)(t * a.k + first);
       r.weight[pair] = w;
@@ -259,7 +271,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
 
   for (int t0 = 0; t0 < a.T; t0 += 8 * NT) {
     const int tokens = a.T - t0 < 8 * NT ? a.T - t0 : 8 * NT;
-    if constexpr (kRouted) build_routing(route, a, t0, tokens, KIND == kStreamDown);
+    if constexpr (kRouted) find_active(route, a, t0, tokens, KIND == kStreamDown);
     const int active = kRouted ? *route.count : 1;
 
     // ---- copies
@@ -414,6 +426,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
     };
 
     for (int s = 0; s < stages - 1; ++s) issue();
+    if constexpr (kRouted) find_pairs(route, a, KIND == kStreamDown);
     if constexpr (KIND == kStreamDown) {
       if (!waited) griddep_wait(), waited = true;
     }

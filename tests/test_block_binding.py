@@ -97,7 +97,7 @@ def test_the_library_refuses_norms():
         return lib.dg_residual_norm_bf16(*_p(X, B, wa, gate, scale, W), eps, *_p(R, Y, Yq, sY, rstd, ra), M, N, None)
 
     assert norm(X=None) == INVALID and norm(M=-1) == INVALID and norm(N=-1) == INVALID
-    assert norm(M=0) == OK and norm(N=0) == OK and norm(N=16385) == UNSUPPORTED
+    assert norm(M=0) == OK and norm(N=0) == OK and norm(N=16385) == UNSUPPORTED and norm(M=(1 << 31) - 1) == UNSUPPORTED
     assert norm(eps=-1.0) == INVALID and norm(eps=float("nan")) == INVALID and norm(eps=float("inf")) == INVALID
     assert norm(B=None) == INVALID and norm(B=None, wa=None, gate=None, scale=None, ra=None) == INVALID   # R without B
     assert norm(wa=None) == INVALID                              # rstd_after without the norm after
@@ -137,7 +137,7 @@ def test_the_library_refuses_routes():
 
     assert route(l=None) == INVALID and route(ids=None) == INVALID and route(w=None) == INVALID and route(T=-1) == INVALID
     assert route(E=0) == INVALID and route(k=0) == INVALID and route(k=9) == INVALID and route(score=2) == INVALID
-    assert route(E=1025) == UNSUPPORTED and route(E=64, k=33) == UNSUPPORTED and route(T=0) == OK
+    assert route(T=(1 << 31) - 1) == UNSUPPORTED and route(E=1025) == UNSUPPORTED and route(E=64, k=33) == UNSUPPORTED and route(T=0) == OK
     assert route(factor=float("nan")) == INVALID and route(factor=1e300) == INVALID
     assert route(l=_at(0) + 2) == ALIGN and route(b=X0 + 2) == ALIGN and route(ids=_at(1) + 1) == ALIGN
     assert lib.dg_route_topk_bf16(*_p(_at(0) + 1, None, _at(1), _at(2)), 0, 1, 1.0, 4, 8, 2, None) == ALIGN
@@ -165,7 +165,7 @@ def test_the_library_refuses_products_of_few_tokens():
             assert moe(name, **{off: X0 + 2}) == ALIGN, off
         assert moe(name, Y=_at(3) + 1) == ALIGN and moe(name, T=-1) == INVALID and moe(name, T=0) == OK and moe(name, N=0) == OK
         assert moe(name, k=0) == INVALID and moe(name, E=0) == INVALID and moe(name, K=0) == INVALID and moe(name, I=0) == INVALID
-        assert moe(name, k=33) == UNSUPPORTED and moe(name, E=1025) == UNSUPPORTED and moe(name, T=1 << 30, k=32) == UNSUPPORTED
+        assert moe(name, k=33) == UNSUPPORTED and moe(name, E=1025) == UNSUPPORTED and moe(name, T=1 << 30, k=32) == UNSUPPORTED and moe(name, T=1 << 28, k=8) == UNSUPPORTED
         assert moe(name, I=192) == ALIGN and moe(name, N=72) == ALIGN and moe(name, K=264) == ALIGN
         assert moe(name, size=100) == INVALID
     assert moe("_mxfp4", K=272) == ALIGN
