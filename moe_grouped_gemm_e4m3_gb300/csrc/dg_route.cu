@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
-  for (long long t = (long long)blockIdx.x * kWarps + threadIdx.x / 32; t < a.T; t += (long long)gridDim.x * kWarps) {
-    const T* row = static_cast<const T*>(a.logits) + t * a.E;
+  for (unsigned t = blockIdx.x * kWarps + threadIdx.x / 32; t < (unsigned)a.T; t += gridDim.x * kWarps) {   // (T and the step: below 2^31 each)
+    const T* row = static_cast<const T*>(a.logits) + (size_t)t * (unsigned)a.E;
+    const size_t to = (size_t)t * (unsigned)a.k + lane;
     float l[VPL];
     load_logits<QUADS>(row, a.E, lane, l);
     Softmax soft{};
@@ -251,10 +252,10 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
       const float x = to_f32(row[choice]);
       weight = a.sigmoid ? sigmoid(x) : soft(x);
     }
-    if (a.renorm) weight = weight / (warp_sum(weight) + 1e-20f);
+    if (a.renorm) weight = __fdiv_rn(weight, warp_sum(weight) + 1e-20f);
     if (lane < a.k) {
-      a.ids[t * a.k + lane] = choice;
-      a.weights[t * a.k + lane] = weight * a.factor;
+      a.ids[to] = choice;
+      a.weights[to] = weight * a.factor;
     }
   }
 }
@@ -264,11 +265,12 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const Route
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x % 32;
-  for (long long t = (long long)blockIdx.x * kWarps + threadIdx.x / 32; t < a.T; t += (long long)gridDim.x * kWarps) {
-    const T* row = static_cast<const T*>(a.logits) + t * a.E;
-    T* out = static_cast<T*>(a.dlogits) + t * a.E;
-    int e = lane < a.k ? a.ids[t * a.k + lane] : -1;
-    float d = lane < a.k ? a.dweights[t * a.k + lane] : 0.0f;
+  for (unsigned t = blockIdx.x * kWarps + threadIdx.x / 32; t < (unsigned)a.T; t += gridDim.x * kWarps) {   // (T and the step: below 2^31 each)
+    const T* row = static_cast<const T*>(a.logits) + (size_t)t * (unsigned)a.E;
+    const size_t to = (size_t)t * (unsigned)a.k + lane;
+    T* out = static_cast<T*>(a.dlogits) + (size_t)t * (unsigned)a.E;
+    int e = lane < a.k ? a.ids[to] : -1;
+    float d = lane < a.k ? a.dweights[to] : 0.0f;
     float l[VPL];
     if (!a.sigmoid) load_logits<QUADS>(row, a.E, lane, l);
     if (e < 0 || e >= a.E) e = -1, d = 0.0f;
