@@ -209,9 +209,12 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 8 : 1) norm_kerne
     columns_of<VEC>(a.w, c, N, before[i]);
   }
   int turn = 0;
+  const float* const gate = a.b ? a.gate : nullptr;
+  float gate_ahead = gate && (int)blockIdx.x < a.M ? gate[blockIdx.x] : 1.0f;   // the next row's, from L2 or farther
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
     const size_t at = (size_t)m * N;
-    float f = a.b && a.gate ? a.gate[m] : 1.0f;   // of the whole row
+    float f = gate_ahead;   // of the whole row
+    if (gate && m + gridDim.x < a.M) gate_ahead = gate[m + gridDim.x];
     rows.arrive(m, gridDim.x);
     Eight r[V] = {};
 #pragma unroll
@@ -404,7 +407,9 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 4 : 1) norm_backw
     int turn = 0;
     if (rows.stages >= 3) {
       // One row's sums are formed beside the gradients of the row before, so the reduction's latency is behind those.
-      Row row = row_of(part);
+      // (its scalars, from L2 or farther, are asked for a row earlier still)
+      const auto ahead_of = [&](long long m) { return row_of(m < a.M ? m : part); };
+      Row row = row_of(part), then = ahead_of(part + a.parts);
       asm volatile("cp.async.wait_group 1;" ::: "memory");   // (of the two rows asked for)
       if (reduce) {
         row_sums(part, rows.head, row.rs, sums);
@@ -414,11 +419,10 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 4 : 1) norm_backw
         const long long next = m + a.parts;
         const int at = rows.head;
         const bool more = next < a.M;
-        Row then = row;
+        const Row later = ahead_of(next + a.parts);
         float more_sums[3] = {0.0f, 0.0f, 0.0f};
         rows.leave();
         if (more) {
-          then = row_of(next);
           rows.arrive_keeping(next, a.parts);
           if (reduce) {
             turn ^= 1;
@@ -429,6 +433,7 @@ __global__ void __launch_bounds__(V == 1 ? 128 : 512, V == 1 ? 4 : 1) norm_backw
         gradients(m, at, row, sums);
         if (more && reduce) block_part(more_sums, red[turn], warps);
         row = then;
+        then = later;
 #pragma unroll
         for (int k = 0; k < 3; ++k) sums[k] = more_sums[k];
       }
