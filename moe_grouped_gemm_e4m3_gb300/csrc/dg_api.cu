@@ -1059,7 +1059,7 @@ dg_status run_moe(const uint8_t* A, const void* sA, const uint8_t* W1, const voi
     return fail(DG_ERR_ALIGNMENT, "A, W1, W2 and the workspace must be 16-byte aligned");
   if (!aligned(sA, 4) || !aligned(sW1, 4) || !aligned(sW2, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(Y, out_f32 ? 4 : 2))
     return fail(DG_ERR_ALIGNMENT, "scales, ids and weights must be 4-byte aligned, Y to its element");
-  if ((long long)T * k * (I / 128) > INT_MAX / 2 || (long long)E * (I / 8) > INT_MAX / 2 || K > INT_MAX - 1024 || I > INT_MAX / 4 || N > INT_MAX - 1024 || T > INT_MAX - 1024)
+  if ((long long)T * k * (I / 128) > INT_MAX / 2 || (long long)E * 2 * I > INT_MAX - 1024 || K > INT_MAX - 1024 || I > INT_MAX / 4 || N > INT_MAX - 1024 || T > INT_MAX - 1024)
     return fail(DG_ERR_UNSUPPORTED, "too many tokens or columns");
   const long long need = dg::moe_workspace_bytes(T, k, I);
   if (!workspace || workspace_bytes < need)

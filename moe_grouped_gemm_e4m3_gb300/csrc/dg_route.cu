@@ -18,6 +18,9 @@
 // other; only then (1 to 3% of the tokens) the rounds are made again with whole keys. The weights are computed from the selected
 // logits by one lane each. In the backward pass every logit's gradient but the selected ones' is −s·Σ s ds (or zero), so these
 // are stored as if none were selected, and the k lanes of the selected store theirs behind them.
+//
+// Bound by its instructions (690 a token of 256 experts with a bias, 537 without): 16384x256 sigmoid scores with a bias 16.5 us,
+// where the read takes 2.6; backward of 16381x160 softmax scores 7 to 9 us (3.2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

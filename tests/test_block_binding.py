@@ -165,7 +165,7 @@ def test_the_library_refuses_products_of_few_tokens():
             assert moe(name, **{off: X0 + 2}) == ALIGN, off
         assert moe(name, Y=_at(3) + 1) == ALIGN and moe(name, T=-1) == INVALID and moe(name, T=0) == OK and moe(name, N=0) == OK
         assert moe(name, k=0) == INVALID and moe(name, E=0) == INVALID and moe(name, K=0) == INVALID and moe(name, I=0) == INVALID
-        assert moe(name, k=33) == UNSUPPORTED and moe(name, E=1025) == UNSUPPORTED and moe(name, T=1 << 30, k=32) == UNSUPPORTED and moe(name, T=1 << 28, k=8) == UNSUPPORTED
+        assert moe(name, k=33) == UNSUPPORTED and moe(name, E=1025) == UNSUPPORTED and moe(name, T=1 << 30, k=32) == UNSUPPORTED and moe(name, T=1 << 28, k=8) == UNSUPPORTED and moe(name, E=1024, I=1 << 20) == UNSUPPORTED
         assert moe(name, I=192) == ALIGN and moe(name, N=72) == ALIGN and moe(name, K=264) == ALIGN
         assert moe(name, size=100) == INVALID
     assert moe("_mxfp4", K=272) == ALIGN
