@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
   const uint32_t to_even = copy_row * kUnitBytes + ((lane % 8) ^ copy_row) * 16, to_odd = (copy_row + 4) * kUnitBytes + ((lane % 8) ^ (copy_row + 4)) * 16;
   const size_t four_rows = (size_t)4 * row_bytes, eight_rows = 2 * four_rows, half_rows = (size_t)half * row_bytes;
   bool waited = KIND != kStreamDown;
+  int buffer = 0;   // of the sums: by turns over the items of all passes, so that none is written while the item before is still added up
 
   for (int t0 = 0; t0 < a.T; t0 += 8 * NT) {
     const int tokens = a.T - t0 < 8 * NT ? a.T - t0 : 8 * NT;
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
     }
     Cursor<KIND> c;
     c.start(warp, units_k, active, blocks);
-    int stage = 0, buffer = 0;
+    int stage = 0;
     for (; c.item_left(active, blocks); buffer ^= 1) {
       const int item_at = c.at, item_block = c.block;
       float2 acc[R][NT][2] = {};

@@ -311,6 +311,29 @@ def test_every_code_and_every_scale(dg):
     assert torch.equal(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("N", [16, 5000])
+@pytest.mark.parametrize("K", [32, 1056])
+def test_four_bit_passes_follow_one_another(dg, N, K):
+    """Many passes of 32 rows in one call, of one item a CTA and hardly any work, give the bits of a call for each pass."""
+    M = 32 * 60 + 7
+    g = _gen(11)
+    A, _ = _rows(g, M, K)
+    scales = _scales(g, False, _cdiv(K, 128), M)      # one a row and group, laid out for each call below
+    B, sB = _four(g, N, K)
+
+    def product(rows):
+        n = rows.stop - rows.start
+        s = torch.zeros(scales.shape[0], 4 * _cdiv(n, 4), device="cuda")
+        s[:, :n] = scales[:, rows]
+        D = torch.empty(n, N, device="cuda")
+        dg.dg_fp8_mxfp4_gemm_nt_f32(A[rows], s, B, sB, D)
+        return D
+
+    want = torch.cat([product(slice(m, min(m + 32, M))) for m in range(0, M - 7, 32)])
+    for _ in range(20):
+        assert torch.equal(product(slice(0, M))[:M - 7], want)
+
+
 def test_four_bit_launch_settings(dg, monkeypatch):
     g = _gen(1)
     A, sA = _rows(g, 11, 1120)
