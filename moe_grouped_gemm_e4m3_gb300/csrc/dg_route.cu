@@ -112,7 +112,7 @@ __device__ __forceinline__ void keys_of(const RouteArgs& a, const Softmax& soft,
                                         uint32_t (&key)[VPL]) {
   if (!a.bias) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = ordered(l[j]);
+    for (int j = 0; j < VPL; ++j) key[j] = ordered(l[j] + 0.0f);   // (-0 ties with 0)
     return;
   }
   float b[VPL];

@@ -96,6 +96,19 @@ def test_masked_logits(dg, score, bias):
     _check(dg, l, 6, b if bias else None, score, True, 2.0)
 
 
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_zeros_of_both_signs_tie(dg, score, dt):
+    """-0 and 0 are the same logit: the lowest index first, with and without a bias."""
+    l = torch.zeros(3, 136, device="cuda", dtype=dt)
+    l[0, ::2] = -0.0
+    l[1, 1::2] = -0.0
+    l[2, :70], l[2, 70:] = -0.0, -1.0
+    zero = torch.zeros(136, device="cuda")
+    for bias in (None, zero, -zero):
+        _check(dg, l, 9, bias, score, True, 1.0)
+
+
 def _gradient(l, ids, dw, score, renorm, factor):
     """From the formulas, in 64 bits, with the sizes of the terms that are added."""
     s = R.scores(l.float(), score)
