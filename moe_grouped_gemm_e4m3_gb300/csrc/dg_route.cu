@@ -4,7 +4,7 @@
 // the logits themselves, which order the same way and have no rounding), ties to the lowest index, in descending order.
 //     w_i = f·s_i                     or, normalised again,  w_i = f·s_i / S,  S = Σ_selected s + 1e-20
 // Backward, with dw' = f·dw:  ds_i = dw'_i   or   (dw'_i − Σ_j dw'_j s_j / S) / S,  zero elsewhere;
-//     dl_e = s_e (ds_e − Σ s ds)  (softmax)   or   ds_e s_e (1 − s_e)  (sigmoid).
+//     dl_e = s_e (ds_e − Σ s ds)  (softmax)   or   ds_e s_e (1 − s_e)  (sigmoid; 1 − s(l) = s(−l)).
 //
 // A score next to the border of the k-th is settled in FP64: FP32 scores within 1.5e-6 (sigmoid) of a round's best are
 // within their rounding of it, so those candidates (rarely any) are computed again, and the selection is that of the exact scores
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_backward_kernel(const Route
         if (j * 32 + lane < a.E) store_f32(out + j * 32 + lane, a.sigmoid ? 0.0f : -along * (l[j] * soft.inverse));
     }
     __syncwarp();   // (the selected ones' stores come behind)
-    if (e >= 0) store_f32(out + e, a.sigmoid ? all * s * (1.0f - s) : s * (all - along));
+    if (e >= 0) store_f32(out + e, a.sigmoid ? all * s * sigmoid(-x) : s * (all - along));   // (1 - s without its cancellation)
   }
 }
 

@@ -179,6 +179,16 @@ def test_backward_against_differences(dg, score, renorm):
         assert abs(slope - float((dl.double() * v).sum())) <= 2.0 ** -12
 
 
+def test_backward_of_saturated_sigmoids(dg):
+    """s(1 - s) where s rounds to one in FP32: relative to the value itself, exp and a division for each factor below 2^-20."""
+    l = torch.linspace(10.0, 40.0, 128, device="cuda").view(2, 64)
+    ids = torch.arange(32, dtype=torch.int32, device="cuda").repeat(2, 1)
+    dl = dg.dg_route_topk_backward(torch.ones(2, 32, device="cuda"), l, ids, torch.empty_like(l), score="sigmoid", renormalize=False)
+    x = l[:, :32].double()
+    want = torch.sigmoid(x) * torch.sigmoid(-x)
+    assert bool(((dl[:, :32].double() - want).abs() <= 2.0 ** -20 * want).all()) and bool((dl[:, 32:] == 0).all())
+
+
 def test_masked_logits_have_no_gradient(dg):
     l, _ = _logits(3, 64)
     l[:, 30:] = -torch.inf
