@@ -468,7 +468,7 @@ dg_status dg_residual_norm_f32_ue8m0(const float* X, const float* B, const float
  *     dB = rstd_after·(Q·w_after - bh·mean(Q·w_after·bh)), dw_after = sum_m Q·bh   (without w_after: dB = Q)
  * Outputs are written, not added to; each may be NULL. dX (also the gradient of the residual path) and dB are rounded once and
  * may each be one of the inputs itself. dgate [M]; dW, dscale, dw_after [N] in FP32, summed in an order that depends on
- * M and N alone (with M = 0 they are zero). workspace: device memory of at least
+ * M and N alone (with M = 0 they are zero; with N = 0 nothing is written). workspace: device memory of at least
  * dg_residual_norm_backward_workspace(M, N) bytes, 16-byte aligned, of this call alone until it has finished (needed only with
  * dW, dscale or dw_after).
  */

@@ -889,7 +889,8 @@ def _workspace(nbytes, given, stream):
     whatever reuses it comes after the call (and which a graph being captured owns)."""
     torch = _torch()
     if given is not None:
-        return given, _ptr(given, "workspace", (torch.uint8,)), given.numel()
+        (p,) = _pointers_here((given, "workspace", (torch.uint8,), getattr(given, "shape", ())))
+        return given, p, given.numel()
     if stream is None:
         t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     else:

@@ -299,6 +299,7 @@ struct Workspace {
         return;
       }
       at = c.ptr(given, kByte, t->sizes());
+      c.here();
       bytes = t->numel();
     } else if (stream != Py_None) {
       c.ok = false;

@@ -70,6 +70,24 @@ def test_wrong_types_and_things_that_are_no_tensors_are_refused(call, arg):
             getattr(dg, call)(**{**CALLS[call], arg: bad})
 
 
+def test_workspaces_are_checked_like_any_tensor(monkeypatch):
+    """Their type, their place and their device, which has to be the current one."""
+    monkeypatch.setattr(dg, "_torch", lambda: torch)      # (without its start of the driver)
+    for bad in ([1], torch.zeros(8), u8(8)):
+        with pytest.raises((TypeError, ValueError), match="workspace must be a torch.Tensor|workspace has dtype|workspace must be a CUDA tensor"):
+            dg._workspace(8, bad, None)
+
+    class Elsewhere:
+        dtype, shape, is_cuda, device = torch.uint8, (64,), True, torch.device("cuda", 1)
+        is_contiguous, data_ptr, numel = lambda s: True, lambda s: X0, lambda s: 64
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="cuda:1"):
+        dg._workspace(8, Elsewhere(), None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert dg._workspace(8, Elsewhere(), None)[1:] == (X0, 64)
+
+
 def test_scores_have_names():
     with pytest.raises(ValueError, match="softmax"):
         dg.dg_route_topk(**CALLS["dg_route_topk"], score="tanh")
