@@ -32,9 +32,10 @@ namespace dg {
 namespace {
 
 constexpr int kWarps = 4;
-// How near keys may be in FP32 and be told apart, relative to max(1, key). Sigmoid: its fast exponential and division are within 4e-7
-// of it, the sum's rounding 6e-8, two keys twice that; softmax: its sum of up to 37 terms one behind the other adds 2.2e-6.
-constexpr float kNearSigmoid = 1.5e-6f, kNearSoftmax = 8e-6f;
+// How near keys may be in FP32 and be told apart: the error of two scores, and the rounding of two sums with a bias, relative to those.
+// A sigmoid by the fast exponential and division is within 4e-7. A softmax's score is within 2.7e-6 of itself (its sum of up to 37 terms
+// one behind the other 2.2e-6), and no score is larger than that of the largest logit, 1 / Σ exp(l - largest).
+constexpr float kNearSigmoid = 1.2e-6f, kNearSoftmax = 6.5e-6f, kNearSum = 2.5e-7f;
 
 // Larger floats have larger integers; what is never selected (NaN, -inf) has 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -175,7 +176,7 @@ __device__ __noinline__ int settle(const T* row, const float* bias, int E, uint3
 // The selection with whole keys, for tokens with near ones: lane i's choice. Out of line; the logits are read again.
 template <int VPL, bool QUADS, typename T>
 __device__ __noinline__ int select_carefully(const RouteArgs& a, const T* row, const Softmax& soft, int lane) {
-  const float near = a.sigmoid ? kNearSigmoid : kNearSoftmax;
+  const float near = a.sigmoid ? kNearSigmoid : kNearSoftmax * soft.inverse;
   float l[VPL], exps[VPL] = {};
   load_logits<QUADS>(row, a.E, lane, l);
   if (!a.sigmoid)
@@ -192,7 +193,7 @@ __device__ __noinline__ int select_carefully(const RouteArgs& a, const T* row, c
     best = __reduce_max_sync(0xffffffffu, best);
     if (best == 0) break;
     const float c = unordered(best);
-    const uint32_t border = a.bias ? max(1u, ordered(c - near * fmaxf(1.0f, fabsf(c)))) : best;
+    const uint32_t border = a.bias ? max(1u, ordered(c - fmaf(kNearSum, fabsf(c), near))) : best;
     uint32_t candidates = 0;
 #pragma unroll
     for (int j = 0; j < VPL; ++j) candidates |= (key[j] >= border ? 1u : 0u) << j;
@@ -245,7 +246,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
     bool near = behind != 0 && (mine ^ behind) <= kIndex;
     if (a.bias && behind != 0) {
       const float x = unordered(mine & ~kIndex), y = unordered(behind | kIndex);
-      near |= x - y <= (a.sigmoid ? kNearSigmoid : kNearSoftmax) * fmaxf(1.0f, fmaxf(fabsf(unordered(mine | kIndex)), fabsf(unordered(behind & ~kIndex))));
+      const float apart = a.sigmoid ? kNearSigmoid : kNearSoftmax * soft.inverse;
+      near |= x - y <= fmaf(kNearSum, fmaxf(fabsf(unordered(mine | kIndex)), fabsf(unordered(behind & ~kIndex))), apart);
     }
     int choice = lane < a.k && mine ? (int)(kIndex - (mine & kIndex)) : -1;
     if (__any_sync(0xffffffffu, near)) choice = select_carefully<VPL, QUADS>(a, row, soft, lane);
