@@ -6,8 +6,7 @@
 // Backward, with dw' = f·dw:  ds_i = dw'_i   or   (dw'_i − Σ_j dw'_j s_j / S) / S,  zero elsewhere;
 //     dl_e = s_e (ds_e − Σ s ds)  (softmax)   or   ds_e s_e (1 − s_e)  (sigmoid; 1 − s(l) = s(−l)).
 //
-// A score next to the border of the k-th is settled in FP64: FP32 scores within 1.5e-6 (sigmoid) of a round's best are
-// within their rounding of it, so those candidates (rarely any) are computed again, and the selection is that of the exact scores
+// The selection is that of the exact scores: choices that FP32 does not tell apart are compared in FP64, so it does not depend on
 // whatever exp's last bits are. Logits that are NaN or -inf, and biases of -inf, are never selected; a token
 // with fewer than k others gets the index -1 and the weight 0 in the places left.
 //
@@ -15,7 +14,10 @@
 // for the index, so that one number tells both: a lane sorts its own, and a round is one warp-wide maximum of the lanes' first
 // and a step of the lane that had it (four times fewer instructions than keys and indexes by themselves). It goes one round
 // further than k, so that wherever the cut bits (or a bias's rounding) could matter two neighbours of the sorted k + 1 are near each
-// other; only then (1 to 3% of the tokens) the rounds are made again with whole keys. The weights are computed from the selected
+// other. Then (1 to 3% of the tokens) the rounds go on until the last one is near no other, the lanes form their choices' whole keys and
+// change places; what those do not tell apart is compared exactly. A warp that is late is what the whole call waits for, so this way is
+// short: with the rounds made again from whole keys instead, which only lists longer than a warp get now, 16384x256 took 17.3 us for 13.6,
+// 8192x512 (softmax) 38.6 for 23.3. The weights are computed from the selected
 // logits by one lane each. In the backward pass every logit's gradient but the selected ones' is −s·Σ s ds (or zero), so these
 // are stored as if none were selected, and the k lanes of the selected store theirs behind them.
 //
@@ -32,10 +34,12 @@ namespace dg {
 namespace {
 
 constexpr int kWarps = 4;
-// How near keys may be in FP32 and be told apart: the error of two scores, and the rounding of two sums with a bias, relative to those.
-// A sigmoid by the fast exponential and division is within 4e-7. A softmax's score is within 2.7e-6 of itself (its sum of up to 37 terms
-// one behind the other 2.2e-6), and no score is larger than that of the largest logit, 1 / Σ exp(l - largest).
-constexpr float kNearSigmoid = 1.2e-6f, kNearSoftmax = 6.5e-6f, kNearSum = 2.5e-7f;
+// How near keys may be in FP32 and be told apart. A sigmoid by the fast exponential and division is within 4e-7 of itself, one by expf and
+// a division within 1.8e-7 (3.6e-7 of its value). A softmax's scores have one sum of exponentials (up to ten additions one behind the
+// other, expf's 2.4e-7 and a division: 9e-7 of the score, in both alike, so of their difference), and each an expf and a product (3.1e-7);
+// no score is larger than that of the largest logit, 1 / Σ exp(l - largest). A sum with a bias rounds by 6e-8 of it.
+constexpr float kNearFastSigmoid = 1.2e-6f, kNearSoftmax = 2e-6f, kNearSum = 1.3e-7f;   // of two keys, and of the larger one
+constexpr float kNearOwn = 3.8e-7f, kNearDifference = 1.1e-6f, kNearBiases = 1.3e-7f;   // of two scores' sum, of their and their biases' differences
 
 // Larger floats have larger integers; what is never selected (NaN, -inf) has 0.
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -95,13 +99,14 @@ __device__ __forceinline__ Softmax softmax_of(const float (&l)[VPL], float (&exp
   for (int j = 0; j < VPL; ++j) best = fmaxf(best, l[j]);   // (a NaN is passed over)
   Softmax s;
   s.top = unordered(__reduce_max_sync(0xffffffffu, ordered(best)));
-  float sum = 0.0f;
+  float part[VPL];
 #pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    exps[j] = l[j] > -INFINITY ? expf(l[j] - s.top) : 0.0f;
-    sum += exps[j];
-  }
-  sum = warp_sum(sum);
+  for (int j = 0; j < VPL; ++j) part[j] = exps[j] = l[j] > -INFINITY ? expf(l[j] - s.top) : 0.0f;
+#pragma unroll
+  for (int w = VPL / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int j = 0; j < w; ++j) part[j] += part[j + w];
+  const float sum = warp_sum(part[0]);
   s.inverse = sum == 0.0f ? 0.0f : 1.0f / sum;
   return s;
 }
@@ -173,10 +178,21 @@ __device__ __noinline__ int settle(const T* row, const float* bias, int E, uint3
   return winner;
 }
 
-// The selection with whole keys, for tokens with near ones: lane i's choice. Out of line; the logits are read again.
+// The exact score of each lane's choice.
+template <typename T>
+__device__ __noinline__ double exact_score(const T* row, int E, int choice, int lane, bool is_sigmoid, float top) {
+  const double l = choice >= 0 ? (double)to_f32(row[choice]) : 0.0;
+  if (is_sigmoid) return 1.0 / (1.0 + exp(-l));
+  double total = 0.0;
+  for (int e = lane; e < E; e += 32)
+    if (to_f32(row[e]) > -INFINITY) total += exp((double)to_f32(row[e]) - (double)top);
+  return exp(l - (double)top) / warp_sum(total);
+}
+
+// The selection with whole keys, for tokens with more near ones than lanes: lane i's choice. Out of line; the logits are read again.
 template <int VPL, bool QUADS, typename T>
 __device__ __noinline__ int select_carefully(const RouteArgs& a, const T* row, const Softmax& soft, int lane) {
-  const float near = a.sigmoid ? kNearSigmoid : kNearSoftmax * soft.inverse;
+  const float near = a.sigmoid ? kNearFastSigmoid : kNearSoftmax * soft.inverse;
   float l[VPL], exps[VPL] = {};
   load_logits<QUADS>(row, a.E, lane, l);
   if (!a.sigmoid)
@@ -231,7 +247,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
     for (int j = 0; j < VPL; ++j) key[j] = key[j] ? (key[j] & ~kIndex) | (kIndex - expert_of<QUADS>(j, lane)) : 0u;   // (the lower index is the larger number)
     sort_descending(key);
     uint32_t mine = 0, top = 0;   // lane i keeps the i-th
-    for (int i = 0; i < rounds; ++i) {
+    auto round = [&](int i) {
       top = __reduce_max_sync(0xffffffffu, key[0]);
       if (key[0] == top) {
 #pragma unroll
@@ -239,18 +255,70 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
         key[VPL - 1] = 0;
       }
       if (lane == i) mine = top;
+    };
+    for (int i = 0; i < rounds; ++i) round(i);
+    // Whether one and the one behind it could change places: the same but for the cut bits (BF16 logits have none there), or (bias)
+    // within the rounding.
+    auto is_near = [&](uint32_t one, uint32_t behind) {
+      if (behind == 0) return false;
+      if (!a.bias) return sizeof(T) == 4 && (one ^ behind) <= kIndex;
+      const float x = unordered(one & ~kIndex), y = unordered(behind | kIndex), apart = a.sigmoid ? kNearFastSigmoid : kNearSoftmax * soft.inverse;
+      return (one ^ behind) <= kIndex || x - y <= fmaf(kNearSum, fmaxf(fabsf(unordered(one | kIndex)), fabsf(unordered(behind & ~kIndex))), apart);
+    };
+    const uint32_t behind = __shfl_down_sync(0xffffffffu, mine, 1);
+    bool near = is_near(mine, lane < 31 ? behind : rounds == 33 ? top : 0u);   // (the 33rd has no lane)
+    uint32_t nears = __ballot_sync(0xffffffffu, near);
+    auto choice_of = [&]() { return mine ? (int)(kIndex - (mine & kIndex)) : -1; };
+    int choice = choice_of();
+    if (nears) {
+      // The list goes on until its last one is near no other, then whole keys tell the order of two near ones (exact ones where those
+      // are near too).
+      int listed = min(rounds, 32);
+      for (; listed < 32 && listed > 1 && (nears >> (listed - 2) & 1); ++listed) {
+        round(listed);
+        if (lane == listed - 1) near = is_near(mine, top);
+        nears = __ballot_sync(0xffffffffu, near);
+      }
+      choice = choice_of();
+      if (nears >> 31 || (listed == 32 && a.k < 32 && nears >> 30)) {   // a list that does not end
+        choice = select_carefully<VPL, QUADS>(a, row, soft, lane);
+      } else {
+        float score = choice >= 0 ? to_f32(row[choice]) : 0.0f;
+        const float b = a.bias && choice >= 0 ? a.bias[choice] : 0.0f;
+        if (a.bias) score = a.sigmoid ? sigmoid(score) : soft(score);
+        double exact = 0.0;
+        bool exactly = false, unclear = false;
+        auto before = [&](int i, bool ask) {   // whether lane i's choice comes before this lane's
+          const int its = __shfl_sync(0xffffffffu, choice, i);
+          if (exactly) {
+            const double other = __shfl_sync(0xffffffffu, exact, i);
+            return ask && (other > exact || (other == exact && its < choice));
+          }
+          const float other = __shfl_sync(0xffffffffu, score, i), ds = other - score, db = __shfl_sync(0xffffffffu, b, i) - b, d = ds + db;
+          unclear |= ask && a.bias && !(fabsf(d) > kNearOwn * (other + score) + kNearDifference * fabsf(ds) + kNearBiases * fabsf(db));
+          return ask && (d > 0.0f || (!(d < 0.0f) && its < choice));   // (two infinite logits are equal)
+        };
+        int from = lane;
+        for (;;) {
+          if ((nears & (nears << 1)) == 0) {   // only neighbours can change places
+            const uint32_t swaps = __ballot_sync(0xffffffffu, before((lane + 1) & 31, near));
+            from = lane + (int)(swaps >> lane & 1) - (int)((swaps << 1) >> lane & 1);
+          } else {
+            int place = 0;
+            for (int i = 0; i < listed; ++i) {
+              const int its = __shfl_sync(0xffffffffu, choice, i);
+              place += before(i, its >= 0 && choice >= 0 && i != lane);
+            }
+            for (int i = 0; i < listed; ++i)
+              if (__shfl_sync(0xffffffffu, choice >= 0 ? place : -1, i) == lane) from = i;
+          }
+          if (exactly || !__any_sync(0xffffffffu, unclear)) break;
+          exact = exact_score(row, a.E, choice, lane, a.sigmoid, soft.top) + (double)b;
+          exactly = true;
+        }
+        choice = __shfl_sync(0xffffffffu, choice, from);
+      }
     }
-    // Whether a choice and the one behind it could change places: the same but for the cut bits, or (bias) within the rounding.
-    uint32_t behind = __shfl_down_sync(0xffffffffu, mine, 1);
-    if (lane == 31) behind = rounds == 33 ? top : 0u;   // (the 33rd has no lane)
-    bool near = behind != 0 && (mine ^ behind) <= kIndex;
-    if (a.bias && behind != 0) {
-      const float x = unordered(mine & ~kIndex), y = unordered(behind | kIndex);
-      const float apart = a.sigmoid ? kNearSigmoid : kNearSoftmax * soft.inverse;
-      near |= x - y <= fmaf(kNearSum, fmaxf(fabsf(unordered(mine | kIndex)), fabsf(unordered(behind & ~kIndex))), apart);
-    }
-    int choice = lane < a.k && mine ? (int)(kIndex - (mine & kIndex)) : -1;
-    if (__any_sync(0xffffffffu, near)) choice = select_carefully<VPL, QUADS>(a, row, soft, lane);
     if (lane >= a.k) choice = -1;
     float weight = 0.0f;
     if (choice >= 0) {

@@ -96,6 +96,41 @@ def test_masked_logits(dg, score, bias):
     _check(dg, l, 6, b if bias else None, score, True, 2.0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(12, 12), (13, 12), (40, 31), (40, 32), (32, 32), (33, 32), (256, 8), (300, 32)])
+def test_runs_of_near_scores(dg, score, E, k):
+    """Pairs, threes and longer runs of logits that share the upper bits of their keys, inside the selection, across its border and
+    beyond 32 of them; the same with biases that bring scores of different logits together."""
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    T = 48
+    l = torch.randn(T, E, generator=g, device="cuda")
+    for t in range(T):
+        run = (1, 2, 2, 3, 4, 7, 40)[t % 7]
+        order = torch.argsort(l[t], descending=True)
+        for at in range(t % 5, E - run + 1, run + 1):         # runs one step or none apart, in no order of the indexes
+            steps = torch.randint(-1, 2, (run,), generator=g, device="cuda") if t % 2 else torch.arange(run, device="cuda")
+            l[t, order[at:at + run]] = l[t, order[at]] * (1 + steps * 2.0 ** -23)
+    _check(dg, l, k, None, score, True, 1.0)
+    _check(dg, l, k, torch.zeros(E, device="cuda"), score, True, 1.0)
+    b = torch.randn(E, generator=g, device="cuda")
+    s = R.scores(l[:1], score)[0]
+    b = (b[E // 2] + s[E // 2] - s).float()                   # the first token's sums: equal to within a rounding
+    _check(dg, l, k, b, score, True, 1.0)
+
+
+def test_infinite_logits_are_equal(dg):
+    l = torch.randn(5, 64, device="cuda")
+    l[0, [50, 3, 17]] = torch.inf
+    l[1, [7, 8]] = torch.inf
+    l[2] = torch.inf
+    for k in (2, 8):
+        for bias in (None, torch.zeros(64, device="cuda")):
+            _check(dg, l, k, bias, "sigmoid", False, 1.0)
+    b = torch.zeros(64, device="cuda")
+    b[[60, 2, 31]] = torch.inf
+    _check(dg, l, 8, b, "sigmoid", False, 1.0)
+
+
 @pytest.mark.parametrize("dt", [F32, BF])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_zeros_of_both_signs_tie(dg, score, dt):
