@@ -41,10 +41,10 @@ constexpr int kWarps = 4;
 constexpr float kNearFastSigmoid = 1.2e-6f, kNearSoftmax = 2e-6f, kNearSum = 1.3e-7f;   // of two keys, and of the larger one
 constexpr float kNearOwn = 3.8e-7f, kNearDifference = 1.1e-6f, kNearBiases = 1.3e-7f;   // of two scores' sum, of their and their biases' differences
 
-// Larger floats have larger integers; what is never selected (NaN, -inf) has 0.
-__device__ __forceinline__ uint32_t ordered(float x) {
+// Larger floats have larger integers, from 2^23 on; what is never selected (NaN, -inf, not `some`) has 0.
+__device__ __forceinline__ uint32_t ordered(float x, bool some = true) {
   const uint32_t b = __float_as_uint(x);
-  return x > -INFINITY ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
+  return some && x > -INFINITY ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
@@ -130,8 +130,7 @@ __device__ __forceinline__ void keys_of(const RouteArgs& a, const Softmax& soft,
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-l[j])));
     else
       s = exps[j] * soft.inverse;
-    const uint32_t k = ordered(s + b[j]);
-    key[j] = l[j] > -INFINITY ? k : 0u;
+    key[j] = ordered(s + b[j], l[j] > -INFINITY);
   }
 }
 
@@ -244,7 +243,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
     uint32_t key[VPL];
     keys_of<QUADS>(a, soft, l, exps, lane, key);
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) key[j] = key[j] ? (key[j] & ~kIndex) | (kIndex - expert_of<QUADS>(j, lane)) : 0u;   // (the lower index is the larger number)
+    for (int j = 0; j < VPL; ++j) key[j] = (key[j] & ~kIndex) | (kIndex - expert_of<QUADS>(j, lane));   // (the lower index is the larger number; of none, up to kIndex)
     sort_descending(key);
     uint32_t mine = 0, top = 0;   // lane i keeps the i-th
     auto round = [&](int i) {
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
     // Whether one and the one behind it could change places: the same but for the cut bits (BF16 logits have none there), or (bias)
     // within the rounding.
     auto is_near = [&](uint32_t one, uint32_t behind) {
-      if (behind == 0) return false;
+      if (behind <= kIndex) return false;   // none
       if (!a.bias) return sizeof(T) == 4 && (one ^ behind) <= kIndex;
       const float x = unordered(one & ~kIndex), y = unordered(behind | kIndex), apart = a.sigmoid ? kNearFastSigmoid : kNearSoftmax * soft.inverse;
       return (one ^ behind) <= kIndex || x - y <= fmaf(kNearSum, fmaxf(fabsf(unordered(one | kIndex)), fabsf(unordered(behind & ~kIndex))), apart);
@@ -268,7 +267,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
     const uint32_t behind = __shfl_down_sync(0xffffffffu, mine, 1);
     bool near = is_near(mine, lane < 31 ? behind : rounds == 33 ? top : 0u);   // (the 33rd has no lane)
     uint32_t nears = __ballot_sync(0xffffffffu, near);
-    auto choice_of = [&]() { return mine ? (int)(kIndex - (mine & kIndex)) : -1; };
+    auto choice_of = [&]() { return mine > kIndex ? (int)(kIndex - (mine & kIndex)) : -1; };
     int choice = choice_of();
     if (nears) {
       // The list goes on until its last one is near no other, then whole keys tell the order of two near ones (exact ones where those
