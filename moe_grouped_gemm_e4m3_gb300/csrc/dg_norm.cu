@@ -15,12 +15,14 @@
 // dB is gate·dgate/N: three sums of one reduction give every scalar of a row.
 //
 // Bound by HBM, with the issue slots half busy (us; floor at the measured copy rate): 8192x7168 BF16 with both norms, gate and scale 83
-// (69), its backward pass 135 (104); 4099x2112 FP32 with E4M3 rows 16 (11.5); one row of 7168 4. The columns' sums (dW, dscale, dw_after) are kept in FP32 registers over the rows of a CTA, one
+// (69), without the norm after, gate and scale 70 (69), the first one's backward pass 135 (104); 4099x2112 FP32 with E4M3 rows 16 (11.5);
+// one row of 7168 4. The columns' sums (dW, dscale, dw_after) are kept in FP32 registers over the rows of a CTA, one
 // partial row a CTA goes to the workspace, and a second kernel adds them in order (no atomics: the same bits every time).
 // Row m belongs to partial m % parts, and parts is a function of the sizes alone, not of dg_set_num_sms.
 //
-// Tried and not kept: the forward pass over three rows at once (one barrier a row, R formed again for Y) 83 to 90 us; one vector a thread
-// and twice the threads for rows of 7168, backward 164 to 220 (64 registers a thread, spilled).
+// Tried and not kept: the forward pass over three rows at once (one barrier a row, R formed again for Y) 83 to 90 us; in teams of 32 warps
+// an SM with the columns' vectors in shared memory, 115; rings of four to six rows, 85 to 86; one vector a thread and twice the threads
+// for rows of 7168, backward 164 to 220 (64 registers a thread, spilled).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
