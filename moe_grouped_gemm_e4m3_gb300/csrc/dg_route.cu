@@ -17,11 +17,11 @@
 // other. Then (1 to 3% of the tokens) the rounds go on until the last one is near no other, the lanes form their choices' whole keys and
 // change places; what those do not tell apart is compared exactly. A warp that is late is what the whole call waits for, so this way is
 // short: with the rounds made again from whole keys instead, which only lists longer than a warp get now, 16384x256 took 17.3 us for 13.6,
-// 8192x512 (softmax) 38.6 for 23.3. The weights are computed from the selected
-// logits by one lane each. In the backward pass every logit's gradient but the selected ones' is −s·Σ s ds (or zero), so these
-// are stored as if none were selected, and the k lanes of the selected store theirs behind them.
+// 8192x512 (softmax) 38.6 for 23.3 (six sets of inputs in turn). The weights are computed from the selected logits by one lane each. In the
+// backward pass every logit's gradient but the selected ones' is −s·Σ s ds (or zero), so these are stored as if none were selected, and
+// the k lanes of the selected store theirs behind them.
 //
-// Bound by its instructions (690 a token of 256 experts with a bias, 537 without): 16384x256 sigmoid scores with a bias 16.5 us,
+// Bound by its instructions (667 a token of 256 experts with a bias, 537 without): 16384x256 sigmoid scores with a bias 12.5 us,
 // where the read takes 2.6; backward of 16381x160 softmax scores 7 to 9 us (3.2).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
