@@ -246,10 +246,12 @@ __device__ __forceinline__ void e8m0_x4(uint32_t w, float (&v)[4]) {
   }
 }
 
-template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
+// WHOLE: E2M1 weights whose rows are whole units, with scales that start on eight bytes in every row.
+template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32, bool WHOLE>
 __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const int stages) {
   extern __shared__ __align__(16) uint8_t ring_of_all[];
   constexpr bool kRouted = KIND != kStreamDense, kFour = FORM == kMxfp4;
+  constexpr bool kCarries = KIND == kStreamDown;   // sums go from one expert to the next
   constexpr int kUnitK = kFour ? 256 : 128, kRows = 16 * R, kStage = stage_bytes(R);
   constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row, unless they start on eight bytes
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, W = blockDim.x / 32, g = lane / 4, t4 = lane % 4;
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
   };
   const int word_steps = FORM == kFp8Packed ? (groups_k + 3) / 4 : groups_k;   // E4M3 weights' scales along K
   const uint8_t* const scales_end = static_cast<const uint8_t*>(a.sw) + (size_t)(kRouted ? a.E : 1) * a.rows * row_scales;
-  const bool eights = kFour && row_scales % 8 == 0 && reinterpret_cast<uintptr_t>(a.sw) % 8 == 0;   // E2M1: a unit's scales of a row in one piece
+  constexpr bool eights = WHOLE;   // a unit's scales of a row in one piece
   // where this lane copies to in a stage: chunk lane % 8 of rows lane / 8 + 4j
   const int copy_row = lane / 8, copy_byte = (lane % 8) * 16;
   const uint32_t to_even = copy_row * kUnitBytes + ((lane % 8) ^ copy_row) * 16, to_odd = (copy_row + 4) * kUnitBytes + ((lane % 8) ^ (copy_row + 4)) * 16;
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
       if (p.item_left(active, blocks)) {
         const uint32_t to = ring + p_stage * kStage;
         // rows copy_row + 4j, which kStreamUp takes from the gate half, the up half, and so on; zeros behind the end of K
-        const int bytes = p.u * kUnitBytes + copy_byte < row_bytes ? 16 : 0;
+        const int bytes = WHOLE || p.u * kUnitBytes + copy_byte < row_bytes ? 16 : 0;
         auto copy = [&](int j, int bytes) {
           const size_t more = KIND == kStreamUp ? (j >> 2) * eight_rows + (j & 1) * four_rows + (j & 2 ? half_rows : 0) : j * four_rows;
           copy_16(to + (j >> 1) * 8 * kUnitBytes + (j & 1 ? to_odd : to_even), p_from + more, bytes);
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
         }
         if constexpr (kFour) {
           // eight scale bytes of each row: in one piece, or from any place the three aligned words that hold them, as far as there are any
-          if (eights) {
+          if constexpr (eights) {
             if (lane < kRows && p_scales[0] != scales_end) {   // (kRows is at most 32)
               copy_8(to + kRows * kUnitBytes + lane * 16, p_scales[0]);
               p_scales[0] += 8 * W;
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
     if (p.item_left(active, blocks)) copy_enter();
 
     // ---- the tokens' operands. Columns without a token, or whose token does not use the expert, read some row there is: their
-    // sums are dropped (`on`). Chunks behind the end of K, whose weights are zeros, read the row's last one.
+    // sums are dropped (`on`, or at the end of the item). Chunks behind the end of K, whose weights are zeros, read the row's last one.
     const uint8_t* x_of[NT];     // this lane's bytes of its tokens' rows
     uint32_t on = 0;             // bit 2i + c: token i·8 + 2·t4 + c has the expert
     const float* s_of[NT][2];    // those tokens' scales, and (kStreamDown) weights
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
       for (int i = 0; i < NT; ++i) {
         if constexpr (kFour) {   // word t4 of each chunk of 32: eight consecutive values
           const uint8_t* x = x_of[i] + c.u * 256 + t4 * 8;
-          if (c.u * 256 + 256 <= a.K) {
+          if (WHOLE || c.u * 256 + 256 <= a.K) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + j * 32));
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
         }
 #pragma unroll
         for (int b = 0; b < (kFour ? 2 : 1); ++b) {
-          const int kb = kFour ? min(2 * c.u + b, groups_k - 1) : c.u;
+          const int kb = kFour ? WHOLE ? 2 * c.u + b : min(2 * c.u + b, groups_k - 1) : c.u;
           float s[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
       float2 acc[R][NT][2] = {};
       uint32_t shift[kFour ? R : 1][2];   // E2M1: where the scale bytes of this lane's rows start in their words
       auto shifts = [&]() {
-        if constexpr (kFour) {
+        if constexpr (kFour && !WHOLE) {
           const size_t first_row = (size_t)(kRouted ? route.active[c.at] : 0) * a.rows;
 #pragma unroll
           for (int r = 0; r < R; ++r)
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
             const uint8_t* rows = unit + (r * 16 + g) * kUnitBytes + t4 * 4;
             const uint8_t* sc = unit + kRows * kUnitBytes + (r * 16 + g) * 16;
             uint2 c0 = *reinterpret_cast<const uint2*>(sc), c1 = *reinterpret_cast<const uint2*>(sc + 128);   // of rows g and g + 8
-            if (!eights) {
+            if constexpr (!eights) {
               const uint32_t b0 = reinterpret_cast<const uint32_t*>(sc)[2], b1 = reinterpret_cast<const uint32_t*>(sc + 128)[2];
               c0 = make_uint2(__funnelshift_r(c0.x, c0.y, shift[r][0]), __funnelshift_r(c0.y, b0, shift[r][0]));
               c1 = make_uint2(__funnelshift_r(c1.x, c1.y, shift[r][1]), __funnelshift_r(c1.y, b1, shift[r][1]));
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
             for (int b = 0; b < 2; ++b) {
               float s0[4], s1[4];
               uint32_t e0 = b ? c0.y : c0.x, e1 = b ? c1.y : c1.x;
-              if (!eights) {   // groups behind the end of K have bytes of another row: none, so that no NaN meets the zeros there
+              if constexpr (!eights) {   // groups behind the end of K have bytes of another row: none, so that no NaN meets the zeros there
                 const int left = a.K / 32 - u * 8 - b * 4;
                 const uint32_t there = left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1;
                 e0 &= there, e1 &= there;
@@ -513,8 +515,8 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
               for (int i = 0; i < NT; ++i)   // (the bits: 0·NaN of another token's expert)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  if (on >> (2 * i) & 1) acc[r][i][h].x = fmaf(part[i][h].x, o.s[i][b].x, acc[r][i][h].x);
-                  if (on >> (2 * i + 1) & 1) acc[r][i][h].y = fmaf(part[i][h].y, o.s[i][b].y, acc[r][i][h].y);
+                  if (!kCarries || (on >> (2 * i) & 1)) acc[r][i][h].x = fmaf(part[i][h].x, o.s[i][b].x, acc[r][i][h].x);
+                  if (!kCarries || (on >> (2 * i + 1) & 1)) acc[r][i][h].y = fmaf(part[i][h].y, o.s[i][b].y, acc[r][i][h].y);
                 }
             }
           }
@@ -544,11 +546,11 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
             const float2 f0 = __fmul2_rn(o.s[i][0], make_float2(s0, s0)), f1 = __fmul2_rn(o.s[i][0], make_float2(s1, s1));
 #pragma unroll
             for (int r = 0; r < R; ++r) {   // (the bits: see above)
-              if (on >> (2 * i) & 1) {
+              if (!kCarries || (on >> (2 * i) & 1)) {
                 acc[r][i][0].x = fmaf(part[r][i][0].x, f0.x, acc[r][i][0].x);
                 acc[r][i][1].x = fmaf(part[r][i][1].x, f1.x, acc[r][i][1].x);
               }
-              if (on >> (2 * i + 1) & 1) {
+              if (!kCarries || (on >> (2 * i + 1) & 1)) {
                 acc[r][i][0].y = fmaf(part[r][i][0].y, f0.y, acc[r][i][0].y);
                 acc[r][i][1].y = fmaf(part[r][i][1].y, f1.y, acc[r][i][1].y);
               }
@@ -661,9 +663,9 @@ FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, cons
     }
 }
 
-template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
-cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
-  auto kernel = stream_kernel<KIND, FORM, NT, R, OUT_F32>;
+template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32, bool WHOLE>
+cudaError_t launch_stream_kernel(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
+  auto kernel = stream_kernel<KIND, FORM, NT, R, OUT_F32, WHOLE>;
   const int items = (rows + 16 * R - 1) / (16 * R);
   static bool configured[64] = {};
   int dev = 0;
@@ -676,6 +678,13 @@ cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, co
   }
   const long long most = (long long)s.limit.sms * plan.ctas;
   return launch_plain(kernel, (int)(items < most ? items : most), plan.warps * 32, plan.smem, s, a, plan.stages);
+}
+
+template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
+cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
+  if constexpr (FORM == kMxfp4)
+    if (a.K % 256 == 0 && reinterpret_cast<uintptr_t>(a.sw) % 8 == 0) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
+  return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, false>(a, rows, plan, s);
 }
 
 // rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
