@@ -505,18 +505,20 @@ __global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const i
                   float2 m[2];
                   mma_16x8x16_zero(m, a0, e4m3_lo(x0), e4m3_hi(x0));
                   mma_16x8x16(m, a1, e4m3_lo(x1), e4m3_hi(x1));
-                  part[i][0].x = j ? fmaf(m[0].x, s0[j], part[i][0].x) : m[0].x * s0[j];
-                  part[i][0].y = j ? fmaf(m[0].y, s0[j], part[i][0].y) : m[0].y * s0[j];
-                  part[i][1].x = j ? fmaf(m[1].x, s1[j], part[i][1].x) : m[1].x * s1[j];
-                  part[i][1].y = j ? fmaf(m[1].y, s1[j], part[i][1].y) : m[1].y * s1[j];
+                  part[i][0] = j ? __ffma2_rn(m[0], make_float2(s0[j], s0[j]), part[i][0]) : __fmul2_rn(m[0], make_float2(s0[j], s0[j]));
+                  part[i][1] = j ? __ffma2_rn(m[1], make_float2(s1[j], s1[j]), part[i][1]) : __fmul2_rn(m[1], make_float2(s1[j], s1[j]));
                 }
               }
 #pragma unroll
               for (int i = 0; i < NT; ++i)   // (the bits: 0·NaN of another token's expert)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  if (!kCarries || (on >> (2 * i) & 1)) acc[r][i][h].x = fmaf(part[i][h].x, o.s[i][b].x, acc[r][i][h].x);
-                  if (!kCarries || (on >> (2 * i + 1) & 1)) acc[r][i][h].y = fmaf(part[i][h].y, o.s[i][b].y, acc[r][i][h].y);
+                  if constexpr (!kCarries) {
+                    acc[r][i][h] = __ffma2_rn(part[i][h], o.s[i][b], acc[r][i][h]);
+                  } else {
+                    if (on >> (2 * i) & 1) acc[r][i][h].x = fmaf(part[i][h].x, o.s[i][b].x, acc[r][i][h].x);
+                    if (on >> (2 * i + 1) & 1) acc[r][i][h].y = fmaf(part[i][h].y, o.s[i][b].y, acc[r][i][h].y);
+                  }
                 }
             }
           }
