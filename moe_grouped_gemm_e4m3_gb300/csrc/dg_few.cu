@@ -248,7 +248,7 @@ __device__ __forceinline__ void e8m0_x4(uint32_t w, float (&v)[4]) {
 
 // WHOLE: E2M1 weights whose rows are whole units, with scales that start on eight bytes in every row.
 template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32, bool WHOLE>
-__global__ void __launch_bounds__(512, 1) stream_kernel(const FewArgs a, const int stages) {
+__global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const FewArgs a, const int stages) {
   extern __shared__ __align__(16) uint8_t ring_of_all[];
   constexpr bool kRouted = KIND != kStreamDense, kFour = FORM == kMxfp4;
   constexpr bool kCarries = KIND == kStreamDown;   // sums go from one expert to the next
@@ -682,24 +682,27 @@ cudaError_t launch_stream_kernel(const FewArgs& a, int rows, const FewPlan& plan
   return launch_plain(kernel, (int)(items < most ? items : most), plan.warps * 32, plan.smem, s, a, plan.stages);
 }
 
+bool whole_units(const FewArgs& a) { return a.K % 256 == 0 && reinterpret_cast<uintptr_t>(a.sw) % 8 == 0; }
+
 template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
 cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
   if constexpr (FORM == kMxfp4)
-    if (a.K % 256 == 0 && reinterpret_cast<uintptr_t>(a.sw) % 8 == 0) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
+    if (whole_units(a)) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
   return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, false>(a, rows, plan, s);
 }
 
 // rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
 // Units of two tiles (32 rows) share the tokens' operands and the steps between them and cost about 1.5 of one tile (us, two and one:
-// 16 tokens through 64 experts 328 and 400, one token through 8 63.4 and 66.1). E2M1 weights, where conversions are most of the work, gain
-// nothing (1x7168x16384 20.5 and 18.3), and four column tiles leave no registers for them.
+// 16 tokens through 64 experts 328 and 400, one token through 8 63.4 and 66.1, 32 tokens through 32 of 4096x2048 199 and 249; four-bit
+// weights, 2 tokens through 32 experts of 7168x2048 68 and 80, 16 tokens 223 and 253). Not E2M1 weights whose rows are no whole units (5
+// tokens through 16 experts of 2080x1408 25.5 and 24.3) or with four column tiles, which leave no registers for them (404 and 311).
 template <Kind KIND, WeightForm FORM, int NT, bool OUT_F32>
 cudaError_t launch_stream_tokens(const FewArgs& a, int rows, int units, const StreamArgs& s) {
   const size_t routing = Routing::bytes(a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
   const FewPlan one = few_plan((rows + 15) / 16, units, NT, 1, routing, s.limit);
-  if constexpr (NT <= 2 && FORM != kMxfp4) {
+  if constexpr (NT <= 2 || FORM != kMxfp4) {
     const FewPlan two = few_plan((rows + 31) / 32, units, NT, 2, routing, s.limit);
-    if (1.5 * two.cost <= 1.1 * one.cost) return launch_stream_nt<KIND, FORM, NT, 2, OUT_F32>(a, rows, two, s);
+    if (1.5 * two.cost <= 1.1 * one.cost && (FORM != kMxfp4 || whole_units(a))) return launch_stream_nt<KIND, FORM, NT, 2, OUT_F32>(a, rows, two, s);
   }
   return launch_stream_nt<KIND, FORM, NT, 1, OUT_F32>(a, rows, one, s);
 }
