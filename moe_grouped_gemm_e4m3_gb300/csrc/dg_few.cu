@@ -18,16 +18,14 @@
 // converting them costs one instruction for two (mma.sync on E4M3 itself takes twice as long here: 13.8 ns a k32 against
 // 2 x 4.2 in FP16). The order of k inside a scale's group is free as long as both operands use the same one, so a lane's
 // operands are consecutive bytes. A group's partial sum meets its scales in FP32: E4M3 weights every 128 values, E2M1 every 32.
-// A token keeps its column whatever the expert, so kStreamDown adds up a token's experts in the accumulators; the sums of columns
-// that an expert does not serve are dropped.
 //
-// Measured (us; floor: the weights read once at the measured copy rate): one token through 8 of 32 experts of 7168x2048, E4M3, 61
-// (52); 16 tokens through 64 such, packed scales, 325 (at most 367: uneven choices read fewer experts); 4 tokens 153. Four bits:
-// 1x7168x16384 17.7 (9.2), 16x24576x1536 15 (3.1), 2 tokens through 32 experts of 7168x2048 92 (48). With E4M3 the read bounds it (5.8 to 7
-// TB/s); with E2M1, at twice the values a byte, instructions do: 381 a unit of 16x256 in 700 cycles of a scheduler, 64 of them
-// conversions of weights and 32 of tokens, the ALU pipe half busy. Neither more warps (24 for 16) nor the tokens' operands staged as
-// FP16 in shared memory took more than 4% off. Batches of items whose units the warps share as ranges (fewer turns, one joining
-// of sums a batch) take longer, 66 us for 60 and 17 for 15: the warps' pieces of a row lie apart then, and the joining is not hidden.
+// Measured (us; floor: the weights read once at the measured copy rate): one token through 8 of 32 experts of 7168x2048, E4M3, 60
+// (52); 16 tokens through 64 such, packed scales, 320 (at most 367: uneven choices read fewer experts); 4 tokens 151; 32 tokens 678. Four
+// bits: 1x7168x16384 16.2 (9.2), 16x24576x1536 12.9 (3.1), through 32 experts of 7168x2048 2 tokens 68 (48) and 16 tokens 213 (110). With
+// E4M3 the read bounds it (5.8 to 7 TB/s); with E2M1, at twice the values a byte, instructions do: of 330 to 380 a unit of 16x256, 64 are
+// conversions of weights and 32 of tokens, with two cycles of the ALU pipe each. Not kept: more warps (24 for 16) and the tokens' operands
+// staged as FP16 in shared memory, at most 4% off; batches of items whose units the warps share as ranges (fewer turns, one joining of
+// sums a batch), 66 us for 60 and 17 for 15: the warps' pieces of a row lie apart then, and the joining is not hidden.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -99,9 +97,10 @@ struct Routing {
   uint16_t* active;    // [E] the active experts, ascending
   uint16_t* first;     // [E] of each active expert: its first pair
   uint16_t* row;       // of a pair: the choice t·k + j (within the pass) whose h row it uses
+  uint16_t* token;     // of a pair
   int* count;          // of active experts
   static constexpr uint16_t kNone = 0xFFFF;
-  __host__ __device__ static size_t bytes(int E, int pairs) { return (size_t)E * 8 + (size_t)pairs * 12 + 16; }
+  __host__ __device__ static size_t bytes(int E, int pairs) { return ((size_t)E * 8 + (size_t)pairs * 14 + 31) / 16 * 16; }
   __device__ Routing(uint8_t* at, int E, int pairs) {
     mask = reinterpret_cast<uint32_t*>(at);
     chosen = reinterpret_cast<float*>(mask + E);
@@ -110,6 +109,7 @@ struct Routing {
     active = choice + pairs;
     first = active + E;
     row = first + E;
+    token = row + pairs;
     count = reinterpret_cast<int*>(at + (bytes(E, pairs) - 16));
   }
 };
@@ -173,6 +173,7 @@ __device__ void find_pairs(const Routing& r, const FewArgs& a, bool with_weights
           if (with_weights) w += r.chosen[t * a.k + j];
         }
       r.row[pair] = (uint16_t)(t * a.k + first);
+      r.token[pair] = (uint16_t)t;
       r.weight[pair] = w;
     }
   }
@@ -219,6 +220,7 @@ struct Cursor {
 // The tokens' side of a unit: this lane's bytes of its column's token, and the scales of the two tokens of its accumulators.
 template <int NT, bool FOUR>
 struct Operands {
+  static constexpr int tiles = NT;
   uint32_t x[NT][FOUR ? 16 : 8];
   float2 s[NT][FOUR ? 2 : 1];
 };
@@ -251,7 +253,11 @@ template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32, bool WHOLE>
 __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const FewArgs a, const int stages) {
   extern __shared__ __align__(16) uint8_t ring_of_all[];
   constexpr bool kRouted = KIND != kStreamDense, kFour = FORM == kMxfp4;
-  constexpr bool kCarries = KIND == kStreamDown;   // sums go from one expert to the next
+  // A token keeps its column whatever the expert, and kStreamDown's sums go from one expert to the next in registers (kCarries). Or an
+  // expert has only its own tokens in columns, one after another, so that mostly one tile of columns is computed (kCompact), and kStreamDown
+  // adds an expert's sums to its tokens' in shared memory: where the columns' work counts, with four tiles of them or E2M1 weights (32
+  // tokens, us: 8 of 64 experts 678 and 776, four bits 4 of 32 222 and 310; 16 tokens, four bits 212 and 223, but E4M3 376 and 326).
+  constexpr bool kCompact = kRouted && (NT > 2 || (NT == 2 && kFour)), kCarries = KIND == kStreamDown && !kCompact;
   constexpr int kUnitK = kFour ? 256 : 128, kRows = 16 * R, kStage = stage_bytes(R);
   constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row, unless they start on eight bytes
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, W = blockDim.x / 32, g = lane / 4, t4 = lane % 4;
@@ -365,37 +371,44 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
     // sums are dropped (`on`, or at the end of the item). Chunks behind the end of K, whose weights are zeros, read the row's last one.
     const uint8_t* x_of[NT];     // this lane's bytes of its tokens' rows
     uint32_t on = 0;             // bit 2i + c: token i·8 + 2·t4 + c has the expert
+    int columns = tokens;        // that the expert has (kCompact)
+    auto tiles = [&]() { return columns <= 8 ? 1 : columns <= 16 ? 2 : 4; };
     const float* s_of[NT][2];    // those tokens' scales, and (kStreamDown) weights
     float weight_of[NT][2];
     auto enter = [&](const Cursor<KIND>& c) {   // at another item or expert
       const uint32_t mask = kRouted ? route.mask[route.active[c.at]] : 0xffffffffu;
-      const int first = KIND == kStreamDown ? route.first[c.at] : 0;
+      const int first = kRouted ? route.first[c.at] : 0;
       on = 0;
+      if constexpr (kCompact) columns = __popc(mask);
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        const int t = i * 8 + g;
-        const bool live = t < tokens && (mask >> t & 1);
-        size_t row = (size_t)(t0 + (live ? t : 0));
-        if constexpr (KIND == kStreamDown) row = (size_t)t0 * a.k + route.row[live ? first + __popc(mask & ((1u << t) - 1)) : first];
+        if (kCompact && i >= tiles()) continue;
+        auto pair_of = [&](int column) {   // (kRouted; some pair there is where the column has none)
+          if constexpr (kCompact) return first + min(column, columns - 1);
+          return column < tokens && (mask >> column & 1) ? first + __popc(mask & ((1u << column) - 1)) : first;
+        };
+        auto token_of = [&](int column) {
+          if constexpr (kCompact) return (int)route.token[pair_of(column)];
+          return column < tokens && (mask >> column & 1) ? column : 0;
+        };
+        const size_t row = KIND == kStreamDown ? (size_t)t0 * a.k + route.row[pair_of(i * 8 + g)] : (size_t)(t0 + token_of(i * 8 + g));
         x_of[i] = a.x + row * a.K;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int tc = i * 8 + 2 * t4 + h;
-          const bool there = tc < tokens && (mask >> tc & 1);
-          if (there) on |= 1u << (2 * i + h);
+          if (kCarries && tc < tokens && (mask >> tc & 1)) on |= 1u << (2 * i + h);
           if constexpr (KIND == kStreamDown) {
-            const int pair = there ? first + __popc(mask & ((1u << tc) - 1)) : first;
-            s_of[i][h] = static_cast<const float*>(a.sx) + ((size_t)t0 * a.k + route.row[pair]) * groups_k;
-            weight_of[i][h] = route.weight[pair];
+            s_of[i][h] = static_cast<const float*>(a.sx) + ((size_t)t0 * a.k + route.row[pair_of(tc)]) * groups_k;
+            weight_of[i][h] = route.weight[pair_of(tc)];
           } else {
-            s_of[i][h] = static_cast<const float*>(a.sx) + t0 + (there ? tc : 0);
+            s_of[i][h] = static_cast<const float*>(a.sx) + t0 + token_of(tc);
           }
         }
       }
     };
-    auto load = [&](const Cursor<KIND>& c, Operands<NT, kFour>& o) {
+    auto load = [&](const Cursor<KIND>& c, auto& o) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int i = 0; i < o.tiles; ++i) {
         if constexpr (kFour) {   // word t4 of each chunk of 32: eight consecutive values
           const uint8_t* x = x_of[i] + c.u * 256 + t4 * 8;
           if (WHOLE || c.u * 256 + 256 <= a.K) {
@@ -457,11 +470,16 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
             for (int h = 0; h < 2; ++h) shift[r][h] = 8 * ((uint32_t)((first_row + row_of(c.block, r * 16 + h * 8 + g)) * row_scales) & 3);
         }
       };
-      if (c.in_item(units_k, active)) shifts(), enter(c);
-      while (c.in_item(units_k, active)) {
-        Operands<NT, kFour> o;
+      float* const mine = sums + ((size_t)buffer * W + warp) * R * NT * 128;   // this warp's sums of the item
+      if constexpr (kCompact && KIND == kStreamDown) {
+        for (int i = lane; i < R * NT * 128; i += 32) mine[i] = 0.0f;
+        __syncwarp();
+      }
+      auto unit_of = [&](auto some) {   // the unit at c, by so many tiles of columns
+        constexpr int TILES = decltype(some)::value;
+        Operands<TILES, kFour> o;
         load(c, o);    // (from L1 or L2: behind the copies' addresses and the wait)
-        issue();
+        if constexpr (!kCompact) issue();
         if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
         else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
         else asm volatile("cp.async.wait_group 1;" ::: "memory");   // (two stages)
@@ -491,7 +509,7 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
               }
               e8m0_x4(e0, s0);
               e8m0_x4(e1, s1);
-              float2 part[NT][2];
+              float2 part[TILES][2];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int chunk = b * 4 + j;
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
                 e2m1_x8(*reinterpret_cast<const uint32_t*>(rows + 8 * kUnitBytes + ((chunk ^ g) * 16)), hi);
                 const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
+                for (int i = 0; i < TILES; ++i) {
                   const uint32_t x0 = o.x[i][2 * chunk], x1 = o.x[i][2 * chunk + 1];
                   float2 m[2];
                   mma_16x8x16_zero(m, a0, e4m3_lo(x0), e4m3_hi(x0));
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
                 }
               }
 #pragma unroll
-              for (int i = 0; i < NT; ++i)   // (the bits: 0·NaN of another token's expert)
+              for (int i = 0; i < TILES; ++i)   // (the bits: 0·NaN of another token's expert)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   if constexpr (!kCarries) {
@@ -528,7 +546,7 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
           const uint32_t c0 = sc[0], c1 = KIND == kStreamUp ? sc[1] : c0;
           const float s0 = FORM == kFp8Packed ? ue8m0_value(c0 >> (8 * (u & 3))) : __uint_as_float(c0);
           const float s1 = FORM == kFp8Packed ? ue8m0_value(c1 >> (8 * (u & 3))) : __uint_as_float(c1);
-          float2 part[R][NT][2] = {};
+          float2 part[R][TILES][2] = {};
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -540,11 +558,11 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
               for (int j = 0; j < 4; ++j) {
                 const uint32_t f[4] = {e4m3_lo(lo[j]), e4m3_lo(hi[j]), e4m3_hi(lo[j]), e4m3_hi(hi[j])};
 #pragma unroll
-                for (int i = 0; i < NT; ++i) mma_16x8x16(part[r][i], f, e4m3_lo(o.x[i][4 * h + j]), e4m3_hi(o.x[i][4 * h + j]));
+                for (int i = 0; i < TILES; ++i) mma_16x8x16(part[r][i], f, e4m3_lo(o.x[i][4 * h + j]), e4m3_hi(o.x[i][4 * h + j]));
               }
             }
 #pragma unroll
-          for (int i = 0; i < NT; ++i) {
+          for (int i = 0; i < TILES; ++i) {
             const float2 f0 = __fmul2_rn(o.s[i][0], make_float2(s0, s0)), f1 = __fmul2_rn(o.s[i][0], make_float2(s1, s1));
 #pragma unroll
             for (int r = 0; r < R; ++r) {   // (the bits: see above)
@@ -559,33 +577,76 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
             }
           }
         }
-        __syncwarp();   // the stage is free for the copies of the next turn
-        if (++stage == stages) stage = 0;
-        if (c.step(W, units_k, active) && c.in_item(units_k, active)) shifts(), enter(c);
-      }
-
-      // the warps' sums, in warp order (two buffers by turns: one barrier an item)
-      float* const mine = sums + (size_t)buffer * W * R * NT * 128;
-#pragma unroll
-      for (int r = 0; r < R; ++r)
+      };
+      auto flush = [&](int at) {   // (kStreamDown, kCompact) the expert's sums to its tokens'
+        const int first = route.first[at];
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mine[(((warp * R + r) * NT + i) * 4 + q) * 32 + lane] = q & 1 ? acc[r][i][q >> 1].y : acc[r][i][q >> 1].x;
+          for (int h = 0; h < 2; ++h) {
+            const int column = i * 8 + 2 * t4 + h;
+            if (column < columns) {
+              const int t = route.token[first + column];
+              float* const to = mine + ((t >> 3) * 4 + (t & 1)) * 32 + g * 4 + ((t & 7) >> 1);
+#pragma unroll
+              for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) to[(r * NT * 4 + q * 2) * 32] += h ? acc[r][i][q].y : acc[r][i][q].x;
+            }
+          }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[r][i][0] = acc[r][i][1] = make_float2(0.0f, 0.0f);
+        __syncwarp();   // (another lane may have the next expert's column of the token)
+      };
+      if (c.in_item(units_k, active)) shifts(), enter(c);
+      while (c.in_item(units_k, active)) {
+        if constexpr (kCompact) {
+          issue();
+          const int used = tiles();
+          if (used == 1)
+            unit_of(std::integral_constant<int, 1>{});
+          else if (NT == 2 || used == 2)
+            unit_of(std::integral_constant<int, 2>{});
+          else
+            unit_of(std::integral_constant<int, NT>{});
+        } else {
+          unit_of(std::integral_constant<int, NT>{});
+        }
+        __syncwarp();   // the stage is free for the copies of the next turn
+        if (++stage == stages) stage = 0;
+        const int at = c.at;
+        if (c.step(W, units_k, active)) {
+          if constexpr (kCompact && KIND == kStreamDown) flush(at);
+          if (c.in_item(units_k, active)) shifts(), enter(c);
+        }
+      }
+
+      // the warps' sums, in warp order (two buffers by turns: one barrier an item)
+      if constexpr (!(kCompact && KIND == kStreamDown)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mine[((r * NT + i) * 4 + q) * 32 + lane] = q & 1 ? acc[r][i][q >> 1].y : acc[r][i][q >> 1].x;
+      }
       __syncthreads();
-      auto sum = [&](int m, int l) {   // token m, row l
+      const float* const all = sums + (size_t)buffer * W * R * NT * 128;
+      auto sum = [&](int m, int l) {   // column m, row l
         const int q = ((l >> 3) & 1) * 2 + m % 2, from = (((l >> 4) * NT + m / 8) * 4 + q) * 32 + (l % 8) * 4 + (m % 8) / 2;
         float s = 0.0f;
-        for (int w = 0; w < W; ++w) s += mine[w * R * NT * 128 + from];
+        for (int w = 0; w < W; ++w) s += all[w * R * NT * 128 + from];
         return s;
       };
       if constexpr (KIND == kStreamUp) {
         const uint32_t mask = route.mask[route.active[item_at]];
-        for (int o = threadIdx.x; o < 8 * R * tokens; o += blockDim.x) {
+        const int first = route.first[item_at], count = kCompact ? __popc(mask) : tokens;
+        for (int o = threadIdx.x; o < 8 * R * count; o += blockDim.x) {
           const int m = o / (8 * R), j = o % (8 * R);
-          if (!(mask >> m & 1)) continue;
-          const size_t row = (size_t)t0 * a.k + route.row[route.first[item_at] + __popc(mask & ((1u << m) - 1))];
+          if (!kCompact && !(mask >> m & 1)) continue;
+          const size_t row = (size_t)t0 * a.k + route.row[first + (kCompact ? m : __popc(mask & ((1u << m) - 1)))];
           const int l = (j >> 3) * 16 + (j & 7);
           const float gate = sum(m, l), up = sum(m, l + 8);
           static_cast<float*>(a.out)[row * half + item_block * 8 * R + j] = silu_f32(gate) * up;

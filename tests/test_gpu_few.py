@@ -123,6 +123,18 @@ def test_choices(dg, form):
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("T,K,I", [(13, 512, 256), (13, 288, 128), (32, 512, 256), (32, 288, 128)])
+def test_experts_of_any_number_of_tokens(dg, form, T, K, I):
+    """One expert with 1 to T tokens in any order, the rest through others, one token twice through the same."""
+    for count in sorted({1, 2, 7, 8, 9, 15, 16, 17, 24, 25, 31, T} & set(range(1, T + 1))):
+        d = _layer(form, T, 2, 4, K, I, 48, seed=count)
+        order = torch.randperm(T, generator=torch.Generator().manual_seed(count)).cuda()
+        d["ids"][:, 0] = torch.where(order < count, 2, 0)
+        d["ids"][:, 1] = torch.where(order % 3 == 0, -1, torch.where(order % 3 == 1, 3, d["ids"][:, 0]))
+        _check(dg, d)
+
+
+@pytest.mark.parametrize("form", FORMS)
 def test_ids_out_of_range_are_flagged_and_count_as_none(dg, form):
     d = _layer(form, 5, 2, 4, 256, 128, 64)
     d["ids"][1, 0], d["ids"][3, 1] = 4, -2
