@@ -22,8 +22,8 @@
 // Measured (us; floor: the weights read once at the measured copy rate): one token through 8 of 32 experts of 7168x2048, E4M3, 60
 // (52); 16 tokens through 64 such, packed scales, 320 (at most 367: uneven choices read fewer experts); 4 tokens 151; 32 tokens 678. Four
 // bits: 1x7168x16384 16.2 (9.2), 16x24576x1536 12.9 (3.1), through 32 experts of 7168x2048 2 tokens 68 (48) and 16 tokens 213 (110). With
-// E4M3 the read bounds it (5.8 to 7 TB/s); with E2M1, at twice the values a byte, instructions do: of 330 to 380 a unit of 16x256, 64 are
-// conversions of weights and 32 of tokens, with two cycles of the ALU pipe each. Not kept: more warps (24 for 16) and the tokens' operands
+// E4M3 the read bounds it (5.8 to 7 TB/s); with E2M1, at twice the values a byte, instructions do: 438 a unit of 32x256 (one column tile), 128 of
+// them conversions of weights and 32 of tokens, with two cycles of the ALU pipe each. Not kept: more warps (24 for 16) and the tokens' operands
 // staged as FP16 in shared memory, at most 4% off; batches of items whose units the warps share as ranges (fewer turns, one joining of
 // sums a batch), 66 us for 60 and 17 for 15: the warps' pieces of a row lie apart then, and the joining is not hidden.
 #include <cuda_bf16.h>
