@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
         else asm volatile("cp.async.wait_group 1;" ::: "memory");   // (two stages)
         __syncwarp();
         const uint8_t* unit = ring_at + stage * kStage;
-        const int u = c.u;
+        [[maybe_unused]] const int u = c.u;
         if constexpr (kFour) {
           // 8 groups of 32: a lane has word t4 of chunk j of its rows
 #pragma unroll
@@ -747,9 +747,10 @@ bool whole_units(const FewArgs& a) { return a.K % 256 == 0 && reinterpret_cast<u
 
 template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
 cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
+  constexpr bool kWholeAlone = FORM == kMxfp4 && R == 2;   // (see launch_stream_tokens)
   if constexpr (FORM == kMxfp4)
-    if (whole_units(a)) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
-  return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, false>(a, rows, plan, s);
+    if (kWholeAlone || whole_units(a)) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
+  if constexpr (!kWholeAlone) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, false>(a, rows, plan, s);
 }
 
 // rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
