@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
         }
       }
     };
+    // Plain loads: the read-only path is for data that nobody writes while the kernel lives, and a kernel that starts early lives beside
+    // the one that writes its tokens (kStreamDown: beside the cast; the others: beside whatever came before the call).
     auto load = [&](const Cursor<KIND>& c, auto& o) {
 #pragma unroll
       for (int i = 0; i < o.tiles; ++i) {
@@ -414,20 +416,20 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
           if (WHOLE || c.u * 256 + 256 <= a.K) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(x + j * 32));
+              const uint2 v = *reinterpret_cast<const uint2*>(x + j * 32);
               o.x[i][2 * j] = v.x, o.x[i][2 * j + 1] = v.y;
             }
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(x_of[i] + min(c.u * 256 + j * 32, a.K - 32) + t4 * 8));
+              const uint2 v = *reinterpret_cast<const uint2*>(x_of[i] + min(c.u * 256 + j * 32, a.K - 32) + t4 * 8);
               o.x[i][2 * j] = v.x, o.x[i][2 * j + 1] = v.y;
             }
           }
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(x_of[i] + min(c.u * 128 + t4 * 32 + h * 16, a.K - 16)));
+            const uint4 v = *reinterpret_cast<const uint4*>(x_of[i] + min(c.u * 128 + t4 * 32 + h * 16, a.K - 16));
             o.x[i][4 * h] = v.x, o.x[i][4 * h + 1] = v.y, o.x[i][4 * h + 2] = v.z, o.x[i][4 * h + 3] = v.w;
           }
         }
@@ -438,11 +440,11 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if constexpr (KIND == kStreamDown)
-              s[h] = s_of[i][h][kb] * weight_of[i][h];   // (written by the launch before: not through the read-only path)
+              s[h] = s_of[i][h][kb] * weight_of[i][h];
             else if constexpr (FORM == kFp8Packed)
-              s[h] = ue8m0_value(__ldg(reinterpret_cast<const uint32_t*>(s_of[i][h]) + (size_t)(kb >> 2) * ldx) >> (8 * (kb & 3)));
+              s[h] = ue8m0_value(reinterpret_cast<const uint32_t*>(s_of[i][h])[(size_t)(kb >> 2) * ldx] >> (8 * (kb & 3)));
             else
-              s[h] = __ldg(s_of[i][h] + (size_t)kb * ldx);
+              s[h] = s_of[i][h][(size_t)kb * ldx];
           }
           o.s[i][b] = make_float2(s[0], s[1]);
         }
@@ -674,9 +676,9 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
 }
 
 // The cast of h [rows, I] in FP32: E4M3 codes and one FP32 scale per group of 128 (UE: a power of two). A warp a group.
+// (No __restrict__: h is written while this kernel may live already, which a read-only load would not allow.)
 template <bool UE>
-__global__ void __launch_bounds__(256) h_cast_kernel(const float* __restrict__ h, const int32_t* __restrict__ ids, uint8_t* __restrict__ q,
-                                                     float* __restrict__ s, long long groups, int per_row) {
+__global__ void __launch_bounds__(256) h_cast_kernel(const float* h, const int32_t* ids, uint8_t* q, float* s, long long groups, int per_row) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x % 32;

@@ -1,0 +1,23 @@
+"""Kernels that start before the launch ahead of them has ended (griddepcontrol) may not use read-only loads: those are for data
+that nobody writes while the kernel lives, and the launch ahead still writes what such a kernel reads behind its wait."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "moe_grouped_gemm_e4m3_gb300", "csrc")
+FILES = ["dg_few.cu", "dg_norm.cu", "dg_route.cu"]
+
+
+def _code(name):
+    """The source without its comments."""
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", text, flags=re.S)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_no_read_only_loads(name):
+    code = _code(name)
+    assert "griddep_wait()" in code
+    assert re.findall(r"__ldg\w*\(|ld\.global\.nc|ld\.global\.\S*\.nc|__restrict__", code) == []
