@@ -30,6 +30,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "dg_few_plan.h"
 #include "dg_launch.h"
 #include "dg_scale.cuh"
 #include "dg_vec.cuh"
@@ -39,10 +40,6 @@ namespace dg {
 namespace {
 
 enum Kind { kStreamUp, kStreamDown, kStreamDense };
-
-constexpr int kUnitBytes = 128;   // of a unit's rows
-// A stage of the ring holds a unit of R tiles of 16 rows: codes, then scales (E2M1: 16 bytes a row; E4M3: one or two words).
-constexpr int stage_bytes(int R) { return 16 * R * (kUnitBytes + 16); }
 
 struct FewArgs {
   const uint8_t* x;        // E4M3 rows: tokens (kStreamUp, kStreamDense) or the cast h of each (token, choice) (kStreamDown)
@@ -100,7 +97,6 @@ struct Routing {
   uint16_t* token;     // of a pair
   int* count;          // of active experts
   static constexpr uint16_t kNone = 0xFFFF;
-  __host__ __device__ static size_t bytes(int E, int pairs) { return ((size_t)E * 8 + (size_t)pairs * 14 + 31) / 16 * 16; }
   __device__ Routing(uint8_t* at, int E, int pairs) {
     mask = reinterpret_cast<uint32_t*>(at);
     chosen = reinterpret_cast<float*>(mask + E);
@@ -110,7 +106,7 @@ struct Routing {
     first = active + E;
     row = first + E;
     token = row + pairs;
-    count = reinterpret_cast<int*>(at + (bytes(E, pairs) - 16));
+    count = reinterpret_cast<int*>(at + (routing_bytes(E, pairs) - 16));
   }
 };
 
@@ -697,37 +693,6 @@ __global__ void __launch_bounds__(256) h_cast_kernel(const float* h, const int32
   }
 }
 
-constexpr int kFewSms = 152;
-
-// How a launch is laid out: warps a CTA, CTAs an SM, stages of a warp's ring.
-struct FewPlan {
-  int warps, ctas, stages;
-  size_t smem;
-  double cost;
-};
-// Sixteen warps fill an SM, twelve on units of two tiles (whose stages are twice as large; 16 x 2 stages, 14 x 3 and 8 x 4 take 5% longer
-// than 12 x 3 for one token through 8 of 32 experts of 7168x2048, E4M3). Fewer warps do not take their steps faster, so the layout is the
-// one with the least rounds of items x turns of a warp, and 0.3 for the item's own steps (without: 63.4 us for 61 there, 162 for 153 with 4
-// tokens). At least four warps a CTA: 16 tokens through 64 experts take 415 us with two and 325 with four. `items` are those of a
-// whole GPU, whatever dg_set_num_sms says.
-FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, const SmLimit& limit) {
-  const int most = R == 2 ? 12 : 16;
-  FewPlan p{};
-  p.cost = 1e300;
-  for (int w = most; w >= 4; --w)
-    for (int c = 1; c * w <= most; ++c) {
-      const double rounds = (double)((items + (long long)kFewSms * c - 1) / ((long long)kFewSms * c));
-      const double cost = rounds * ((units + w - 1) / w + 0.3) * most;
-      if (cost < p.cost * (1.0 - 1e-9)) p.cost = cost, p.warps = w, p.ctas = c;
-    }
-  if (limit.capped) p.ctas = 1;
-  for (;; --p.ctas)
-    for (p.stages = 4; p.stages >= (p.ctas == 1 ? 2 : 3); --p.stages) {
-      p.smem = (size_t)p.warps * (p.stages * stage_bytes(R) + 2 * R * NT * 128 * sizeof(float)) + routing;
-      if (p.ctas * (p.smem + 1024) <= (size_t)227 << 10) return p;
-    }
-}
-
 template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32, bool WHOLE>
 cudaError_t launch_stream_kernel(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
   auto kernel = stream_kernel<KIND, FORM, NT, R, OUT_F32, WHOLE>;
@@ -749,32 +714,26 @@ bool whole_units(const FewArgs& a) { return a.K % 256 == 0 && reinterpret_cast<u
 
 template <Kind KIND, WeightForm FORM, int NT, int R, bool OUT_F32>
 cudaError_t launch_stream_nt(const FewArgs& a, int rows, const FewPlan& plan, const StreamArgs& s) {
-  constexpr bool kWholeAlone = FORM == kMxfp4 && R == 2;   // (see launch_stream_tokens)
+  constexpr bool kWholeAlone = FORM == kMxfp4 && R == 2;   // (see few_choice)
   if constexpr (FORM == kMxfp4)
     if (kWholeAlone || whole_units(a)) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, true>(a, rows, plan, s);
   if constexpr (!kWholeAlone) return launch_stream_kernel<KIND, FORM, NT, R, OUT_F32, false>(a, rows, plan, s);
 }
 
-// rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
-// Units of two tiles (32 rows) share the tokens' operands and the steps between them and cost about 1.5 of one tile (us, two and one:
-// 16 tokens through 64 experts 328 and 400, one token through 8 63.4 and 66.1, 32 tokens through 32 of 4096x2048 199 and 249; four-bit
-// weights, 2 tokens through 32 experts of 7168x2048 68 and 80, 16 tokens 223 and 253). Not E2M1 weights whose rows are no whole units (5
-// tokens through 16 experts of 2080x1408 25.5 and 24.3) or with four column tiles, which leave no registers for them (404 and 311).
+// (rows, units: see few_choice)
 template <Kind KIND, WeightForm FORM, int NT, bool OUT_F32>
 cudaError_t launch_stream_tokens(const FewArgs& a, int rows, int units, const StreamArgs& s) {
-  const size_t routing = Routing::bytes(a.E, (a.T < 8 * NT ? a.T : 8 * NT) * a.k);
-  const FewPlan one = few_plan((rows + 15) / 16, units, NT, 1, routing, s.limit);
-  if constexpr (NT <= 2 || FORM != kMxfp4) {
-    const FewPlan two = few_plan((rows + 31) / 32, units, NT, 2, routing, s.limit);
-    if (1.5 * two.cost <= 1.1 * one.cost && (FORM != kMxfp4 || whole_units(a))) return launch_stream_nt<KIND, FORM, NT, 2, OUT_F32>(a, rows, two, s);
-  }
-  return launch_stream_nt<KIND, FORM, NT, 1, OUT_F32>(a, rows, one, s);
+  const FewChoice c = few_choice(a.T, a.k, a.E, rows, units, FORM == kMxfp4, whole_units(a), s.limit.capped);
+  if constexpr (few_two_tiles(NT, FORM == kMxfp4))
+    if (c.R == 2) return launch_stream_nt<KIND, FORM, NT, 2, OUT_F32>(a, rows, c.plan, s);
+  return launch_stream_nt<KIND, FORM, NT, 1, OUT_F32>(a, rows, c.plan, s);
 }
 
 template <Kind KIND, WeightForm FORM, bool OUT_F32>
 cudaError_t launch_stream(const FewArgs& a, int rows, int units, const StreamArgs& s) {
-  if (a.T <= 8) return launch_stream_tokens<KIND, FORM, 1, OUT_F32>(a, rows, units, s);
-  if (a.T <= 16) return launch_stream_tokens<KIND, FORM, 2, OUT_F32>(a, rows, units, s);
+  const int tiles = few_tiles(a.T);
+  if (tiles == 1) return launch_stream_tokens<KIND, FORM, 1, OUT_F32>(a, rows, units, s);
+  if (tiles == 2) return launch_stream_tokens<KIND, FORM, 2, OUT_F32>(a, rows, units, s);
   return launch_stream_tokens<KIND, FORM, 4, OUT_F32>(a, rows, units, s);
 }
 
