@@ -38,32 +38,35 @@ inline int few_stages(int warps, int ctas, int NT, int R, size_t routing) {
 // Sixteen warps fill an SM, twelve on units of two tiles (whose stages are twice as large; 16 x 2 stages, 14 x 3 and 8 x 4 take 5% longer
 // than 12 x 3 for one token through 8 of 32 experts of 7168x2048, E4M3). Fewer warps do not take their steps faster, so the layout is the
 // one with the least rounds of items x turns of a warp, and 0.3 for the item's own steps (without: 63.4 us for 61 there, 162 for 153 with 4
-// tokens). At least four warps a CTA: 16 tokens through 64 experts take 415 us with two and 325 with four. Warps that do not fit with two
-// stages (twelve on two tiles with 32 tokens and the tables of 1023 experts and 32 choices) are no layout.
+// tokens), of those that fit: with CTAs taken off afterwards instead, SMs ran on half of their warps with 17 tokens and more (32 tokens
+// through 8 of 64 experts of 7168x2048 677 us for 551, 24 through 8 of 32 424 for 343). At least four warps a CTA: 16 tokens through 64
+// experts take 415 us with two and 325 with four. Of one CTA with two stages some number of warps always fits.
 inline FewPlan few_plan(long long items, int units, int NT, int R, size_t routing, bool capped) {
   const int most = few_most_warps(R);
   FewPlan p{};
   p.cost = 1e300;
   for (int w = most; w >= 4; --w) {
-    if (few_stages(w, 1, NT, R, routing) == 0) continue;
     for (int c = 1; c * w <= most; ++c) {
+      if (few_stages(w, c, NT, R, routing) == 0) continue;
       const double rounds = (double)((items + (long long)kFewSms * c - 1) / ((long long)kFewSms * c));
       const double cost = rounds * ((units + w - 1) / w + 0.3) * most;
       if (cost < p.cost * (1.0 - 1e-9)) p.cost = cost, p.warps = w, p.ctas = c;
     }
   }
   if (capped) p.ctas = 1;
-  while ((p.stages = few_stages(p.warps, p.ctas, NT, R, routing)) == 0) --p.ctas;   // (one fits)
+  p.stages = few_stages(p.warps, p.ctas, NT, R, routing);
   p.smem = few_smem(p.warps, p.stages, NT, R, routing);
   return p;
 }
 
 // The unit's tiles of rows and the layout of a call's product.
 // rows: of weights, over all experts that can be active (kStreamDown: of one); units: of an item along its contraction.
-// Units of two tiles (32 rows) share the tokens' operands and the steps between them and cost about 1.5 of one tile (us, two and one:
-// 16 tokens through 64 experts 328 and 400, one token through 8 63.4 and 66.1, 32 tokens through 32 of 4096x2048 199 and 249; four-bit
-// weights, 2 tokens through 32 experts of 7168x2048 68 and 80, 16 tokens 223 and 253). Not E2M1 weights whose rows are no whole units (5
-// tokens through 16 experts of 2080x1408 25.5 and 24.3) or with four column tiles, which leave no registers for them (404 and 311).
+// Units of two tiles (32 rows) share the tokens' operands and the steps between them and cost about 1.5 of one tile (us, two and one: one
+// token through 8 of 32 experts of 7168x2048 59 and 65, 16 tokens through 8 of 64 320 and 399, 32 such 551 and 638; where rows are too few
+// for it, 32 tokens through 8 of 256 of 2048x512 148 and 125; four-bit weights, 2 tokens through 8 of 32 experts of 7168x2048 68 and 82, 16
+// tokens 212 and 234; of 26 sizes the rule's side is the faster one or within 2% of it in 24, 3% of 3 us and of 23 in the others). Not E2M1
+// weights whose rows are no whole units (5 tokens through 16 experts of 2080x1408 25.5 and 24.3) or with four column tiles, which leave no
+// registers for them (404 and 311).
 struct FewChoice {
   int R;
   FewPlan plan;

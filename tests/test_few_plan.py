@@ -40,3 +40,26 @@ def test_tables_of_many_experts_leave_room(N, E):
         for T in (32, 33):
             up, down = P.layer(T, 32, E, 128, I, N, "")
             assert up[2] >= 1 and down[2] >= 1 and down[1] < 12
+
+
+def _cost(rows, units, R, warps, ctas):
+    rounds = -(-(-(-rows // (16 * R))) // (152 * ctas))
+    return rounds * (-(-units // warps) + 0.3) * (12 if R == 2 else 16)
+
+
+def test_the_layout_that_was_weighed_is_the_one_that_runs():
+    """The cost is that of the CTAs an SM that fit, and no layout that fits costs less."""
+    for T, (k, E), rows, units, (four, whole) in _domain():
+        R, warps, ctas, _, _, cost = at = P.choice(T, k, E, rows, units, four, whole)
+        assert cost == pytest.approx(_cost(rows, units, R, warps, ctas)), (T, k, E, rows, units, four, at)
+        most = 12 if R == 2 else 16
+        for w in range(4, most + 1):
+            for c in range(1, most // w + 1):
+                if P.stages(T, k, E, w, c, R):
+                    assert _cost(rows, units, R, w, c) >= cost * (1 - 1e-6), (T, k, E, rows, units, four, at, w, c)
+
+
+def test_units_of_two_tiles_are_weighed_by_what_fits():
+    """32 tokens through 8 of 64 experts of 7168x2048: six warps at two CTAs an SM do not fit, twelve at one do."""
+    for product in P.layer(32, 8, 64, 7168, 2048, 7168, ""):
+        assert product[:3] == (2, 12, 1)
