@@ -36,10 +36,14 @@ namespace {
 constexpr int kWarps = 4;
 // How near keys may be in FP32 and be told apart. A sigmoid by the fast exponential and division is within 4e-7 of itself, one by expf and
 // a division within 1.8e-7 (3.6e-7 of its value). A softmax's scores have one sum of exponentials (up to ten additions one behind the
-// other, expf's 2.4e-7 and a division: 9e-7 of the score, in both alike, so of their difference), and each an expf and a product (3.1e-7);
-// no score is larger than that of the largest logit, 1 / Σ exp(l - largest). A sum with a bias rounds by 6e-8 of it.
+// other, expf's 2.4e-7, a division, and the distances' rounding below, at most 2.6e-7 of the sum of 1024: 1.2e-6 of the score, in both
+// alike, so of their difference). Each has an expf and a product (3.1e-7), and its logit's distance to the largest is rounded before
+// (6e-8 of the distance, which is so much of the score: scores 18 below the largest were told apart that were not so). No score is larger
+// than that of the largest logit, 1 / Σ exp(l - largest), and what is d below it e^d smaller. A sum with a bias rounds by 6e-8 of it.
 constexpr float kNearFastSigmoid = 1.2e-6f, kNearSoftmax = 2e-6f, kNearSum = 1.3e-7f;   // of two keys, and of the larger one
-constexpr float kNearOwn = 3.8e-7f, kNearDifference = 1.1e-6f, kNearBiases = 1.3e-7f;   // of two scores' sum, of their and their biases' differences
+// Of each score, of a softmax's with its distance to the largest logit; of the two scores' and their biases' differences; and where scores
+// have no FP32 numbers.
+constexpr float kNearOwn = 3.8e-7f, kNearDistance = 6e-8f, kNearDifference = 1.4e-6f, kNearBiases = 1.3e-7f, kNearTiny = 1e-38f;
 
 // Larger floats have larger integers, from 2^23 on; what is never selected (NaN, -inf, not `some`) has 0.
 __device__ __forceinline__ uint32_t ordered(float x, bool some = true) {
@@ -282,9 +286,13 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
       if (nears >> 31 || (listed == 32 && a.k < 32 && nears >> 30)) {   // a list that does not end
         choice = select_carefully<VPL, QUADS>(a, row, soft, lane);
       } else {
-        float score = choice >= 0 ? to_f32(row[choice]) : 0.0f;
+        float score = choice >= 0 ? to_f32(row[choice]) : 0.0f, own = kNearOwn;
         const float b = a.bias && choice >= 0 ? a.bias[choice] : 0.0f;
-        if (a.bias) score = a.sigmoid ? sigmoid(score) : soft(score);
+        if (a.bias) {
+          if (!a.sigmoid) own = fmaf(kNearDistance, soft.top - score, own);
+          score = a.sigmoid ? sigmoid(score) : soft(score);
+          own *= score;
+        }
         double exact = 0.0;
         bool exactly = false, unclear = false;
         auto before = [&](int i, bool ask) {   // whether lane i's choice comes before this lane's
@@ -294,7 +302,8 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
             return ask && (other > exact || (other == exact && its < choice));
           }
           const float other = __shfl_sync(0xffffffffu, score, i), ds = other - score, db = __shfl_sync(0xffffffffu, b, i) - b, d = ds + db;
-          unclear |= ask && a.bias && !(fabsf(d) > kNearOwn * (other + score) + kNearDifference * fabsf(ds) + kNearBiases * fabsf(db));
+          const float owns = own + __shfl_sync(0xffffffffu, own, i) + kNearTiny;
+          unclear |= ask && a.bias && !(fabsf(d) > owns + kNearDifference * fabsf(ds) + kNearBiases * fabsf(db));
           return ask && (d > 0.0f || (!(d < 0.0f) && its < choice));   // (two infinite logits are equal)
         };
         int from = lane;
