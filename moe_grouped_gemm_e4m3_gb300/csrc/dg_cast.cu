@@ -109,8 +109,7 @@ struct CastShared {
 };
 
 template <bool UE>
-__global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uint16_t* __restrict__ x,
-                                                                       const int32_t* __restrict__ m_indices,
+__global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uint16_t* x, const int32_t* m_indices,
                                                                        const CastForms f, int M, int N, int tiles) {
   extern __shared__ __align__(16) uint8_t smem[];
   CastShared& sh = *reinterpret_cast<CastShared*>(smem);
@@ -126,7 +125,7 @@ __global__ void __launch_bounds__(kCastThreads, kCastCtas) cast_kernel(const uin
 #pragma unroll
     for (int i = 0; i < kCastRows; ++i) {
       const int row = tile / Nb % Mb * 128 + t / 16 + i * kCastStep;
-      idx[i] = m_indices && tile < tiles && row < M ? __ldg(m_indices + row) : 0;
+      idx[i] = m_indices && tile < tiles && row < M ? m_indices[row] : 0;
     }
   };
   auto fetch = [&](int tile, int buf, const int (&idx)[kCastRows]) {
@@ -299,10 +298,8 @@ __device__ __forceinline__ float cluster_max(const float* mine) {
 }
 
 template <bool UE, bool BLOCKS, int SPLIT>
-__global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const uint16_t* __restrict__ dh,
-                                                                          const uint16_t* __restrict__ gu,
-                                                                          const int32_t* __restrict__ m_indices,
-                                                                          const Dropout d, const CastForms f,
+__global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const uint16_t* dh, const uint16_t* gu,
+                                                                          const int32_t* m_indices, const Dropout d, const CastForms f,
                                                                           const CastForms f_h, int M, int I, int tiles) {
   constexpr int kGateRows = GatePlan<SPLIT>::kRows, kGateStep = GatePlan<SPLIT>::kStep;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -322,7 +319,7 @@ __global__ void __launch_bounds__(kGateThreads, 1) swiglu_backward_kernel(const 
 #pragma unroll
     for (int i = 0; i < kGateRows; ++i) {
       const int row = tile / nI * 128 + t_row + i * kGateStep;
-      idx[i] = m_indices && tile < tiles && row < M ? __ldg(m_indices + row) : 0;
+      idx[i] = m_indices && tile < tiles && row < M ? m_indices[row] : 0;
     }
   };
   auto fetch = [&](int tile, int buf, const int (&idx)[kGateRows]) {

@@ -175,7 +175,7 @@ __device__ __forceinline__ void gated_cluster_reduce(const GatedExt& e, void* H,
         u4.x += us[s].x; u4.y += us[s].y; u4.z += us[s].z; u4.w += us[s].w;
       }
     if (m_indices) {
-      const int idx = __ldg(m_indices + a_row + r);
+      const int idx = m_indices[a_row + r];
       if (idx != g) {
         if (idx != -1 && c == 0) atomicOr(status, bad_group_bit);
         continue;   // a padding row (or another group's): left untouched

@@ -37,19 +37,19 @@ struct FewPlan {
 // compiler sank the scales' loads to their uses, each a round trip to L2).
 __device__ __forceinline__ uint4 load_16(const uint8_t* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 
 __device__ __forceinline__ uint32_t load_4(const uint32_t* p) {
   uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p) {   // read once: not kept in L1
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -70,8 +70,7 @@ __device__ __forceinline__ float scale_value(uint32_t bits, int kb) {
 // CAPPED: fewer CTAs than groups of 8 columns (dg_set_num_sms), each taking several; a loop in the other form spills.
 template <bool UE, bool OUT_F32, int NT, bool CAPPED>
 __global__ void __launch_bounds__(FewPlan<NT>::kThreads, 2)
-    gated_few_kernel(const uint8_t* __restrict__ A, const void* __restrict__ sA, const uint8_t* __restrict__ B,
-                     const void* __restrict__ sB, void* H, uint16_t* GU, const Dropout drop, int M, int I, int K) {
+    gated_few_kernel(const uint8_t* A, const void* sA, const uint8_t* B, const void* sB, void* H, uint16_t* GU, const Dropout drop, int M, int I, int K) {
   constexpr int kWarps = FewPlan<NT>::kWarps, kBatch = FewPlan<NT>::kBatch;
   __shared__ float sums[kWarps][NT][4][32];
   griddep_wait();

@@ -349,9 +349,9 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
         const bool has_nb1 = SWIGLU || nb0 + 1 < p.nnb;
         const int q_end = (tile.kb1 - 1) >> 2;
         for (int quad = tile.kb0 >> 2; quad <= q_end; ++quad, ++sf_it) {
-          const uint32_t a = row_exists ? __ldg(sfa_ptr + (size_t)quad * p.ldsa) : 0x7F7F7F7Fu;
-          const uint32_t b0 = __ldg(sfb_ptr + quad);
-          const uint32_t b1 = has_nb1 ? __ldg(sfb1_ptr + quad) : 0x7F7F7F7Fu;
+          const uint32_t a = row_exists ? sfa_ptr[(size_t)quad * p.ldsa] : 0x7F7F7F7Fu;
+          const uint32_t b0 = sfb_ptr[quad];
+          const uint32_t b1 = has_nb1 ? sfb1_ptr[quad] : 0x7F7F7F7Fu;
           const uint32_t slot = sf_it % SLOTS;
           if (!mbar_wait_warp(&sf_empty_bar[slot], ((sf_it / SLOTS) & 1) ^ 1, abort_flag, p.status, p.flags)) {
             alive = false;
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
       if constexpr (MODE == kContiguous) {
         write_row = false;
         if (row_exists) {
-          const int idx = (kGated && !p.m_indices) ? 0 : __ldg(p.m_indices + m_local);
+          const int idx = (kGated && !p.m_indices) ? 0 : p.m_indices[m_local];
           write_row = (idx == tile.g);
           if (idx != tile.g && idx != -1) atomicOr(p.status, kStatusBadGroup);
         }
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(BsRoles::kThreads, 1)
           if (n >= p.N) continue;
           const size_t d_row = (size_t)(a_row + r);
           if constexpr (MODE == kContiguous) {
-            const int idx = __ldg(p.m_indices + a_row + r);
+            const int idx = p.m_indices[a_row + r];
             if (idx != g) {
               if (idx != -1 && c4 == 0) atomicOr(p.status, kStatusBadGroup);
               continue;   // a padding row (or another group's): left untouched

@@ -11,6 +11,8 @@
 
 #include <cstdint>
 
+#include "dg_ptx.cuh"
+
 namespace dg {
 
 struct Dropout {
@@ -24,8 +26,8 @@ struct Philox {
   uint32_t k0 = 0, k1 = 0, c2 = 0, c3 = 0;
   __device__ __forceinline__ Philox() {}
   __device__ __forceinline__ explicit Philox(const uint64_t* rng) {
-    const uint64_t seed = __ldg(reinterpret_cast<const unsigned long long*>(rng));
-    const uint64_t offset = __ldg(reinterpret_cast<const unsigned long long*>(rng) + 1);
+    // (in place: loads that the compiler gathers cost the few-token gated projection registers, which it then spills)
+    const uint64_t seed = load_here(rng), offset = load_here(rng + 1);
     k0 = (uint32_t)seed;
     k1 = (uint32_t)(seed >> 32);
     c2 = (uint32_t)offset;

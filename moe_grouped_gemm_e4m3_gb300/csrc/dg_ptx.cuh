@@ -254,9 +254,23 @@ __device__ __forceinline__ float4 cluster_sum_v4(uint32_t addr, int S) {
 // Programmatic dependent launch. A kernel launched with programmatic stream serialization may start
 // before the kernel ahead of it in the stream has finished; griddep_wait() then blocks until that
 // kernel has completed and its memory operations are visible. Without the launch attribute both
-// instructions do nothing.
+// instructions do nothing. What the wait guards is read by plain loads and asynchronous copies: the
+// read-only path (ld.global.nc, __ldg, const __restrict__) is for data that nobody writes while the
+// kernel lives, and this one lives beside its writer.
 
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Plain loads that stay where they stand, for the places where the compiler's own choice is worse (see each).
+__device__ __forceinline__ int32_t load_here(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint64_t load_here(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.global.u64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
+}
 
 // Lets the next kernel in the stream (if launched for it) begin its own launch while this one runs.
 __device__ __forceinline__ void griddep_launch_dependents() {
