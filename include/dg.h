@@ -486,7 +486,7 @@ dg_status dg_residual_norm_backward_f32(const float* dY, const float* dR, const 
 /*
  * The router: the k experts of each token from its logits [T,E] (FP32 or BF16), in descending order.
  *   score: softmax over the E logits, or each one's sigmoid. Selected are the k largest of score + bias[e] (bias NULL: of
- *   the logits), ties to the lowest index; scores closer than FP32 tells apart are settled in FP64. A logit that is NaN or -inf
+ *   the logits), ties to the lowest index; sums closer than FP32 tells apart are settled in FP64, and those that tie there tie. A logit that is NaN or -inf
  *   and a bias of -inf are never selected; a token with fewer than k others gets ids of -1 with weight 0 in the last places.
  *   weights [T,k] = factor·score of the selected (without the bias), with renormalize divided by their sum + 1e-20.
  * The ids [T,k] are those dg_fp8_moe_swiglu takes. E at most 1024, k at most min(E, 32).

@@ -41,9 +41,10 @@ constexpr int kWarps = 4;
 // (6e-8 of the distance, which is so much of the score: scores 18 below the largest were told apart that were not so). No score is larger
 // than that of the largest logit, 1 / Σ exp(l - largest), and what is d below it e^d smaller. A sum with a bias rounds by 6e-8 of it.
 constexpr float kNearFastSigmoid = 1.2e-6f, kNearSoftmax = 2e-6f, kNearSum = 1.3e-7f;   // of two keys, and of the larger one
-// Of each score, of a softmax's with its distance to the largest logit; of the two scores' and their biases' differences; and where scores
-// have no FP32 numbers.
-constexpr float kNearOwn = 3.8e-7f, kNearDistance = 6e-8f, kNearDifference = 1.4e-6f, kNearBiases = 1.3e-7f, kNearTiny = 1e-38f;
+// Of each score, of a softmax's with its distance to the largest logit; of each bias (a step of FP64: where the sums tie there, they tie,
+// although FP32 may know which score is the larger one: equal biases of scores below 1e-16 of them); of the two scores' and their biases'
+// differences; and where scores have no FP32 numbers.
+constexpr float kNearOwn = 3.8e-7f, kNearDistance = 6e-8f, kNearBias = 2.3e-16f, kNearDifference = 1.4e-6f, kNearBiases = 1.3e-7f, kNearTiny = 1e-38f;
 
 // Larger floats have larger integers, from 2^23 on; what is never selected (NaN, -inf, not `some`) has 0.
 __device__ __forceinline__ uint32_t ordered(float x, bool some = true) {
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(32 * kWarps, VPL <= 8 ? 8 : 1) route_kernel(co
         if (a.bias) {
           if (!a.sigmoid) own = fmaf(kNearDistance, soft.top - score, own);
           score = a.sigmoid ? sigmoid(score) : soft(score);
-          own *= score;
+          own = fmaf(own, score, kNearBias * fabsf(b));
         }
         double exact = 0.0;
         bool exactly = false, unclear = false;

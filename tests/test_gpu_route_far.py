@@ -42,3 +42,18 @@ def test_scores_far_below_the_largest(dg, top, near):  # noqa: F811
         ids, _ = _route(dg, l, k, b, score="softmax", renormalize=False)
         want, _ = R.route(l, b, k, "softmax", False, 1.0)
         assert torch.equal(ids.cpu(), want), int((ids.cpu() != want).any(1).sum())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k", [(14, 11), (256, 20), (512, 32)])
+def test_sums_that_tie_in_64_bits(dg, E, k, dt, score):  # noqa: F811
+    """Equal biases (they move in steps) of scores too small for FP64 to see beside them: the lowest index first, whatever FP32 knows
+    of the scores by themselves."""
+    g = torch.Generator().manual_seed(E)
+    l = (12 * torch.randn(64, E, generator=g) - 30).to(dt).cuda()
+    b = (torch.round(16 * torch.randn(E, generator=g)) / 16).cuda()
+    for bias in (b, torch.full_like(b, 0.5), torch.zeros_like(b)):
+        ids, _ = _route(dg, l, k, bias, score=score, renormalize=False)
+        want, _ = R.route(l, bias, k, score, False, 1.0)
+        assert torch.equal(ids.cpu(), want), int((ids.cpu() != want).any(1).sum())
