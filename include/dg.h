@@ -440,7 +440,7 @@ dg_status dg_dropout_f32(const float* X, const float* R, float* Y, const uint64_
  *     P = B·ra·w_after, ra = 1/sqrt(mean(B^2) + eps)   (or P = B where w_after is NULL)
  *     R = X + gate[m]·scale[n]·P                       (gate [M], scale [N]: 1 where NULL; R = X without B)
  *     Y = R·r·W, r = 1/sqrt(mean(R^2) + eps)           (nothing where W is NULL)
- * in FP32. X, B, R, Y are BF16 bits or FP32; the vectors FP32. R [M,N] receives the stream, rounded once (NULL: not
+ * in FP32 (the squares' sums too: they have to be FP32 numbers). X, B, R, Y are BF16 bits or FP32; the vectors FP32. R [M,N] receives the stream, rounded once (NULL: not
  * wanted); Y is formed from the unrounded R and rounded once. Yq, sY: Y as E4M3 rows with scales [ceil(N/128)][align4(M)],
  * cast from the FP32 Y as dg_cast_fp8 casts its row form (entries m >= M 0, packed 127); N a multiple of 16 then.
  * rstd [M] (r) and rstd_after [M] (ra): for the backward pass, or NULL. R and Y may each be X or B itself (not both the same);

@@ -20,12 +20,17 @@
 // operands are consecutive bytes. A group's partial sum meets its scales in FP32: E4M3 weights every 128 values, E2M1 every 32.
 //
 // Measured (us; floor: the weights read once at the measured copy rate): one token through 8 of 32 experts of 7168x2048, E4M3, 60
-// (52); 16 tokens through 64 such, packed scales, 320 (at most 367: uneven choices read fewer experts); 4 tokens 151; 32 tokens 678. Four
-// bits: 1x7168x16384 16.2 (9.2), 16x24576x1536 12.9 (3.1), through 32 experts of 7168x2048 2 tokens 68 (48) and 16 tokens 213 (110). With
-// E4M3 the read bounds it (5.8 to 7 TB/s); with E2M1, at twice the values a byte, instructions do: 438 a unit of 32x256 (one column tile), 128 of
-// them conversions of weights and 32 of tokens, with two cycles of the ALU pipe each. Not kept: more warps (24 for 16) and the tokens' operands
-// staged as FP16 in shared memory, at most 4% off; batches of items whose units the warps share as ranges (fewer turns, one joining of
-// sums a batch), 66 us for 60 and 17 for 15: the warps' pieces of a row lie apart then, and the joining is not hidden.
+// (52); through 64 such, packed scales, 4 tokens 151, 16 tokens 320 (at most 367: uneven choices read fewer experts), 32 tokens 551 (410).
+// Four bits: 1x7168x16384 16.2 (9.2), 16x24576x1536 11.4 to 13.1 (3.1; the upper one with six sets of inputs in turn, more than L2 holds),
+// through 8 of 32 experts of 7168x2048 2 tokens 68 (48) and 16 tokens 212 (110), 32 tokens through 4 of 32 of 4096x2048 216 (62).
+// With E4M3 and up to 16 tokens the read bounds it (5.8 to 7 TB/s). The four-bit products saturate nothing: 1x7168x16384 has 40% of the
+// issue slots in use, 40% of the ALU pipe, 23% of the tensor pipe and 41% of the DRAM cycles, with 2.2 warps a scheduler that wait for
+// loads (20 to 25% of a warp's time), fixed latencies (17%) and the pipe of the conversions (9%), and its 224 items are one or two an SM
+// (18 to 54% of the issue slots); 16x24576x1536 has 35%, 28% and 18%, and waits for L1, its queues and shared memory (24%), fixed latencies
+// (21%), loads (14%) and the barrier after every six units (7%). 438 instructions a unit of 32x256 (one column tile), 160 of them
+// conversions. Not kept: more warps (24 for 16) and the tokens' operands staged as FP16 in shared memory, at most 4% off; batches of items
+// whose units the warps share as ranges (fewer turns, one joining of sums a batch), 66 us for 60 and 17 for 15: the warps' pieces of a row
+// lie apart then, and the joining is not hidden. E2M1 kernels of four column tiles spill (360 to 690 bytes a thread).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -252,7 +257,8 @@ __global__ void __launch_bounds__(R == 2 ? 384 : 512, 1) stream_kernel(const Few
   // A token keeps its column whatever the expert, and kStreamDown's sums go from one expert to the next in registers (kCarries). Or an
   // expert has only its own tokens in columns, one after another, so that mostly one tile of columns is computed (kCompact), and kStreamDown
   // adds an expert's sums to its tokens' in shared memory: where the columns' work counts, with four tiles of them or E2M1 weights (32
-  // tokens, us: 8 of 64 experts 678 and 776, four bits 4 of 32 222 and 310; 16 tokens, four bits 212 and 223, but E4M3 376 and 326).
+  // tokens, us, compact and carried: 8 of 64 experts 551 and 666, four bits 4 of 32 216 and 333; 16 tokens, four bits 212 and 221, but E4M3
+  // 377 and 325).
   constexpr bool kCompact = kRouted && (NT > 2 || (NT == 2 && kFour)), kCarries = KIND == kStreamDown && !kCompact;
   constexpr int kUnitK = kFour ? 256 : 128, kRows = 16 * R, kStage = stage_bytes(R);
   constexpr int kScaleCopies = (kRows * 3 + 31) / 32;   // E2M1: three words a row, unless they start on eight bytes

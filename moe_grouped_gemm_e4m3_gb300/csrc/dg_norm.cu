@@ -16,7 +16,10 @@
 //
 // Bound by HBM, with the issue slots half busy (us; floor at the measured copy rate): 8192x7168 BF16 with both norms, gate and scale 83
 // (69), without the norm after, gate and scale 70 (69), the first one's backward pass 135 (104); 4099x2112 FP32 with E4M3 rows 16 (11.5);
-// one row of 7168 4. The columns' sums (dW, dscale, dw_after) are kept in FP32 registers over the rows of a CTA, one
+// one row of 7168 4. Farther off where a row does not fit: the backward pass of FP32 rows has a ring of one row at 2112, 4096 and 7168
+// columns (8192x7168 301 for 208, 8192x4096 148 for 119, 8192x2112 89 for 61; two rows at 5120, 184 for 149), so that nothing is asked
+// for ahead, and above 8192 columns a thread's four vectors of column state spill (668 to 884 bytes a thread: 4096x16384 BF16 324 for 119,
+// 4096x12288 281 for 89; forward, 52 to 104 bytes, 116 for 79 and 101 for 60). The columns' sums (dW, dscale, dw_after) are kept in FP32 registers over the rows of a CTA, one
 // partial row a CTA goes to the workspace, and a second kernel adds them in order (no atomics: the same bits every time).
 // Row m belongs to partial m % parts, and parts is a function of the sizes alone, not of dg_set_num_sms.
 //
@@ -522,6 +525,7 @@ bool all_aligned(std::initializer_list<const void*> ps) {
 }
 
 // How rows of N are laid out: vectors and threads of a CTA, CTAs an SM, and how many of them take the rows by turns.
+// (152 SMs: those of the GPU that this is for; the sums' order depends on it, and so not on dg_set_num_sms.)
 constexpr int kNormSms = 152, kRingBytes = 216 << 10;   // (the ring: of an SM, over its CTAs)
 struct RowPlan {
   int V, threads, per_sm, parts;
